@@ -190,16 +190,16 @@ def _norm_own(s):
     t, hq, hk, d = c["t"], c["hq"], c["hk"], c["d"]
     q_out = torch.empty(t, hq, d, dtype=x.dtype, device=x.device)
     if c["cache"]:
-        k_out, v_out, slots = s["k_cache"], s["v_cache"], s["slots"].data_ptr()
+        k_out, v_out, slots, rows = s["k_cache"], s["v_cache"], s["slots"].data_ptr(), c["cache"]
     else:
         k_out, v_out = (torch.empty(t, hk, d, dtype=x.dtype, device=x.device) for _ in range(2))
-        slots = 0
+        slots, rows = 0, t
     row, base, size = (hq + 2 * hk) * d, x.data_ptr(), x.element_size()
     ox.oidnx_qk_norm_rope(base, row, d, q_out.data_ptr(), hq * d, d,
                           base + hq * d * size, row, d, k_out.data_ptr(), hk * d, d,
                           base + (hq + hk) * d * size, row, d, v_out.data_ptr(), hk * d, d,
                           _ptr(s["q_weight"]), _ptr(s["k_weight"]), 1e-6, s["cos"].data_ptr(), s["sin"].data_ptr(),
-                          s["cos"].shape[0], s["positions"].data_ptr(), slots, t, hq, hk, d, c["rot"],
+                          s["cos"].shape[0], s["positions"].data_ptr(), slots, rows, t, hq, hk, d, c["rot"],
                           int(c["interleaved"]), _precision(ox, x), torch.cuda.current_stream().cuda_stream)
     return q_out, k_out, v_out
 
