@@ -35,7 +35,8 @@ ERR_TIMEOUT = 7
 ERR_NOT_COMMITTED = 8
 
 IMAGE_COLOR, IMAGE_ALBEDO, IMAGE_NORMAL, IMAGE_OUTPUT = 0, 1, 2, 3
-PRECISION_AUTO, PRECISION_FP32, PRECISION_FP16 = 0, 1, 2
+PRECISION_AUTO, PRECISION_FP32, PRECISION_FP16, PRECISION_BF16 = 0, 1, 2, 3
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 TRANSFER_PU, TRANSFER_LOG = 0, 1
 
 LAYER_NAMES = (
@@ -82,6 +83,15 @@ _sig("oidnx_filter_release", None, _vp)
 _sig("oidnx_conv_create", _st, _vp, _vp, _i, _i, _i, ctypes.POINTER(_vp))
 _sig("oidnx_conv_execute", _st, _vp, _vp, _vp, _i, _i, _i, _vp)
 _sig("oidnx_conv_release", None, _vp)
+_ll = ctypes.c_longlong
+_fl = ctypes.c_float
+_view = (_vp, _ll, _ll)
+_sig("oidnx_linear", _st, _vp, _ll, _vp, _ll, _vp, _vp, _ll, _vp, _ll, _i, _i, _i, _i, _i, _vp)
+_sig("oidnx_qk_norm_rope", _st, *_view * 6, _vp, _vp, _fl, _vp, _vp, _ll, _vp, _vp, _ll,
+     _i, _i, _i, _i, _i, _i, _i, _vp)
+_sig("oidnx_window_attention", _st, *(_vp, _ll, _ll, _ll) * 4, _vp, _vp, _vp,
+     _i, _i, _i, _i, _i, _i, _i, _i, _fl, _i, _vp)
+_sig("oidnx_token_sync_status", _st, _vp)
 _sig("oidnx_plan_tiles", _st, _i, _i, _i, _i, ctypes.POINTER(_i), _i, ctypes.POINTER(_i))
 _sig("oidnx_default_overlap", _i)
 _sig("oidnx_version", ctypes.c_char_p)
@@ -242,6 +252,38 @@ def oidnx_conv_execute(c, in_ptr, out_ptr, w, h, relu=1, stream=0):
 
 def oidnx_conv_release(c):
     _lib.oidnx_conv_release(c)
+
+
+def oidnx_linear(x, ldx, w, ldw, bias, residual, ldr, y, ldy, m, n, k, act, precision, stream=0):
+    """y = act(x w^T + bias) + residual; bias and residual may be 0."""
+    _check(_lib.oidnx_linear(x, ldx, w, ldw, bias, residual, ldr, y, ldy, m, n, k, act, precision,
+                             stream))
+
+
+def oidnx_qk_norm_rope(q, q_st, q_sh, q_out, qo_st, qo_sh, k, k_st, k_sh, k_out, ko_st, ko_sh,
+                       v, v_st, v_sh, v_out, vo_st, vo_sh, q_weight, k_weight, eps, cos_table,
+                       sin_table, table_rows, positions, slots, cache_rows, t, hq, hk, d, rot,
+                       interleaved, precision, stream=0):
+    """Norm and rotation of query and key heads, keys and values appended at
+    their slots; q_weight, k_weight, slots and the pair v, v_out may be 0."""
+    _check(_lib.oidnx_qk_norm_rope(q, q_st, q_sh, q_out, qo_st, qo_sh, k, k_st, k_sh, k_out, ko_st,
+                                   ko_sh, v, v_st, v_sh, v_out, vo_st, vo_sh, q_weight, k_weight,
+                                   eps, cos_table, sin_table, table_rows, positions, slots,
+                                   cache_rows, t, hq, hk, d, rot, interleaved, precision, stream))
+
+
+def oidnx_window_attention(q, q_sb, q_st, q_sh, k, k_sb, k_st, k_sh, v, v_sb, v_st, v_sh,
+                           o, o_sb, o_st, o_sh, lse, q_lens, kv_lens, b, tq, cap, hq, hk, d,
+                           window, sinks, scale, precision, stream=0):
+    """Attention with a sliding window and sinks over a linear or ring cache;
+    lse, q_lens and kv_lens may be 0."""
+    _check(_lib.oidnx_window_attention(q, q_sb, q_st, q_sh, k, k_sb, k_st, k_sh, v, v_sb, v_st,
+                                       v_sh, o, o_sb, o_st, o_sh, lse, q_lens, kv_lens, b, tq, cap,
+                                       hq, hk, d, window, sinks, scale, precision, stream))
+
+
+def oidnx_token_sync_status(stream=0):
+    _check(_lib.oidnx_token_sync_status(stream))
 
 
 def oidnx_plan_tiles(width, height, max_tile_size=0, overlap=-1):

@@ -1,0 +1,146 @@
+// Shared declarations of the token operators (linear layer, query/key norm
+// with rotation, window attention): launch parameters, type helpers and the
+// launchers that token_host.cpp chooses from.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "../../include/oidnx.h"
+#include "internal.h"
+
+namespace oidnx {
+
+// ---------------------------------------------------------------- types
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Two consecutive 16-bit values <-> one 32-bit word.
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t w);
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<__half2*>(&w));
+}
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w));
+}
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// The 16 bytes of a vector load as fp32 values (8 of 16 bits or 4 of 32), and back.
+template <typename T> struct Vec16 {
+  static constexpr int N = 16 / sizeof(T);
+  static __device__ __forceinline__ void unpack(uint4 r, float (&v)[N]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        v[i] = __uint_as_float(w[i]);
+      } else {
+        const float2 f = unpack2<T>(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&v)[N]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
+      else w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// ---------------------------------------------------------------- linear
+// y[i][j] = act(sum_k x[i][k] w[j][k] + bias[j]) + residual[i][j]; row strides
+// in elements.
+struct LinearParams {
+  const void* x;
+  const void* w;
+  const void* bias;      // [n] or null
+  const void* residual;  // or null
+  void* y;
+  int64_t ldx, ldw, ldr, ldy;
+  int m, n, k, act;
+  int* status;
+};
+
+// ---------------------------------------------------------------- norm and rotation
+// Index 0 = queries, 1 = keys, 2 = values; strides in elements.
+struct NormParams {
+  const void* in[3];
+  void* out[3];
+  int64_t in_t[3], in_h[3], out_t[3], out_h[3];
+  int heads[3];
+  const void* weight[2];
+  float eps;
+  const float* cos_t;
+  const float* sin_t;
+  int64_t table_rows;
+  const int* positions;
+  const int* slots;  // or null: row t
+  int64_t cache_rows;
+  int t, d, rot, interleaved;
+};
+
+// ---------------------------------------------------------------- attention
+// Strides in elements: batch, token, head.
+struct AttnParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  float* lse;         // [b][hq][tq] or null
+  const int* q_lens;  // [b] or null: tq
+  const int* kv_lens; // [b] or null: cap
+  int64_t q_s[3], k_s[3], v_s[3], o_s[3];
+  int b, tq, cap, hq, hk, d;
+  int window;  // 0: none
+  int sinks;
+  int held_sinks;  // min(sinks, cap): the slots that the ring leaves alone
+  float scale;
+  int* status;
+};
+
+__device__ __forceinline__ int attn_q_len(const AttnParams& p, int b) {
+  const int n = p.q_lens ? p.q_lens[b] : p.tq;
+  return n < 0 ? 0 : n > p.tq ? p.tq : n;
+}
+__device__ __forceinline__ int attn_kv_len(const AttnParams& p, int b) {
+  const int n = p.kv_lens ? p.kv_lens[b] : p.cap;
+  return n < 0 ? 0 : n;
+}
+// First position after the sinks whose key the cache still holds when n keys
+// have been written: the ring keeps the last cap - held_sinks of them.
+__device__ __forceinline__ int attn_ring_begin(const AttnParams& p, int n) {
+  const int b = n - (p.cap - p.held_sinks);
+  return b > p.held_sinks ? b : p.held_sinks;
+}
+// Cache slot of a held position.
+__device__ __forceinline__ int attn_slot(const AttnParams& p, int pos) {
+  if (pos < p.cap) return pos;
+  return p.held_sinks + (pos - p.held_sinks) % (p.cap - p.held_sinks);
+}
+
+cudaError_t launch_linear_any(const LinearParams& p, int precision, cudaStream_t stream);
+cudaError_t launch_norm_vec(const NormParams& p, int precision, cudaStream_t stream);
+cudaError_t launch_norm_any(const NormParams& p, int precision, cudaStream_t stream);
+cudaError_t launch_attn_any(const AttnParams& p, int precision, cudaStream_t stream);
+
+}  // namespace oidnx

@@ -1,0 +1,204 @@
+// Entry points of the token operators: argument checks and the choice of
+// kernel.  Each is a direct call on device pointers; nothing is kept from one
+// call for the next but the device error word.
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+#include <mutex>
+
+#include "../../include/oidnx.h"
+#include "token.h"
+
+namespace oidnx {
+oidnx_status report_error(oidnx_status status, const char* message);
+cudaError_t token_status_address(int** out);
+cudaError_t token_status_take(int* word, cudaStream_t stream);
+}  // namespace oidnx
+
+using namespace oidnx;
+
+namespace {
+
+template <typename... A>
+oidnx_status fail(oidnx_status s, const char* fmt, A... args) {
+  char buf[512];
+  snprintf(buf, sizeof(buf), fmt, args...);
+  return report_error(s, buf);
+}
+oidnx_status fail(oidnx_status s, const char* text) { return report_error(s, text); }
+
+oidnx_status finish(cudaError_t e, const char* call) {
+  if (e != cudaSuccess) {
+    cudaGetLastError();  // a refused launch must not show up in the caller's next check
+    return fail(e == cudaErrorMemoryAllocation ? OIDNX_ERR_OUT_OF_MEMORY : OIDNX_ERR_CUDA, "%s: %s", call,
+                cudaGetErrorString(e));
+  }
+  report_error(OIDNX_OK, "");
+  return OIDNX_OK;
+}
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+}  // namespace
+
+extern "C" {
+
+oidnx_status oidnx_linear(const void* x, long long ldx, const void* w, long long ldw, const void* bias,
+                          const void* residual, long long ldr, void* y, long long ldy, int m, int n, int k, int act,
+                          int precision, void* stream) {
+  if (m < 0 || n < 0 || k < 0) return fail(OIDNX_ERR_INVALID_ARGUMENT, "linear: negative size (%d, %d, %d)", m, n, k);
+  if (act < OIDNX_ACT_NONE || act > OIDNX_ACT_SILU)
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "linear: unknown activation %d", act);
+  if (precision == OIDNX_PRECISION_FP32) return fail(OIDNX_ERR_UNSUPPORTED, "linear: fp16 or bf16 only");
+  if (precision != OIDNX_PRECISION_FP16 && precision != OIDNX_PRECISION_BF16)
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "linear: unknown precision %d", precision);
+  if (m == 0 || n == 0) return finish(cudaSuccess, "linear");
+  if (!y || (k > 0 && (!x || !w))) return fail(OIDNX_ERR_INVALID_ARGUMENT, "linear: NULL x, w or y");
+  if (ldx < k || ldw < k || ldy < n || (residual && ldr < n))
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "linear: a row stride is shorter than its row");
+  if (!aligned(x, 2) || !aligned(w, 2) || !aligned(bias, 2) || !aligned(residual, 2) || !aligned(y, 2))
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "linear: pointers must be aligned to their elements");
+  LinearParams p = {};
+  p.x = x, p.w = w, p.bias = bias, p.residual = residual, p.y = y;
+  p.ldx = ldx, p.ldw = ldw, p.ldr = ldr, p.ldy = ldy;
+  p.m = m, p.n = n, p.k = k, p.act = act;
+  cudaError_t e = token_status_address(&p.status);
+  if (e == cudaSuccess) e = launch_linear_any(p, precision, static_cast<cudaStream_t>(stream));
+  return finish(e, "linear");
+}
+
+oidnx_status oidnx_qk_norm_rope(const void* q, long long q_st, long long q_sh, void* q_out, long long qo_st,
+                                long long qo_sh, const void* k, long long k_st, long long k_sh, void* k_out,
+                                long long ko_st, long long ko_sh, const void* v, long long v_st, long long v_sh,
+                                void* v_out, long long vo_st, long long vo_sh, const void* q_weight,
+                                const void* k_weight, float eps, const float* cos_table, const float* sin_table,
+                                long long table_rows, const int* positions, const int* slots, long long cache_rows,
+                                int t, int hq, int hk, int d, int rot, int interleaved, int precision, void* stream) {
+  if (precision < OIDNX_PRECISION_FP32 || precision > OIDNX_PRECISION_BF16)
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: unknown precision %d", precision);
+  if (t < 0 || hq < 0 || hk < 0 || d <= 0 || rot < 0 || rot > d || rot % 2)
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: bad sizes (t %d, heads %d and %d, d %d, rot %d)", t, hq, hk,
+                d, rot);
+  if (hq > 65536 || hk > 65536) return fail(OIDNX_ERR_UNSUPPORTED, "qk_norm_rope: more than 65536 heads");
+  if (!(eps >= 0.f) || std::isinf(eps)) return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: bad eps");
+  if (t == 0 || (hq == 0 && hk == 0)) return finish(cudaSuccess, "qk_norm_rope");
+  if ((hq && (!q || !q_out)) || (hk && (!k || !k_out)) || !v != !v_out)
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: NULL heads");
+  if (rot && (!cos_table || !sin_table || !positions || table_rows < 0))
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: NULL tables or positions");
+  const size_t size = precision == OIDNX_PRECISION_FP32 ? 4 : 2;
+  const void* all[] = {q, q_out, k, k_out, v, v_out, q_weight, k_weight};
+  for (const void* a : all)
+    if (!aligned(a, size))
+      return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: pointers must be aligned to their elements");
+  if (!aligned(cos_table, 4) || !aligned(sin_table, 4) || !aligned(positions, 4) || !aligned(slots, 4))
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: tables, positions and slots must be 4-byte aligned");
+  NormParams p = {};
+  const void* in[3] = {q, k, v};
+  void* out[3] = {q_out, k_out, v_out};
+  const long long it[3] = {q_st, k_st, v_st}, ih[3] = {q_sh, k_sh, v_sh};
+  const long long ot[3] = {qo_st, ko_st, vo_st}, oh[3] = {qo_sh, ko_sh, vo_sh};
+  p.heads[0] = hq, p.heads[1] = hk, p.heads[2] = v ? hk : 0;
+  // 16-byte form: every head starts on 16 bytes and rotation pairs are whole
+  // chunks apart (half-split) or do not straddle one (adjacent pairs)
+  const int vec = static_cast<int>(16 / size);
+  bool fast = d % vec == 0 && d / vec <= 64 && (interleaved ? rot % vec == 0 : rot / 2 % vec == 0) &&
+              aligned(q_weight, 16) && aligned(k_weight, 16) && aligned(cos_table, 16) && aligned(sin_table, 16);
+  for (int i = 0; i < 3; ++i) {
+    p.in[i] = in[i], p.out[i] = out[i];
+    p.in_t[i] = it[i], p.in_h[i] = ih[i], p.out_t[i] = ot[i], p.out_h[i] = oh[i];
+    if (p.heads[i])
+      fast = fast && aligned(in[i], 16) && aligned(out[i], 16) && it[i] % vec == 0 && ih[i] % vec == 0 &&
+             ot[i] % vec == 0 && oh[i] % vec == 0;
+  }
+  p.weight[0] = q_weight, p.weight[1] = k_weight;
+  p.eps = eps, p.cos_t = cos_table, p.sin_t = sin_table, p.table_rows = table_rows;
+  p.positions = positions, p.slots = slots, p.cache_rows = cache_rows;
+  p.t = t, p.d = d, p.rot = rot, p.interleaved = interleaved != 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return finish(fast ? launch_norm_vec(p, precision, s) : launch_norm_any(p, precision, s), "qk_norm_rope");
+}
+
+oidnx_status oidnx_window_attention(const void* q, long long q_sb, long long q_st, long long q_sh, const void* k,
+                                    long long k_sb, long long k_st, long long k_sh, const void* v, long long v_sb,
+                                    long long v_st, long long v_sh, void* o, long long o_sb, long long o_st,
+                                    long long o_sh, float* lse, const int* q_lens, const int* kv_lens, int b, int tq,
+                                    int cap, int hq, int hk, int d, int window, int sinks, float scale, int precision,
+                                    void* stream) {
+  if (precision == OIDNX_PRECISION_FP32) return fail(OIDNX_ERR_UNSUPPORTED, "window_attention: fp16 or bf16 only");
+  if (precision != OIDNX_PRECISION_FP16 && precision != OIDNX_PRECISION_BF16)
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "window_attention: unknown precision %d", precision);
+  if (b < 0 || tq < 0 || cap < 0 || hq < 0 || hk <= 0 || hq % hk || d <= 0 || window < 0 || sinks < 0)
+    return fail(OIDNX_ERR_INVALID_ARGUMENT,
+                "window_attention: bad sizes (b %d, tq %d, cap %d, heads %d and %d, d %d, window %d, sinks %d)", b, tq,
+                cap, hq, hk, d, window, sinks);
+  if (d > 256) return fail(OIDNX_ERR_UNSUPPORTED, "window_attention: heads of more than 256 values (%d)", d);
+  if (!std::isfinite(scale)) return fail(OIDNX_ERR_INVALID_ARGUMENT, "window_attention: scale is not finite");
+  if (b == 0 || tq == 0 || hq == 0) return finish(cudaSuccess, "window_attention");
+  if (static_cast<double>(b) * tq * hq > 4e9)
+    return fail(OIDNX_ERR_UNSUPPORTED, "window_attention: more than 4e9 query heads");
+  if (!q || !o || (cap > 0 && (!k || !v))) return fail(OIDNX_ERR_INVALID_ARGUMENT, "window_attention: NULL q, k, v or o");
+  if (!aligned(q, 2) || !aligned(k, 2) || !aligned(v, 2) || !aligned(o, 2) || !aligned(lse, 4) || !aligned(q_lens, 4) ||
+      !aligned(kv_lens, 4))
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "window_attention: pointers must be aligned to their elements");
+  AttnParams p = {};
+  p.q = q, p.k = k, p.v = v, p.o = o, p.lse = lse, p.q_lens = q_lens, p.kv_lens = kv_lens;
+  p.q_s[0] = q_sb, p.q_s[1] = q_st, p.q_s[2] = q_sh;
+  p.k_s[0] = k_sb, p.k_s[1] = k_st, p.k_s[2] = k_sh;
+  p.v_s[0] = v_sb, p.v_s[1] = v_st, p.v_s[2] = v_sh;
+  p.o_s[0] = o_sb, p.o_s[1] = o_st, p.o_s[2] = o_sh;
+  p.b = b, p.tq = tq, p.cap = cap, p.hq = hq, p.hk = hk, p.d = d;
+  p.window = window, p.sinks = sinks, p.held_sinks = sinks < cap ? sinks : cap, p.scale = scale;
+  cudaError_t e = token_status_address(&p.status);
+  if (e == cudaSuccess) e = launch_attn_any(p, precision, static_cast<cudaStream_t>(stream));
+  return finish(e, "window_attention");
+}
+
+oidnx_status oidnx_token_sync_status(void* stream) {
+  int word = 0;
+  const cudaError_t e = token_status_take(&word, static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess && word)
+    return fail(OIDNX_ERR_TIMEOUT, "a device-side wait gave up (status bits 0x%x)", word);
+  return finish(e, "token_sync_status");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- error word
+namespace {
+__device__ int g_token_status;
+constexpr int kMaxDevices = 64;
+std::mutex g_status_mutex;
+int* g_status_addr[kMaxDevices] = {};
+}  // namespace
+
+// The current device's error word (looked up once a device).
+cudaError_t oidnx::token_status_address(int** out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(g_status_mutex);
+  if (!g_status_addr[dev]) {
+    void* p = nullptr;
+    e = cudaGetSymbolAddress(&p, g_token_status);
+    if (e != cudaSuccess) return e;
+    g_status_addr[dev] = static_cast<int*>(p);
+  }
+  *out = g_status_addr[dev];
+  return cudaSuccess;
+}
+
+// Wait for `stream`, then read and clear the error word.
+cudaError_t oidnx::token_status_take(int* word, cudaStream_t stream) {
+  int* at = nullptr;
+  cudaError_t e = token_status_address(&at);
+  if (e != cudaSuccess) return e;
+  e = cudaMemcpyAsync(word, at, sizeof(int), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e == cudaSuccess && *word) {
+    e = cudaMemsetAsync(at, 0, sizeof(int), stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  }
+  return e;
+}

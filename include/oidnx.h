@@ -57,6 +57,8 @@ typedef enum {
 enum { OIDNX_IMAGE_COLOR = 0, OIDNX_IMAGE_ALBEDO = 1, OIDNX_IMAGE_NORMAL = 2,
        OIDNX_IMAGE_OUTPUT = 3 };
 enum { OIDNX_PRECISION_AUTO = 0, OIDNX_PRECISION_FP32 = 1, OIDNX_PRECISION_FP16 = 2 };
+/* bf16 storage: the token operators only (filters and convs refuse it).  */
+enum { OIDNX_PRECISION_BF16 = 3 };
 enum { OIDNX_TRANSFER_PU = 0, OIDNX_TRANSFER_LOG = 1 };
 
 /* Create a filter from an "OXW1" weight blob (host memory, copied).
@@ -340,6 +342,100 @@ oidnx_status oidnx_conv_create(const float* weight, const float* bias, int cout,
 oidnx_status oidnx_conv_execute(oidnx_conv* c, const void* in, void* out, int w,
                                 int h, int relu, void* stream);
 void oidnx_conv_release(oidnx_conv* c);
+
+/* ---- token operators ----------------------------------------------------
+ * The serving side of an attention layer over tokens (the pixels of a
+ * bottleneck map, or one token per frame along a stream): a linear layer, the
+ * norm and rotation of queries and keys with their append to a cache, and
+ * attention with a sliding window and sinks over that cache.  The pages have
+ * no counterpart of these calls; they are an addition of this library.
+ *
+ * For all of them: direct calls on device pointers, enqueued on `stream`;
+ * nothing is allocated, and nothing is kept from one call for the next.
+ * Strides and row lengths count elements.  Pointers need the alignment of
+ * their elements only; 16-byte aligned pointers and strides of whole 16
+ * bytes run the fast forms.  Sums, norms and softmax statistics are fp32 and
+ * each output is rounded once.  The caller keeps every buffer alive until
+ * the work on `stream` is done, and orders the call after whatever wrote its
+ * inputs on other streams.  Calls can be captured into a CUDA graph once one
+ * call has been made on the device.  A device-side timeout is reported by
+ * oidnx_token_sync_status.  */
+
+enum { OIDNX_ACT_NONE = 0, OIDNX_ACT_RELU = 1, OIDNX_ACT_GELU = 2 /* erf */,
+       OIDNX_ACT_GELU_TANH = 3, OIDNX_ACT_SILU = 4 };
+
+/* Linear layer with its epilogue:
+ *   y[i][j] = act(sum_k x[i][k] w[j][k] + bias[j]) + residual[i][j]
+ * for i < m, j < n, k < K.  x, w, residual and y are matrices with row
+ * strides ldx, ldw, ldr, ldy; bias ([n]) and residual may be NULL; y may be
+ * the residual (same pointer and stride) but overlaps nothing else.  All of
+ * one type: precision OIDNX_PRECISION_FP16 or _BF16.  k = 0 gives
+ * act(bias) + residual.
+ * Errors: INVALID_ARGUMENT (NULL, negative sizes, strides shorter than
+ * rows, misaligned pointers, unknown act or precision), UNSUPPORTED (fp32),
+ * CUDA.  */
+oidnx_status oidnx_linear(const void* x, long long ldx, const void* w, long long ldw, const void* bias,
+                          const void* residual, long long ldr, void* y, long long ldy, int m, int n,
+                          int k, int act, int precision, void* stream);
+
+/* Norm of each query and key head, rotation by position, and the append of
+ * keys and values to a cache.  For token i and head h, with x of d values:
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (weight [d], NULL: 1)
+ *   the pairs (a, b) of y's first `rot` values become (a c - b s, b c + a s)
+ * where pair r is values (r, r + rot / 2), or (2 r, 2 r + 1) with
+ * interleaved = 1, and c, s = cos_table, sin_table[positions[i]][r] (fp32
+ * [table_rows][rot / 2]).  A position outside the table gives NaN in the
+ * rotated values.  Queries go to row i of q_out; keys, and values unchanged,
+ * to row slots[i] of k_out and v_out (NULL slots: row i).  A token whose row
+ * is outside [0, cache_rows) has its key and value dropped (padding).  v and
+ * v_out may both be NULL.  *_st and *_sh are the token (row) and head
+ * strides.  Outputs may be their own inputs (same pointer and strides, and
+ * no slots); two tokens of one call must not share a slot.
+ * precision: OIDNX_PRECISION_FP32, _FP16 or _BF16 (heads and weights).
+ * Errors: INVALID_ARGUMENT (NULL, sizes, odd rot or rot > d, eps, misaligned
+ * pointers, unknown precision), UNSUPPORTED (over 65536 heads), CUDA.  */
+oidnx_status oidnx_qk_norm_rope(const void* q, long long q_st, long long q_sh, void* q_out,
+                                long long qo_st, long long qo_sh, const void* k, long long k_st,
+                                long long k_sh, void* k_out, long long ko_st, long long ko_sh,
+                                const void* v, long long v_st, long long v_sh, void* v_out,
+                                long long vo_st, long long vo_sh, const void* q_weight,
+                                const void* k_weight, float eps, const float* cos_table,
+                                const float* sin_table, long long table_rows, const int* positions,
+                                const int* slots, long long cache_rows, int t, int hq, int hk, int d,
+                                int rot, int interleaved, int precision, void* stream);
+
+/* Attention with a sliding window and sinks, over a linear or ring cache.
+ * Sequence s has q_lens[s] queries (rows 0 .. of q; NULL: tq) and kv_lens[s]
+ * keys written so far, the queries' own among them (NULL: cap).  Query i
+ * stands at position p = kv_len - q_len + i.  It sees key j when j <= p and
+ * (window == 0 or j > p - window or j < sinks), if the cache still holds it:
+ * key j sits in slot j while j < cap, and once cap keys are written the slots
+ * behind the sinks are a ring, key j in slot sinks + (j - sinks) mod
+ * (cap - sinks).  (A stream of any length thus needs sinks + window slots.)
+ *   o = sum_j softmax_j(scale q.k_j) v_j,  lse = log(sum_j exp(scale q.k_j))
+ * A query that sees no key (also one before the first key, p < 0) and rows
+ * from q_len on give o = 0 and lse = -inf.  Slots without a seen key are
+ * never used, whatever they hold.  Query head h reads key head
+ * h / (hq / hk).  Strides: *_sb sequence, *_st token or slot, *_sh head;
+ * the d values of a head are contiguous.  lse (fp32 [b][hq][tq]) may be NULL;
+ * q_lens and kv_lens are device arrays.  o overlaps no input.
+ * precision: OIDNX_PRECISION_FP16 or _BF16.  d <= 256; heads of up to 128
+ * values in whole 16-byte pieces run on the tensor cores.
+ * Errors: INVALID_ARGUMENT (NULL, sizes, hq not a multiple of hk, scale,
+ * misaligned pointers, unknown precision), UNSUPPORTED (fp32, d > 256, over
+ * 4e9 query heads), CUDA.  */
+oidnx_status oidnx_window_attention(const void* q, long long q_sb, long long q_st, long long q_sh,
+                                    const void* k, long long k_sb, long long k_st, long long k_sh,
+                                    const void* v, long long v_sb, long long v_st, long long v_sh,
+                                    void* o, long long o_sb, long long o_st, long long o_sh,
+                                    float* lse, const int* q_lens, const int* kv_lens, int b, int tq,
+                                    int cap, int hq, int hk, int d, int window, int sinks,
+                                    float scale, int precision, void* stream);
+
+/* Wait for `stream`, then report and clear the token operators' error word
+ * on the current device: OK, or TIMEOUT if a kernel's bounded wait gave up
+ * (that call's output is then undefined).  Errors: CUDA.  */
+oidnx_status oidnx_token_sync_status(void* stream);
 
 /* ---- host-only helpers (no GPU needed) --------------------------------- */
 
