@@ -1,0 +1,213 @@
+// Linear layer for few tokens: bound by the weight's bytes, so the weight is
+// the operand with 128 rows and the tokens are the narrow one,
+//   acc[j][i] = sum_k w[j][k] x[i][k],
+// and K is split over the CTAs of a cluster, so that every SM streams weights
+// however few output tiles there are.  Each CTA leaves its fp32 part of the
+// 128 x BN tile in its shared memory; after a cluster barrier every CTA sums
+// 128 / split rows over the parts (always in the same order) and applies the
+// epilogue.
+#include <type_traits>
+
+#include "linear_load.cuh"
+#include "ptx.cuh"
+#include "token.h"
+#include "token_math.cuh"
+
+namespace oidnx {
+namespace {
+
+constexpr int kThreads = 256;  // warp 0 loads, warp 1 multiplies, warps 4-7 read the accumulator; all join the sums
+constexpr int kGatherThreads = 256;
+
+template <int BN> struct Split {
+  static constexpr int kA = 128 * 128;
+  static constexpr int kB = BN * 128;
+  static constexpr int kStage = kA + kB;
+  // two CTAs per SM
+  static constexpr int kStages = 110 * 1024 / kStage;
+  static constexpr int kSmem = kStages * kStage + 2048;
+  static constexpr int kCols = BN < 32 ? 32 : BN;
+  static_assert(kStages * kStage >= 128 * BN * 4, "the parts reuse the stages");
+};
+
+template <typename T, int BN, bool GATHER>
+__global__ void __launch_bounds__(kThreads + (GATHER ? kGatherThreads : 0), GATHER ? 1 : 2)
+    linear_split_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                        const LinearParams p, const int split) {
+  using S = Split<BN>;
+  constexpr int NS = S::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* stages = smem_raw + pad;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stages + NS * S::kStage);
+  uint64_t* empty = full + NS;
+  uint64_t* done = empty + NS;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int j0 = blockIdx.x / split * 128, i0 = blockIdx.y * BN;
+  const int blocks = p.k > 0 ? (p.k + kKB - 1) / kKB : 1;
+  const int first = static_cast<int>(static_cast<int64_t>(blocks) * part / split);
+  const int last = static_cast<int>(static_cast<int64_t>(blocks) * (part + 1) / split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], GATHER ? kGatherThreads : 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    fence_mbarrier_init();
+  }
+  if (warp == 1) tmem_alloc(slot, S::kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  float* sums = reinterpret_cast<float*>(stages);  // [BN][128], once every product has read the stages
+  if (warp == 0) {
+    if (!GATHER && lane == 0) {
+      const uint64_t pol = l2_evict_normal();
+      uint32_t s = 0, ph = 0;
+      for (int k = first; k < last; ++k) {
+        if (!mbar_wait_bounded(&empty[s], ph ^ 1, p.status, kErrTimeoutProducer)) break;
+        uint8_t* A = stages + s * S::kStage;
+        mbar_arrive_expect_tx(&full[s], S::kStage);
+        tma_load_2d(A, &map_w, &full[s], k * kKB, j0, pol);
+        tma_load_2d(A + S::kA, &map_x, &full[s], k * kKB, i0, pol);
+        if (++s == NS) s = 0, ph ^= 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      const uint32_t idesc = idesc_16(std::is_same<T, __nv_bfloat16>::value, 128, BN);
+      uint32_t s = 0, ph = 0;
+      for (int k = first; k < last; ++k) {
+        if (!mbar_wait_bounded(&full[s], ph, p.status, kErrTimeoutMma)) break;
+        tc_fence_after();
+        const uint64_t ad = smem_desc_sw128(smem_u32(stages + s * S::kStage));
+        const uint64_t bd = smem_desc_sw128(smem_u32(stages + s * S::kStage + S::kA));
+#pragma unroll
+        for (int i = 0; i < kKB / 16; ++i) mma_f16_ss(tmem, ad + 2 * i, bd + 2 * i, idesc, k > first || i > 0);
+        mma_commit(&empty[s]);
+        if (++s == NS) s = 0, ph ^= 1;
+      }
+      mma_commit(done);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(done, 0, p.status, kErrTimeoutEpilogue));
+    tc_fence_after();
+    const int quarter = warp & 3;
+    if (ok) {
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 16) {
+        if (i0 + c >= p.m) break;
+        uint32_t raw[16];
+        tmem_ld16_nowait(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, raw);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          // an empty range of K has issued no product: its part is zero
+          sums[(c + i) * 128 + quarter * 32 + lane] = last > first ? __uint_as_float(raw[i]) : 0.f;
+      }
+    }
+  } else if (GATHER && warp >= 8) {
+    const int tid = threadIdx.x - kThreads;
+    uint32_t s = 0, ph = 0;
+    for (int k = first; k < last; ++k) {
+      if (!mbar_wait_bounded(&empty[s], ph ^ 1, p.status, kErrTimeoutProducer)) break;
+      uint8_t* A = stages + s * S::kStage;
+      gather_tile<128, kGatherThreads>(A, p.w, p.ldw, p.n, p.k, j0, k * kKB, tid);
+      if constexpr (BN * 8 >= kGatherThreads) {
+        gather_tile<BN, kGatherThreads>(A + S::kA, p.x, p.ldx, p.m, p.k, i0, k * kKB, tid);
+      } else {
+        if (tid < BN * 8) gather_tile<BN, BN * 8>(A + S::kA, p.x, p.ldx, p.m, p.k, i0, k * kKB, tid);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&full[s]);
+      if (++s == NS) s = 0, ph ^= 1;
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if (split > 1) cluster_sync();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kCols);
+  }
+
+  // this CTA's rows of the tile, for all its tokens
+  const int rows = 128 / split, r0 = part * rows;
+  const int tokens = min(BN, p.m - i0);
+  for (int e = threadIdx.x; e < rows * tokens; e += blockDim.x) {
+    const int i = e / rows, r = r0 + e % rows;
+    const int j = j0 + r;
+    if (j >= p.n) continue;
+    float z;
+    if (split == 1) {
+      z = sums[i * 128 + r];
+    } else {
+      float v[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        v[s] = s < split ? ld_cluster_f32(map_to_rank(sums + i * 128 + r, s)) : 0.f;
+      z = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
+    if (p.bias) z += to_f32<T>(static_cast<const T*>(p.bias)[j]);
+    float one[1] = {z};
+    activate_all(one, p.act);
+    z = one[0];
+    const int64_t row = i0 + i;
+    if (p.residual) z += to_f32<T>(static_cast<const T*>(p.residual)[row * p.ldr + j]);
+    static_cast<T*>(p.y)[row * p.ldy + j] = from_f32<T>(z);
+  }
+  if (split > 1) {
+    __syncwarp();
+    cluster_sync();  // a part stays until everyone has read it
+  }
+}
+
+template <typename T, int BN, bool GATHER>
+cudaError_t launch(const LinearTcLaunch& L, cudaStream_t stream) {
+  using S = Split<BN>;
+  auto kernel = linear_split_kernel<T, BN, GATHER>;
+  static SmemReady ready;
+  const cudaError_t e = ready.ensure(kernel, S::kSmem, L.device);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((L.p.n + 127) / 128 * L.split, (L.p.m + BN - 1) / BN);
+  cfg.blockDim = dim3(kThreads + (GATHER ? kGatherThreads : 0));
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = L.split;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = L.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, L.map_x, L.map_w, L.p, L.split);
+}
+
+template <typename T, bool GATHER>
+cudaError_t launch_bn(const LinearTcLaunch& L, cudaStream_t stream) {
+  if (L.bn <= 16) return launch<T, 16, GATHER>(L, stream);
+  if (L.bn <= 32) return launch<T, 32, GATHER>(L, stream);
+  if (L.bn <= 64) return launch<T, 64, GATHER>(L, stream);
+  return launch<T, 128, GATHER>(L, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_split(const LinearTcLaunch& L, bool bf16, cudaStream_t stream) {
+  if (bf16)
+    return L.gather ? launch_bn<__nv_bfloat16, true>(L, stream) : launch_bn<__nv_bfloat16, false>(L, stream);
+  return L.gather ? launch_bn<__half, true>(L, stream) : launch_bn<__half, false>(L, stream);
+}
+
+}  // namespace oidnx

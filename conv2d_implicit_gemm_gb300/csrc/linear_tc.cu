@@ -1,0 +1,395 @@
+// Linear layer on the 5th-generation tensor cores: y = act(x w^T + bias) + residual.
+//
+//  * Output tiles of 128 x BN per CTA, or 256 x 256 per CTA pair
+//    (cta_group::2: each CTA holds its 128 rows of x and half of the tile's
+//    rows of w, and the pair reads both), fp32 accumulators in tensor memory,
+//    two of them, so that one tile's epilogue runs under the next tile's
+//    products.  Persistent CTAs walk the tiles in groups of 8 row blocks, so
+//    that the tiles in flight share their operands in L2.
+//  * K in blocks of 64 values: one 128-byte swizzled TMA box per operand and
+//    block.  Matrices whose rows do not start on 16 bytes are gathered by
+//    eight more warps into the same layout.
+//  * Epilogue: eight warps, each 32 rows x half the columns, through 32 x 64
+//    tiles of 16-bit values that TMA stores (and, for the residual, loads
+//    first); outputs that TMA cannot store go through 32 x 32 fp32 tiles and
+//    single values, coalesced along the row.
+//  * The MMA warp overwrites the accumulator with its first product and adds
+//    the others; products outside the matrix are zeros that TMA fills in.
+//  * Every wait is bounded.  A role that gives up records it and leaves its
+//    loop; its own loads were issued before that wait of two seconds and have
+//    landed, and the other roles give up in turn, so the block ends together.
+#include <climits>
+#include <type_traits>
+
+#include "linear_load.cuh"
+#include "ptx.cuh"
+#include "token.h"
+#include "token_math.cuh"
+
+namespace oidnx {
+namespace {
+
+constexpr int kEpiWarps = 8;
+constexpr int kGatherWarps = 8;
+constexpr int kFirstEpi = 4;  // warp 0 loads, warp 1 multiplies, 2 and 3 rest
+constexpr int kLinThreads = (kFirstEpi + kEpiWarps) * 32;
+constexpr int kLinThreadsGather = kLinThreads + kGatherWarps * 32;
+constexpr int kStageOut = 4096;  // bytes of staging per epilogue warp
+constexpr int kRowGroup = 8;     // row blocks walked together
+
+template <int CG, int BN> struct Shape {
+  static constexpr int kA = 128 * 128;              // bytes of a CTA's x block
+  static constexpr int kB = BN / CG * 128;          // bytes of its w block
+  static constexpr int kStage = kA + kB;
+  static constexpr int kStages = (227 * 1024 - 2048 - kEpiWarps * kStageOut) / kStage < 8
+                                     ? (227 * 1024 - 2048 - kEpiWarps * kStageOut) / kStage
+                                     : 8;
+  static constexpr int kSmem = kStages * kStage + kEpiWarps * kStageOut + 2048;
+  static constexpr int kCols = 2 * BN < 32 ? 32 : 2 * BN;
+};
+
+struct TcArgs {
+  LinearParams p;
+  int tiles_m, tiles_n;
+  int tma_out;  // y (and the residual) go through TMA
+};
+
+// Walk step -> tile: groups of kRowGroup row blocks, column by column.
+__device__ __forceinline__ void tile_of(const TcArgs& a, int t, int* tm, int* tn) {
+  const int per = kRowGroup * a.tiles_n;
+  const int g = t / per, i = t - g * per;
+  const int rows = min(kRowGroup, a.tiles_m - g * kRowGroup);
+  *tn = i / rows;
+  *tm = g * kRowGroup + i - *tn * rows;
+}
+
+// Bias of 32 columns from c0 on (zeros outside), for every lane.
+template <typename T>
+__device__ __forceinline__ void add_bias(const LinearParams& p, int c0, float (&v)[32]) {
+  if (!p.bias) return;
+  const T* b = static_cast<const T*>(p.bias) + c0;
+  if (c0 + 32 <= p.n && (reinterpret_cast<uintptr_t>(b) & 15) == 0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float f[8];
+      Vec16<T>::unpack(__ldg(reinterpret_cast<const uint4*>(b) + q), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[8 * q + i] += f[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (c0 + i < p.n) v[i] += to_f32<T>(b[i]);
+  }
+}
+
+// Columns [c0, c0 + COLS) of 32 rows from r0 on, accumulators at `tmem` (lane
+// = row), through the warp's staging tile.  `bar`/`phase`: residual loads.
+template <typename T, int COLS>
+__device__ __forceinline__ bool epilogue_tma(const TcArgs& a, const CUtensorMap* map_y, const CUtensorMap* map_r,
+                                             uint32_t tmem, int r0, int c0, uint8_t* stage, uint64_t* bar,
+                                             uint32_t* phase, int lane) {
+  const LinearParams& p = a.p;
+  constexpr int W = COLS < 64 ? COLS : 64;  // columns of one staging tile
+#pragma unroll 1
+  for (int c = 0; c < COLS; c += W) {
+    if (c0 + c >= p.n) break;
+    if (lane == 0) {
+      bulk_wait_read<0>();  // the store before has left the tile
+      if (p.residual) {
+        mbar_arrive_expect_tx(bar, 32 * W * 2);
+        tma_load_2d(stage, map_r, bar, c0 + c, r0, l2_evict_first());
+      }
+    }
+    __syncwarp();
+    if (p.residual) {
+      const bool landed = mbar_wait_bounded(bar, *phase, p.status, kErrTimeoutEpilogue);
+      *phase ^= 1;
+      if (!__all_sync(0xFFFFFFFFu, landed)) return false;
+    }
+#pragma unroll
+    for (int h = 0; h < W; h += 32) {
+      uint32_t raw[32];
+      tmem_ld32_nowait(tmem + c + h, raw);
+      tmem_wait_ld();
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
+      add_bias<T>(p, c0 + c + h, v);
+      activate_all(v, p.act);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int piece = h / 8 + q;
+        // 128-byte rows swizzled by row mod 8; 64-byte rows by (row / 2) mod 4
+        uint4* at = reinterpret_cast<uint4*>(
+            stage + lane * (W * 2) + ((W == 64 ? piece ^ (lane & 7) : piece ^ ((lane >> 1) & 3)) << 4));
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = v[8 * q + i];
+        if (p.residual) {
+          float f[8];
+          Vec16<T>::unpack(*at, f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] += f[i];
+        }
+        *at = Vec16<T>::pack(o);
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(map_y, stage, c0 + c, r0);
+      bulk_commit();
+    }
+  }
+  return true;
+}
+
+// The same through single values: any row stride and alignment.
+template <typename T, int COLS>
+__device__ __forceinline__ void epilogue_any(const TcArgs& a, uint32_t tmem, int r0, int c0, uint8_t* stage, int lane) {
+  const LinearParams& p = a.p;
+  float* tile = reinterpret_cast<float*>(stage);  // [row][column ^ row]
+#pragma unroll 1
+  for (int c = 0; c < COLS; c += 32) {
+    if (c0 + c >= p.n) break;
+    uint32_t raw[32];
+    tmem_ld32_nowait(tmem + c, raw);
+    tmem_wait_ld();
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
+    add_bias<T>(p, c0 + c, v);
+    activate_all(v, p.act);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) tile[lane * 32 + (i ^ lane)] = v[i];
+    __syncwarp();
+    const int col = c0 + c + lane, rows = min(32, p.m - r0);
+    if (col < p.n) {
+      T* y = static_cast<T*>(p.y) + r0 * p.ldy + col;
+      const T* res = static_cast<const T*>(p.residual) + r0 * p.ldr + col;
+#pragma unroll 8
+      for (int r = 0; r < rows; ++r) {
+        float z = tile[r * 32 + (lane ^ r)];
+        if (p.residual) z += to_f32<T>(res[r * p.ldr]);
+        y[r * p.ldy] = from_f32<T>(z);
+      }
+    }
+    __syncwarp();
+  }
+}
+
+template <typename T, int CG, int BN, bool GATHER>
+__global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
+    linear_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                     const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_y,
+                     const TcArgs a) {
+  using S = Shape<CG, BN>;
+  constexpr int NS = S::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* stages = smem_raw + pad;  // every tile starts on 1024 bytes
+  uint8_t* staging = stages + NS * S::kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStageOut);
+  uint64_t* empty = full + NS;
+  uint64_t* tfull = empty + NS;    // [2]
+  uint64_t* tempty = tfull + 2;    // [2]
+  uint64_t* rbar = tempty + 2;     // [kEpiWarps] residual tiles
+  uint32_t* slot = reinterpret_cast<uint32_t*>(rbar + kEpiWarps);
+  const LinearParams& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+  const int kb = p.k > 0 ? (p.k + kKB - 1) / kKB : 1;  // k = 0: one block of zeros
+  const int tiles = a.tiles_m * a.tiles_n;
+  const int walker = blockIdx.x / CG, walkers = gridDim.x / CG;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], GATHER ? kGatherWarps * 32 : 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], CG * kEpiWarps);
+    }
+    for (int w = 0; w < kEpiWarps; ++w) mbar_init(&rbar[w], 1);
+    fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    if (CG == 2) tmem_alloc_pair(slot, S::kCols);
+    else tmem_alloc(slot, S::kCols);
+  }
+  tc_fence_before();
+  if (CG == 2) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  if (warp == 0) {
+    if (!GATHER && lane == 0) {
+      prefetch_tmap(&map_x);
+      prefetch_tmap(&map_w);
+      const uint64_t pol = l2_evict_normal();
+      uint32_t s = 0, ph = 0;
+      bool ok = true;
+      for (int t = walker; t < tiles && ok; t += walkers) {
+        int tm, tn;
+        tile_of(a, t, &tm, &tn);
+        const int row = (tm * CG + static_cast<int>(rank)) * 128;
+        const int col = tn * BN + static_cast<int>(rank) * (BN / CG);
+        for (int k = 0; k < kb; ++k) {
+          ok = mbar_wait_bounded(&empty[s], ph ^ 1, p.status, kErrTimeoutProducer);
+          if (!ok) break;
+          uint8_t* A = stages + s * S::kStage;
+          if (CG == 2) {
+            const uint32_t bar = map_to_rank(&full[s], 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStage);
+            tma_load_2d_pair(A, &map_x, bar, k * kKB, row, pol);
+            tma_load_2d_pair(A + S::kA, &map_w, bar, k * kKB, col, pol);
+          } else {
+            mbar_arrive_expect_tx(&full[s], S::kStage);
+            tma_load_2d(A, &map_x, &full[s], k * kKB, row, pol);
+            tma_load_2d(A + S::kA, &map_w, &full[s], k * kKB, col, pol);
+          }
+          if (++s == NS) s = 0, ph ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc = idesc_16(std::is_same<T, __nv_bfloat16>::value, 128 * CG, BN);
+      uint32_t s = 0, ph = 0;
+      int n = 0;
+      bool ok = true;
+      for (int t = walker; t < tiles && ok; t += walkers, ++n) {
+        const int b = n & 1;
+        ok = mbar_wait_bounded(&tempty[b], ((n >> 1) & 1) ^ 1, p.status, kErrTimeoutMma);
+        tc_fence_after();
+        const uint32_t d = tmem + b * BN;
+        for (int k = 0; k < kb && ok; ++k) {
+          ok = mbar_wait_bounded(&full[s], ph, p.status, kErrTimeoutMma);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t ad = smem_desc_sw128(smem_u32(stages + s * S::kStage));
+          const uint64_t bd = smem_desc_sw128(smem_u32(stages + s * S::kStage + S::kA));
+#pragma unroll
+          for (int i = 0; i < kKB / 16; ++i) {
+            if (CG == 2) mma_f16_ss_pair(d, ad + 2 * i, bd + 2 * i, idesc, k > 0 || i > 0);
+            else mma_f16_ss(d, ad + 2 * i, bd + 2 * i, idesc, k > 0 || i > 0);
+          }
+          if (CG == 2) mma_commit_pair(&empty[s]);
+          else mma_commit(&empty[s]);
+          if (++s == NS) s = 0, ph ^= 1;
+        }
+        if (CG == 2) mma_commit_pair(&tfull[b]);
+        else mma_commit(&tfull[b]);
+      }
+    }
+  } else if (warp >= kFirstEpi && warp < kFirstEpi + kEpiWarps) {
+    const int e = warp - kFirstEpi;
+    const int quarter = warp & 3, half = e >> 2;  // the TMEM lanes a warp may read; its columns
+    uint8_t* stage = staging + e * kStageOut;
+    uint32_t rphase = 0;
+    int n = 0;
+    for (int t = walker; t < tiles; t += walkers, ++n) {
+      const int b = n & 1;
+      int tm, tn;
+      tile_of(a, t, &tm, &tn);
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[b], (n >> 1) & 1, p.status, kErrTimeoutEpilogue))) break;
+      tc_fence_after();
+      const int r0 = (tm * CG + static_cast<int>(rank)) * 128 + quarter * 32;
+      const int c0 = tn * BN + half * (BN / 2);
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * BN + half * (BN / 2);
+      if (r0 < p.m) {
+        if (a.tma_out) {
+          if (!epilogue_tma<T, BN / 2>(a, &map_y, &map_r, acc, r0, c0, stage, &rbar[e], &rphase, lane)) break;
+        } else {
+          epilogue_any<T, BN / 2>(a, acc, r0, c0, stage, lane);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2) mbar_arrive_cluster(map_to_rank(&tempty[b], 0));
+        else mbar_arrive(&tempty[b]);
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  } else if (GATHER && warp >= kFirstEpi + kEpiWarps) {
+    const int tid = threadIdx.x - kLinThreads;
+    uint32_t s = 0, ph = 0;
+    bool ok = true;
+    for (int t = walker; t < tiles && ok; t += walkers) {
+      int tm, tn;
+      tile_of(a, t, &tm, &tn);
+      for (int k = 0; k < kb; ++k) {
+        ok = mbar_wait_bounded(&empty[s], ph ^ 1, p.status, kErrTimeoutProducer);
+        if (!ok) break;
+        uint8_t* A = stages + s * S::kStage;
+        gather_tile<128, kGatherWarps * 32>(A, p.x, p.ldx, p.m, p.k, tm * 128, k * kKB, tid);
+        gather_tile<BN, kGatherWarps * 32>(A + S::kA, p.w, p.ldw, p.n, p.k, tn * BN, k * kKB, tid);
+        fence_proxy_async_smem();
+        mbar_arrive(&full[s]);
+        if (++s == NS) s = 0, ph ^= 1;
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if (CG == 2) cluster_sync();  // the pair's products read both CTAs' shared memory
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    if (CG == 2) tmem_dealloc_pair(tmem, S::kCols);
+    else tmem_dealloc(tmem, S::kCols);
+  }
+}
+
+template <typename T, int CG, int BN, bool GATHER>
+cudaError_t launch(const LinearTcLaunch& L, cudaStream_t stream) {
+  using S = Shape<CG, BN>;
+  TcArgs a = {L.p, (L.p.m + 128 * CG - 1) / (128 * CG), (L.p.n + BN - 1) / BN, L.tma_out};
+  auto kernel = linear_tc_kernel<T, CG, BN, GATHER>;
+  static SmemReady ready;
+  const cudaError_t e = ready.ensure(kernel, S::kSmem, L.device);
+  if (e != cudaSuccess) return e;
+  const long long tiles = static_cast<long long>(a.tiles_m) * a.tiles_n;
+  if (tiles > INT_MAX) return cudaErrorInvalidValue;
+  const int walkers = static_cast<int>(tiles < L.sms / CG ? tiles : L.sms / CG);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(walkers * CG);
+  cfg.blockDim = dim3(GATHER ? kLinThreadsGather : kLinThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = CG;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, L.map_x, L.map_w, L.map_r, L.map_y, a);
+}
+
+template <typename T>
+cudaError_t launch_t(const LinearTcLaunch& L, cudaStream_t stream) {
+  if (L.gather) {
+    if (L.bn == 64) return launch<T, 1, 64, true>(L, stream);
+    return launch<T, 1, 128, true>(L, stream);
+  }
+  if (L.pair) return launch<T, 2, 256, false>(L, stream);
+  if (L.bn == 64) return launch<T, 1, 64, false>(L, stream);
+  return launch<T, 1, 128, false>(L, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_tc(const LinearTcLaunch& L, bool bf16, cudaStream_t stream) {
+  return bf16 ? launch_t<__nv_bfloat16>(L, stream) : launch_t<__half>(L, stream);
+}
+
+}  // namespace oidnx

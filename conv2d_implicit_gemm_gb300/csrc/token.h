@@ -3,6 +3,8 @@
 // launchers that token_host.cpp chooses from.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -81,6 +83,31 @@ struct LinearParams {
   int* status;
 };
 
+// Launch of a tensor-core form; maps that a form does not use are zero.
+struct LinearTcLaunch {
+  LinearParams p;
+  CUtensorMap map_x, map_w, map_r, map_y;
+  int device, sms;
+  int bn;       // columns per tile: 64 or 128 (pair: 256); split form: tokens per tile
+  int pair;     // CTA pairs on 256 x 256 tiles
+  int gather;   // x and w through plain loads
+  int tma_out;  // y and residual through TMA
+  int split;    // split form: CTAs of a cluster along K
+};
+
+// Which devices a kernel's shared-memory limit has been raised on.
+struct SmemReady {
+  std::atomic<uint64_t> done{0};
+  template <typename K> cudaError_t ensure(K kernel, int bytes, int device) {
+    const uint64_t bit = uint64_t(1) << device;  // devices 0 to 63
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
+
 // ---------------------------------------------------------------- norm and rotation
 // Index 0 = queries, 1 = keys, 2 = values; strides in elements.
 struct NormParams {
@@ -138,7 +165,8 @@ __device__ __forceinline__ int attn_slot(const AttnParams& p, int pos) {
   return p.held_sinks + (pos - p.held_sinks) % (p.cap - p.held_sinks);
 }
 
-cudaError_t launch_linear_any(const LinearParams& p, int precision, cudaStream_t stream);
+cudaError_t launch_linear_tc(const LinearTcLaunch& L, bool bf16, cudaStream_t stream);
+cudaError_t launch_linear_split(const LinearTcLaunch& L, bool bf16, cudaStream_t stream);
 cudaError_t launch_norm_vec(const NormParams& p, int precision, cudaStream_t stream);
 cudaError_t launch_norm_any(const NormParams& p, int precision, cudaStream_t stream);
 cudaError_t launch_attn_any(const AttnParams& p, int precision, cudaStream_t stream);

@@ -11,7 +11,7 @@
 
 namespace oidnx {
 oidnx_status report_error(oidnx_status status, const char* message);
-cudaError_t token_status_address(int** out);
+cudaError_t token_device(int* device, int* sms, int** status);
 cudaError_t token_status_take(int* word, cudaStream_t stream);
 }  // namespace oidnx
 
@@ -39,6 +39,73 @@ oidnx_status finish(cudaError_t e, const char* call) {
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+// ---------------------------------------------------------------- tensor maps
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<EncodeFn>(ptr)
+               : EncodeFn(nullptr);
+  }();
+  return fn;
+}
+
+// A matrix of rows x cols 16-bit values with row stride ld, in boxes of
+// box_cols (64: 128-byte rows, 32: 64-byte rows) x box_rows, swizzled.
+bool matrix_map(CUtensorMap* map, bool bf16, const void* base, int64_t ld, int rows, int cols, int box_rows, int box_cols) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+  const EncodeFn fn = encode_fn();
+  return fn && fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                  const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows that TMA can address: all start on 16 bytes, strides below 2^40 bytes.
+bool tma_rows(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0 && ld < (int64_t(1) << 38); }
+
+// ---------------------------------------------------------------- linear: choice of form
+cudaError_t run_linear(const LinearParams& params, bool bf16, cudaStream_t stream) {
+  LinearTcLaunch L = {};
+  L.p = params;
+  LinearParams& p = L.p;
+  cudaError_t e = token_device(&L.device, &L.sms, &p.status);
+  if (e != cudaSuccess) return e;
+  L.gather = p.k == 0 || !tma_rows(p.x, p.ldx) || !tma_rows(p.w, p.ldw);
+  bool ok = true;
+  if (p.m <= 128) {
+    L.bn = p.m <= 16 ? 16 : p.m <= 32 ? 32 : p.m <= 64 ? 64 : 128;
+    const int tiles = (p.n + 127) / 128 * ((p.m + L.bn - 1) / L.bn), blocks = (p.k + 63) / 64;
+    L.split = 1;
+    while (L.split < 8 && tiles * L.split * 2 <= 2 * L.sms && blocks / (L.split * 2) >= 4) L.split *= 2;
+    if (!L.gather)
+      ok = matrix_map(&L.map_x, bf16, p.x, p.ldx, p.m, p.k, L.bn, 64) &&
+           matrix_map(&L.map_w, bf16, p.w, p.ldw, p.n, p.k, 128, 64);
+    return ok ? launch_linear_split(L, bf16, stream) : cudaErrorInvalidValue;
+  }
+  const auto tiles = [&](int rows, int cols) { return int64_t((p.m + rows - 1) / rows) * ((p.n + cols - 1) / cols); };
+  L.pair = !L.gather && tiles(256, 256) >= L.sms / 2 - 8;
+  L.bn = L.pair ? 256 : tiles(128, 128) * 2 <= L.sms ? 64 : 128;
+  L.tma_out = tma_rows(p.y, p.ldy) && (!p.residual || tma_rows(p.residual, p.ldr));
+  if (!L.gather)
+    ok = matrix_map(&L.map_x, bf16, p.x, p.ldx, p.m, p.k, 128, 64) &&
+         matrix_map(&L.map_w, bf16, p.w, p.ldw, p.n, p.k, L.pair ? 128 : L.bn, 64);
+  if (L.tma_out) {
+    const int cols = L.bn == 64 ? 32 : 64;
+    ok = ok && matrix_map(&L.map_y, bf16, p.y, p.ldy, p.m, p.n, 32, cols) &&
+         (!p.residual || matrix_map(&L.map_r, bf16, p.residual, p.ldr, p.m, p.n, 32, cols));
+  }
+  return ok ? launch_linear_tc(L, bf16, stream) : cudaErrorInvalidValue;
+}
+
 }  // namespace
 
 extern "C" {
@@ -62,9 +129,7 @@ oidnx_status oidnx_linear(const void* x, long long ldx, const void* w, long long
   p.x = x, p.w = w, p.bias = bias, p.residual = residual, p.y = y;
   p.ldx = ldx, p.ldw = ldw, p.ldr = ldr, p.ldy = ldy;
   p.m = m, p.n = n, p.k = k, p.act = act;
-  cudaError_t e = token_status_address(&p.status);
-  if (e == cudaSuccess) e = launch_linear_any(p, precision, static_cast<cudaStream_t>(stream));
-  return finish(e, "linear");
+  return finish(run_linear(p, precision == OIDNX_PRECISION_BF16, static_cast<cudaStream_t>(stream)), "linear");
 }
 
 oidnx_status oidnx_qk_norm_rope(const void* q, long long q_st, long long q_sh, void* q_out, long long qo_st,
@@ -149,7 +214,8 @@ oidnx_status oidnx_window_attention(const void* q, long long q_sb, long long q_s
   p.o_s[0] = o_sb, p.o_s[1] = o_st, p.o_s[2] = o_sh;
   p.b = b, p.tq = tq, p.cap = cap, p.hq = hq, p.hk = hk, p.d = d;
   p.window = window, p.sinks = sinks, p.held_sinks = sinks < cap ? sinks : cap, p.scale = scale;
-  cudaError_t e = token_status_address(&p.status);
+  int device, sms;
+  cudaError_t e = token_device(&device, &sms, &p.status);
   if (e == cudaSuccess) e = launch_attn_any(p, precision, static_cast<cudaStream_t>(stream));
   return finish(e, "window_attention");
 }
@@ -168,31 +234,39 @@ oidnx_status oidnx_token_sync_status(void* stream) {
 namespace {
 __device__ int g_token_status;
 constexpr int kMaxDevices = 64;
-std::mutex g_status_mutex;
-int* g_status_addr[kMaxDevices] = {};
+struct DeviceInfo {
+  int* status = nullptr;
+  int sms = 0;
+};
+std::mutex g_device_mutex;
+DeviceInfo g_devices[kMaxDevices];
 }  // namespace
 
-// The current device's error word (looked up once a device).
-cudaError_t oidnx::token_status_address(int** out) {
+// The current device, its SM count and its error word (looked up once).
+cudaError_t oidnx::token_device(int* device, int* sms, int** status) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  std::lock_guard<std::mutex> lock(g_status_mutex);
-  if (!g_status_addr[dev]) {
+  std::lock_guard<std::mutex> lock(g_device_mutex);
+  DeviceInfo& d = g_devices[dev];
+  if (!d.status) {
     void* p = nullptr;
-    e = cudaGetSymbolAddress(&p, g_token_status);
+    e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaGetSymbolAddress(&p, g_token_status);
     if (e != cudaSuccess) return e;
-    g_status_addr[dev] = static_cast<int*>(p);
+    d.status = static_cast<int*>(p);
   }
-  *out = g_status_addr[dev];
+  *device = dev;
+  *sms = d.sms;
+  *status = d.status;
   return cudaSuccess;
 }
 
 // Wait for `stream`, then read and clear the error word.
 cudaError_t oidnx::token_status_take(int* word, cudaStream_t stream) {
-  int* at = nullptr;
-  cudaError_t e = token_status_address(&at);
+  int device, sms, *at = nullptr;
+  cudaError_t e = token_device(&device, &sms, &at);
   if (e != cudaSuccess) return e;
   e = cudaMemcpyAsync(word, at, sizeof(int), cudaMemcpyDeviceToHost, stream);
   if (e == cudaSuccess) e = cudaStreamSynchronize(stream);

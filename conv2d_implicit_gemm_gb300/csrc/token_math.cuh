@@ -5,16 +5,40 @@
 
 namespace oidnx {
 
-__device__ __forceinline__ float activate(float z, int act) {
+// 1 / (1 + e^-z): the hardware's exp2 and reciprocal are good to about 2^-22,
+// far below the 16-bit rounding that follows.  e^-z overflows to infinity
+// for z < -88, which gives the limit 0.
+__device__ __forceinline__ float sigmoid_fast(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
+template <int ACT> __device__ __forceinline__ float activate(float z) {
+  if constexpr (ACT == OIDNX_ACT_RELU) return z < 0.f ? 0.f : z;  // a NaN stays one
+  if constexpr (ACT == OIDNX_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  // 0.5 z (1 + tanh u) = z / (1 + e^-2u)
+  if constexpr (ACT == OIDNX_ACT_GELU_TANH)
+    return z * sigmoid_fast(1.5957691216057308f * fmaf(0.044715f * z, z * z, z));
+  if constexpr (ACT == OIDNX_ACT_SILU) return z * sigmoid_fast(z);
+  return z;
+}
+
+template <int N> __device__ __forceinline__ void activate_all(float (&v)[N], int act) {
   switch (act) {
-    case OIDNX_ACT_RELU: return z < 0.f ? 0.f : z;  // a NaN stays one
-    case OIDNX_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    case OIDNX_ACT_GELU_TANH: {
-      const float u = 0.79788456080286536f * fmaf(0.044715f * z, z * z, z);
-      return 0.5f * z * (1.f + tanhf(u));
-    }
-    case OIDNX_ACT_SILU: return z / (1.f + expf(-z));
-    default: return z;
+    case OIDNX_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = activate<OIDNX_ACT_RELU>(v[i]);
+      break;
+    case OIDNX_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = activate<OIDNX_ACT_GELU>(v[i]);
+      break;
+    case OIDNX_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = activate<OIDNX_ACT_GELU_TANH>(v[i]);
+      break;
+    case OIDNX_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = activate<OIDNX_ACT_SILU>(v[i]);
+      break;
+    default: break;
   }
 }
 
