@@ -1,6 +1,7 @@
 // Entry points of the token operators: argument checks and the choice of
 // kernel.  Each is a direct call on device pointers; nothing is kept from one
 // call for the next but the device error word.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -104,6 +105,27 @@ cudaError_t run_linear(const LinearParams& params, bool bf16, cudaStream_t strea
          (!p.residual || matrix_map(&L.map_r, bf16, p.residual, p.ldr, p.m, p.n, 32, cols));
   }
   return ok ? launch_linear_tc(L, bf16, stream) : cudaErrorInvalidValue;
+}
+
+// ---------------------------------------------------------------- attention: choice of form
+cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
+  int device, sms;
+  const cudaError_t e = token_device(&device, &sms, &p.status);
+  if (e != cudaSuccess) return e;
+  const int group = p.hq / p.hk;
+  bool pieces = p.d % 8 == 0 && p.d <= 128 && aligned(p.q, 16) && aligned(p.k, 16) && aligned(p.v, 16) && aligned(p.o, 16);
+  for (int i = 0; i < 3; ++i)
+    pieces = pieces && p.q_s[i] % 8 == 0 && p.k_s[i] % 8 == 0 && p.v_s[i] % 8 == 0 && p.o_s[i] % 8 == 0;
+  const int64_t rows = static_cast<int64_t>(p.tq) * group, units = static_cast<int64_t>(p.b) * p.hk * ((rows + 31) / 32);
+  if (pieces && rows <= 64 && units < (1 << 27)) {
+    // the most keys that a query tile can see
+    int64_t keys = p.cap;
+    if (p.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(p.window) + p.held_sinks + p.tq - 1);
+    int split = 1;
+    while (split < 8 && units * split < 2 * sms && keys / (2 * split) >= 128) split *= 2;
+    return launch_attn_token(p, precision == OIDNX_PRECISION_BF16, split, device, stream);
+  }
+  return launch_attn_any(p, precision, stream);
 }
 
 }  // namespace
@@ -214,10 +236,7 @@ oidnx_status oidnx_window_attention(const void* q, long long q_sb, long long q_s
   p.o_s[0] = o_sb, p.o_s[1] = o_st, p.o_s[2] = o_sh;
   p.b = b, p.tq = tq, p.cap = cap, p.hq = hq, p.hk = hk, p.d = d;
   p.window = window, p.sinks = sinks, p.held_sinks = sinks < cap ? sinks : cap, p.scale = scale;
-  int device, sms;
-  cudaError_t e = token_device(&device, &sms, &p.status);
-  if (e == cudaSuccess) e = launch_attn_any(p, precision, static_cast<cudaStream_t>(stream));
-  return finish(e, "window_attention");
+  return finish(run_attention(p, precision, static_cast<cudaStream_t>(stream)), "window_attention");
 }
 
 oidnx_status oidnx_token_sync_status(void* stream) {
