@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liboidnx.so")
 SOURCES = ["oidnx_host.cpp", "conv_tc.cu", "conv_pair.cu", "conv_final.cu", "conv_tail.cu",
            "conv_head.cu", "io_passes.cu", "noalloc.cu", "token_host.cpp", "linear_tc.cu", "linear_split.cu",
-           "qk_norm_rope.cu", "attn_any.cu", "attn_token.cu"]
+           "qk_norm_rope.cu", "attn_any.cu", "attn_token.cu", "attn_prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

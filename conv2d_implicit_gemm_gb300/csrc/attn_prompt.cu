@@ -1,0 +1,529 @@
+// Window attention for prompts on the 5th-generation tensor cores.
+//
+// A CTA takes two tiles of 128 query rows of one key head (queries x the heads
+// of its group, query-major, so that keys and values are read once for the
+// group) and walks the visible keys in tiles of 128: the sinks, then the
+// window, in runs of consecutive cache slots.
+//
+//   S = Q K^T (tcgen05, accumulators in tensor memory), softmax in registers
+//   (one thread a row), P in 16 bits over S in tensor memory, O += P V with P
+//   as the tensor-memory operand and V read as it lies (values contiguous).
+//
+//  * The two row tiles alternate on the tensor cores: one's softmax runs under
+//    the other's products.
+//  * The running maximum that P is relative to follows the true one only when
+//    it falls more than 2^8 behind, so O is rescaled rarely; P <= 2^8 stays
+//    within 16 bits and the sums are fp32, so nothing is lost by it.
+//  * P is rounded to the storage type, as both operands of a product have one
+//    type; its error is that of the inputs' own rounding and averages out
+//    over the keys.  The sum of the weights is taken before the rounding.
+//  * Tiles that every row sees whole skip the mask.  In the others a value
+//    that is no number must not reach rows that do not see it (0 x NaN):
+//    two warps look the tile's values over first, clear what lies past the
+//    keys, and where a key itself holds such a value the CTA's rows are done
+//    again one by one.
+//
+// Warps 0-3 and 4-7: softmax of row tile 0 and 1, rescaling, output; warp 8
+// loads (TMA), warp 9 multiplies, warps 10 and 11 look values over.
+#include <type_traits>
+
+#include "attn_row.cuh"
+#include "ptx.cuh"
+#include "token.h"
+
+namespace oidnx {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTileKeys = 128;
+
+template <int DB> struct Pr {  // DB: 64-value blocks of a head (1 or 2)
+  static constexpr int kTile = DB * 16384;  // 128 rows
+  static constexpr int kStages = DB == 2 ? 2 : 4;
+  static constexpr int kSmem = (2 + 2 * kStages) * kTile + 1024 + 512;
+};
+
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f2_of(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Value operand: rows of 64 values (128 bytes, swizzled) a key, 8 keys 1024
+// bytes apart, 64-value blocks 16384 bytes apart; values contiguous (N-major).
+__device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
+  return smem_desc_sw128(saddr) | (static_cast<uint64_t>(16384u >> 4) << 16);
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(src))
+               : "memory");
+}
+
+struct Tile {
+  int slot, pos, count;
+};
+
+// What a CTA works on; every role computes the same.
+struct Plan {
+  int b, kvh, group, per;  // per: queries of a row tile
+  int n, nq, pq;           // keys written, queries, position of query 0
+  int i00, min0, max0, min1, max1;  // first query; first and last position of each row tile (last < first: no row)
+  int sinks, n_sinks;                  // keys and tiles of the sinks' run
+  int begin, slot0, len_a, n_a, len_b; // the window: up to the ring's end, and from its start on
+  int tiles;
+
+  __device__ __forceinline__ Tile tile(const AttnParams& p, int j) const {
+    Tile t;
+    if (j < n_sinks) {
+      t.slot = t.pos = j * kTileKeys;
+      t.count = min(kTileKeys, sinks - t.pos);
+    } else if (j < n_sinks + n_a) {
+      const int o = (j - n_sinks) * kTileKeys;
+      t.slot = slot0 + o, t.pos = begin + o, t.count = min(kTileKeys, len_a - o);
+    } else {
+      const int o = (j - n_sinks - n_a) * kTileKeys;
+      t.slot = p.held_sinks + o, t.pos = begin + len_a + o, t.count = min(kTileKeys, len_b - o);
+    }
+    return t;
+  }
+  // query index, and whether row tile t has a row that sees anything
+  __device__ __forceinline__ int i0(int t) const { return i00 + t * per; }
+  __device__ __forceinline__ bool active(int t) const { return t ? max1 >= min1 : max0 >= min0; }
+  // Does some row of tile t see some key of the tile; does every row see every key?
+  __device__ __forceinline__ bool seen(const AttnParams& p, int t, const Tile& k) const {
+    const int lo = t ? min1 : min0, hi = t ? max1 : max0;
+    return hi >= lo && k.pos <= hi && (p.window == 0 || k.pos + k.count - 1 > lo - p.window || k.pos < p.sinks);
+  }
+  __device__ __forceinline__ bool whole(const AttnParams& p, int t, const Tile& k) const {
+    const int lo = t ? min1 : min0, hi = t ? max1 : max0;
+    return k.count == kTileKeys && k.pos + k.count - 1 <= lo &&
+           (p.window == 0 || k.pos > hi - p.window || k.pos + k.count <= p.sinks);
+  }
+  __device__ __forceinline__ bool looked_over(const AttnParams& p, const Tile& k) const {
+    return (seen(p, 0, k) && !whole(p, 0, k)) || (seen(p, 1, k) && !whole(p, 1, k));
+  }
+};
+
+__device__ __forceinline__ Plan make_plan(const AttnParams& p) {
+  Plan w;
+  const int heads = p.b * p.hk;
+  // row tiles from the last to the first (causal: the longest first), the heads of one next to each other
+  const int unit = blockIdx.x % heads;
+  const int rows = static_cast<int>(gridDim.x) / heads - 1 - static_cast<int>(blockIdx.x) / heads;
+  w.b = unit / p.hk, w.kvh = unit % p.hk;
+  w.group = p.hq / p.hk;
+  w.per = 128 / w.group;
+  w.n = attn_kv_len(p, w.b), w.nq = attn_q_len(p, w.b);
+  w.pq = w.n - w.nq;
+  w.i00 = 2 * rows * w.per;
+  // a tile without queries, or all before the first key: last < first
+  w.min0 = max(w.pq + w.i00, 0);
+  w.max0 = w.pq + min(w.i00 + w.per, w.nq) - 1;
+  w.min1 = max(w.pq + w.i00 + w.per, 0);
+  w.max1 = w.pq + min(w.i00 + 2 * w.per, w.nq) - 1;
+  const bool on0 = w.active(0), on1 = w.active(1);
+  const int lo = on0 ? w.min0 : w.min1, hi = on1 ? w.max1 : on0 ? w.max0 : -1;
+  w.sinks = w.n_sinks = w.begin = w.slot0 = w.len_a = w.n_a = w.len_b = w.tiles = 0;
+  if (hi < 0) return w;
+  w.sinks = min(min(p.held_sinks, w.n), hi + 1);
+  w.begin = attn_ring_begin(p, w.n);
+  if (p.window > 0) w.begin = max(w.begin, lo - p.window + 1);
+  int len = max(hi + 1 - w.begin, 0);
+  if (len == 0) w.begin = 0;
+  w.slot0 = len ? attn_slot(p, w.begin) : 0;
+  if (len && w.begin == w.sinks && w.slot0 == w.sinks) {  // one run from the first key on
+    w.begin = w.slot0 = 0;
+    len += w.sinks;
+    w.sinks = 0;
+  }
+  w.len_a = min(len, p.cap - w.slot0);
+  w.len_b = len - w.len_a;
+  w.n_sinks = (w.sinks + kTileKeys - 1) / kTileKeys;
+  w.n_a = (w.len_a + kTileKeys - 1) / kTileKeys;
+  w.tiles = w.n_sinks + w.n_a + (w.len_b + kTileKeys - 1) / kTileKeys;
+  return w;
+}
+
+template <typename T, int DB>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
+                       const AttnParams p) {
+  using C = Pr<DB>;
+  constexpr int NS = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* Q = smem_raw + pad;  // [2 row tiles]; the output tiles at the end
+  uint8_t* Ks = Q + 2 * C::kTile;
+  uint8_t* Vs = Ks + NS * C::kTile;
+  uint64_t* qfull = reinterpret_cast<uint64_t*>(Vs + NS * C::kTile);  // [2]
+  uint64_t* kfull = qfull + 2;    // [NS]
+  uint64_t* kempty = kfull + NS;
+  uint64_t* vfull = kempty + NS;
+  uint64_t* vempty = vfull + NS;
+  uint64_t* sfull = vempty + NS;  // [2]
+  uint64_t* pfull = sfull + 2;    // [2]
+  uint64_t* odone = pfull + 2;    // [2]
+  uint64_t* vclean = odone + 2;   // [NS]
+  uint32_t* slot = reinterpret_cast<uint32_t*>(vclean + NS);
+  int* odd = reinterpret_cast<int*>(slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&kfull[s], 1);
+      mbar_init(&kempty[s], 1);
+      mbar_init(&vfull[s], 1);
+      mbar_init(&vempty[s], 1);
+      mbar_init(&vclean[s], 64);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&qfull[t], 1);
+      mbar_init(&sfull[t], 1);
+      mbar_init(&pfull[t], 128);
+      mbar_init(&odone[t], 1);
+    }
+    *odd = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 9) tmem_alloc(slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  griddep_launch_dependents();
+  griddep_wait();
+  const Plan w = make_plan(p);
+  const int kd = (p.d + 15) / 16;  // blocks of 16 values of a head
+  // columns: S (then P) of tile 0 and 1, O of tile 0 and 1
+  const auto s_col = [tmem](int t) { return tmem + t * 128; };
+  const auto o_col = [tmem](int t) { return tmem + 256 + t * 64 * DB; };
+
+  if (warp >= 8) {
+    if (warp == 8) {
+      if (lane == 0) {
+        const uint64_t pol = l2_evict_normal();
+        const int q_bytes = w.per * w.group * 128;
+        bool ok = true;
+        for (int j = 0; j < w.tiles && ok; ++j) {
+          const Tile k = w.tile(p, j);
+          const int s = j % NS, ph = (j / NS) & 1;
+          ok = mbar_wait_bounded(&kempty[s], ph ^ 1, p.status, kErrTimeoutProducer);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&kfull[s], C::kTile);
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+            tma_load_4d(Ks + s * C::kTile + d * 16384, &map_k, &kfull[s], d * 64, k.slot, w.kvh, w.b, pol);
+          if (j == 0) {
+            for (int t = 0; t < 2; ++t) {
+              if (!w.active(t)) continue;
+              mbar_arrive_expect_tx(&qfull[t], DB * q_bytes);
+#pragma unroll
+              for (int d = 0; d < DB; ++d)
+                tma_load_4d(Q + t * C::kTile + d * 16384, &map_q, &qfull[t], d * 64, w.kvh * w.group, w.i0(t), w.b, pol);
+            }
+          }
+          ok = mbar_wait_bounded(&vempty[s], ph ^ 1, p.status, kErrTimeoutProducer);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&vfull[s], C::kTile);
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+            tma_load_4d(Vs + s * C::kTile + d * 16384, &map_v, &vfull[s], d * 64, k.slot, w.kvh, w.b, pol);
+        }
+      }
+    } else if (warp == 9) {
+      if (elect_one()) {
+        constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+        const uint32_t id_pv = idesc_16(bf, 128, kd * 16, true);
+        int n_p[2] = {0, 0};
+        uint32_t clean = 0;  // phase of each stage's looked-over barrier
+        bool ok = true;
+        auto score = [&](int t, int j, const Tile& k) {  // S of row tile t and key tile j
+          const uint32_t id = idesc_16(bf, 128, (k.count + 15) / 16 * 16);
+          const uint32_t qa = smem_u32(Q + t * C::kTile), ka = smem_u32(Ks + (j % NS) * C::kTile);
+          for (int i = 0; i < kd; ++i) {
+            const uint32_t off = (i >> 2) * 16384 + (i & 3) * 32;
+            mma_f16_ss(s_col(t), smem_desc_sw128(qa + off), smem_desc_sw128(ka + off), id, i > 0);
+          }
+          mma_commit(&sfull[t]);
+        };
+        if (w.tiles > 0) {
+          const Tile k = w.tile(p, 0);
+          ok = mbar_wait_bounded(&kfull[0], 0, p.status, kErrTimeoutMma);
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (!w.active(t)) continue;
+            ok = mbar_wait_bounded(&qfull[t], 0, p.status, kErrTimeoutMma);
+            tc_fence_after();
+            if (ok && w.seen(p, t, k)) score(t, 0, k);
+          }
+          mma_commit(&kempty[0]);
+        }
+        for (int j = 0; j < w.tiles && ok; ++j) {
+          const Tile k = w.tile(p, j);
+          const int s = j % NS;
+          const bool more = j + 1 < w.tiles;
+          const Tile kn = w.tile(p, more ? j + 1 : j);
+          ok = mbar_wait_bounded(&vfull[s], (j / NS) & 1, p.status, kErrTimeoutMma);
+          if (ok && w.looked_over(p, k)) {
+            ok = mbar_wait_bounded(&vclean[s], clean >> s & 1, p.status, kErrTimeoutMma);
+            clean ^= 1u << s;
+          }
+          bool next_ready = false;
+          const uint32_t va = smem_u32(Vs + s * C::kTile);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok) break;
+            if (w.seen(p, t, k)) {
+              ok = mbar_wait_bounded(&pfull[t], n_p[t] & 1, p.status, kErrTimeoutMma);
+              if (!ok) break;
+              tc_fence_after();
+              const int steps = (k.count + 15) / 16;
+              for (int i = 0; i < steps; ++i)
+                mma_ts(o_col(t), s_col(t) + i * 8, value_desc(va + i * 2048), id_pv, n_p[t] > 0 || i > 0);
+              mma_commit(&odone[t]);
+              ++n_p[t];
+            }
+            if (more && w.seen(p, t, kn)) {
+              if (!next_ready) {
+                ok = mbar_wait_bounded(&kfull[(j + 1) % NS], ((j + 1) / NS) & 1, p.status, kErrTimeoutMma);
+                if (!ok) break;
+                tc_fence_after();
+                next_ready = true;
+              }
+              score(t, j + 1, kn);
+            }
+          }
+          mma_commit(&vempty[s]);
+          if (more) mma_commit(&kempty[(j + 1) % NS]);
+        }
+      }
+    } else {
+      // look over the values of tiles that some row does not see whole
+      const int tid = threadIdx.x - 320;
+      for (int j = 0; j < w.tiles; ++j) {
+        const Tile k = w.tile(p, j);
+        if (!w.looked_over(p, k)) continue;
+        const int s = j % NS;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&vfull[s], (j / NS) & 1, p.status, kErrTimeoutProducer))) break;
+        uint8_t* V = Vs + s * C::kTile;
+        const int rows = (k.count + 15) / 16 * 16;
+        bool found = false;
+#pragma unroll 4
+        for (int e = tid; e < rows * 8 * DB; e += 64) {
+          const int block = e / (rows * 8), r = e / 8 % rows;  // any order of a row's pieces will do
+          uint4* at = reinterpret_cast<uint4*>(V + block * 16384 + r * 128 + (e % 8) * 16);
+          const uint4 v = *at;
+          const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+          constexpr uint32_t x = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+          bool bad = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bad |= (q[i] & x) == x || (q[i] & (x << 16)) == (x << 16);
+          if (bad) {
+            if (r >= k.count) *at = make_uint4(0u, 0u, 0u, 0u);
+            else found = true;
+          }
+        }
+        if (found) *odd = 1;
+        fence_proxy_async_smem();
+        mbar_arrive(&vclean[s]);
+      }
+    }
+  } else {
+    const int t = warp >> 2;
+    const int r = threadIdx.x & 127;  // row of the tile = lane of tensor memory
+    const int i = w.i0(t) + r / w.group;
+    const bool valid = r < w.per * w.group && i < w.nq && w.pq + i >= 0;
+    const int pos = valid ? w.pq + i : -1;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float c = p.scale * 1.4426950408889634f;  // scores to powers of two
+    float top = -INFINITY;  // what P is relative to
+    float sum = 0.f;
+    int n = 0;
+    bool ok = true;
+    for (int j = 0; j < w.tiles && ok; ++j) {
+      const Tile k = w.tile(p, j);
+      if (!w.seen(p, t, k)) continue;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sfull[t], n & 1, p.status, kErrTimeoutEpilogue));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t raw[4][32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q * 32 < k.count) {
+          tmem_ld32_nowait(s_col(t) + lanes + q * 32, raw[q]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) raw[q][e] = 0xFF800000u;
+        }
+      }
+      tmem_wait_ld();
+      if (!w.whole(p, t, k)) {
+        const int hi = min(k.count - 1, pos - k.pos);  // columns lo .. hi, and the sinks
+        const int lo = p.window > 0 ? pos - p.window + 1 - k.pos : 0;
+        const int sk = min(p.sinks - k.pos, hi + 1);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int x = q * 32 + e;
+            if (!((x >= lo && x <= hi) || x < sk)) raw[q][e] = 0xFF800000u;
+          }
+      }
+      float m4[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        m4[q] = __uint_as_float(raw[q][0]);
+#pragma unroll
+        for (int e = 1; e < 31; e += 2)
+          m4[q] = fmaxf(m4[q], fmaxf(__uint_as_float(raw[q][e]), __uint_as_float(raw[q][e + 1])));
+        m4[q] = fmaxf(m4[q], __uint_as_float(raw[q][31]));
+      }
+      const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      const bool rise = (m - top) * c > 8.f;
+      if (__any_sync(0xFFFFFFFFu, rise)) {
+        const float up = fmaxf(m, top);
+        const float f = up == -INFINITY ? 1.f : exp2_fast((top - up) * c);
+        top = up;
+        sum *= f;
+        if (n > 0) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&odone[t], (n - 1) & 1, p.status, kErrTimeoutEpilogue));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int x = 0; x < kd * 16; x += 16) {
+            uint32_t o[16];
+            tmem_ld16_nowait(o_col(t) + lanes + x, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(o_col(t) + lanes + x, o);
+          }
+        }
+      }
+      const float base = top == -INFINITY ? 0.f : top * c;
+      const uint64_t c2 = f2(c, c), b2 = f2(-base, -base);
+      uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q * 32 >= k.count) continue;
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x = f2_of(fma2(f2(__uint_as_float(raw[q][e]), __uint_as_float(raw[q][e + 1])), c2, b2));
+          const float u = exp2_fast(x.x), v = exp2_fast(x.y);
+          acc[(e >> 1) & 1] = add2(acc[(e >> 1) & 1], f2(u, v));
+          pk[e / 2] = pack2<T>(u, v);
+        }
+        tmem_st16(s_col(t) + lanes + q * 16, pk);
+      }
+      const float2 a = f2_of(add2(acc[0], acc[1]));
+      sum += a.x + a.y;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&pfull[t]);
+      ++n;
+    }
+    if (n > 0 && ok) {
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&odone[t], (n - 1) & 1, p.status, kErrTimeoutEpilogue));
+      tc_fence_after();
+    }
+    // output: through the row tile's query tile, which no product reads any more
+    const bool some = valid && n > 0 && !(sum == 0.f);
+    const float inv = some ? 1.f / sum : 0.f;
+    uint8_t* out = Q + t * C::kTile;
+#pragma unroll 1
+    for (int x = 0; x < DB * 64; x += 32) {
+      if (x >= p.d) break;
+      uint32_t o[32];
+      if (n > 0) {
+        tmem_ld32_nowait(o_col(t) + lanes + x, o);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = some ? __uint_as_float(o[q * 8 + e]) * inv : 0.f;
+        const int pc = (x % 64) / 8 + q;
+        *reinterpret_cast<uint4*>(out + (x / 64) * 16384 + r * 128 + ((pc ^ (r & 7)) << 4)) = Vec16<T>::pack(v);
+      }
+    }
+    if (p.lse && r < w.per * w.group && i < p.tq) {
+      const int h = w.kvh * w.group + r % w.group;
+      p.lse[(static_cast<int64_t>(w.b) * p.hq + h) * p.tq + i] =
+          some ? (top * c + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    }
+    fence_proxy_async_smem();
+    named_barrier_sync(1 + t, 128);
+    if (r == 0 && w.i0(t) < p.tq) {
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+        if (d * 64 < p.d) tma_store_4d(&map_o, out + d * 16384, d * 64, w.kvh * w.group, w.i0(t), w.b);
+      bulk_commit();
+      bulk_wait_all();
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (*odd) {
+    // a key's value is no number: every row again, on its own
+    for (int r = warp; r < 2 * w.per * w.group; r += kThreads / 32) {
+      const int i = w.i00 + r / w.group;
+      if (i < p.tq) attend_row<T, 2 * DB>(p, w.b, i, w.kvh * w.group + r % w.group, lane);
+    }
+  }
+}
+
+template <typename T, int DB>
+cudaError_t launch(const AttnLaunch& L, cudaStream_t stream) {
+  auto kernel = attn_prompt_kernel<T, DB>;
+  static SmemReady ready;
+  const cudaError_t e = ready.ensure(kernel, Pr<DB>::kSmem, L.device);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(L.grid), dim3(kThreads), Pr<DB>::kSmem, stream, L.map_q, L.map_k, L.map_v, L.map_o, L.p);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prompt(const AttnLaunch& L, bool bf16, cudaStream_t stream) {
+  if (L.p.d <= 64) return bf16 ? launch<__nv_bfloat16, 1>(L, stream) : launch<__half, 1>(L, stream);
+  return bf16 ? launch<__nv_bfloat16, 2>(L, stream) : launch<__half, 2>(L, stream);
+}
+
+}  // namespace oidnx

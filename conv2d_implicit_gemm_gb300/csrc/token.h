@@ -170,6 +170,13 @@ cudaError_t launch_linear_split(const LinearTcLaunch& L, bool bf16, cudaStream_t
 cudaError_t launch_norm_vec(const NormParams& p, int precision, cudaStream_t stream);
 cudaError_t launch_norm_any(const NormParams& p, int precision, cudaStream_t stream);
 cudaError_t launch_attn_token(const AttnParams& p, bool bf16, int split, int device, cudaStream_t stream);
+struct AttnLaunch {
+  AttnParams p;
+  CUtensorMap map_q, map_k, map_v, map_o;
+  int device;
+  unsigned grid;
+};
+cudaError_t launch_attn_prompt(const AttnLaunch& L, bool bf16, cudaStream_t stream);
 cudaError_t launch_attn_any(const AttnParams& p, int precision, cudaStream_t stream);
 
 }  // namespace oidnx

@@ -2,6 +2,7 @@
 // kernel.  Each is a direct call on device pointers; nothing is kept from one
 // call for the next but the device error word.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -108,6 +109,23 @@ cudaError_t run_linear(const LinearParams& params, bool bf16, cudaStream_t strea
 }
 
 // ---------------------------------------------------------------- attention: choice of form
+// Heads of 16-bit values as [sequence][outer][inner][value] in boxes of 64
+// values x box1 x box2, 128-byte rows, swizzled.  outer and inner are tokens
+// and heads in either order.
+bool heads_map(CUtensorMap* map, bool bf16, const void* base, int d, int n1, int64_t s1, int n2, int64_t s2, int n3,
+               int64_t s3, int box1, int box2) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2),
+                              static_cast<cuuint64_t>(n3)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2,
+                                 static_cast<cuuint64_t>(s3) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2), 1}, step[4] = {1, 1, 1, 1};
+  const EncodeFn fn = encode_fn();
+  return fn && fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
   int device, sms;
   const cudaError_t e = token_device(&device, &sms, &p.status);
@@ -124,6 +142,21 @@ cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
     int split = 1;
     while (split < 8 && units * split < 2 * sms && keys / (2 * split) >= 128) split *= 2;
     return launch_attn_token(p, precision == OIDNX_PRECISION_BF16, split, device, stream);
+  }
+  bool tiles = pieces && group <= 128 && p.scale > 0.f && p.cap > 0;
+  for (int i = 0; i < 3; ++i)
+    for (const int64_t s : {p.q_s[i], p.k_s[i], p.v_s[i], p.o_s[i]}) tiles = tiles && s > 0 && s < (int64_t(1) << 38);
+  const int per = 128 / group;  // queries of a row tile
+  const int64_t grid = (static_cast<int64_t>(p.tq) + 2 * per - 1) / (2 * per) * p.b * p.hk;
+  if (tiles && grid <= INT_MAX) {
+    AttnLaunch L = {};
+    L.p = p, L.device = device, L.grid = static_cast<unsigned>(grid);
+    const bool bf16 = precision == OIDNX_PRECISION_BF16;
+    if (heads_map(&L.map_q, bf16, p.q, p.d, p.hq, p.q_s[2], p.tq, p.q_s[1], p.b, p.q_s[0], group, per) &&
+        heads_map(&L.map_o, bf16, p.o, p.d, p.hq, p.o_s[2], p.tq, p.o_s[1], p.b, p.o_s[0], group, per) &&
+        heads_map(&L.map_k, bf16, p.k, p.d, p.cap, p.k_s[1], p.hk, p.k_s[2], p.b, p.k_s[0], 128, 1) &&
+        heads_map(&L.map_v, bf16, p.v, p.d, p.cap, p.v_s[1], p.hk, p.v_s[2], p.b, p.v_s[0], 128, 1))
+      return launch_attn_prompt(L, bf16, stream);
   }
   return launch_attn_any(p, precision, stream);
 }
