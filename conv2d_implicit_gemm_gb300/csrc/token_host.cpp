@@ -219,16 +219,17 @@ oidnx_status oidnx_qk_norm_rope(const void* q, long long q_st, long long q_sh, v
   const long long it[3] = {q_st, k_st, v_st}, ih[3] = {q_sh, k_sh, v_sh};
   const long long ot[3] = {qo_st, ko_st, vo_st}, oh[3] = {qo_sh, ko_sh, vo_sh};
   p.heads[0] = hq, p.heads[1] = hk, p.heads[2] = v ? hk : 0;
-  // 16-byte form: every head starts on 16 bytes and rotation pairs are whole
-  // chunks apart (half-split) or do not straddle one (adjacent pairs)
-  const int vec = static_cast<int>(16 / size);
-  bool fast = d % vec == 0 && d / vec <= 64 && (interleaved ? rot % vec == 0 : rot / 2 % vec == 0) &&
-              aligned(q_weight, 16) && aligned(k_weight, 16) && aligned(cos_table, 16) && aligned(sin_table, 16);
+  // Vector form: loads of four values (eight where pairs are adjacent), the
+  // rotated part and the rest both in whole groups of four pairs.
+  const int vec = static_cast<int>(interleaved ? 16 / size < 8 ? 4 : 8 : 4);
+  const size_t align = vec * size < 16 ? vec * size : 16;
+  bool fast = d % 8 == 0 && d <= 256 && rot % 8 == 0 && aligned(q_weight, align) && aligned(k_weight, align) &&
+              aligned(cos_table, 16) && aligned(sin_table, 16);
   for (int i = 0; i < 3; ++i) {
     p.in[i] = in[i], p.out[i] = out[i];
     p.in_t[i] = it[i], p.in_h[i] = ih[i], p.out_t[i] = ot[i], p.out_h[i] = oh[i];
     if (p.heads[i])
-      fast = fast && aligned(in[i], 16) && aligned(out[i], 16) && it[i] % vec == 0 && ih[i] % vec == 0 &&
+      fast = fast && aligned(in[i], align) && aligned(out[i], align) && it[i] % vec == 0 && ih[i] % vec == 0 &&
              ot[i] % vec == 0 && oh[i] % vec == 0;
   }
   p.weight[0] = q_weight, p.weight[1] = k_weight;
