@@ -19,27 +19,30 @@ namespace {
 constexpr int kThreads = 256;  // warp 0 loads, warp 1 multiplies, warps 4-7 read the accumulator; all join the sums
 constexpr int kGatherThreads = 256;
 
-template <int BN> struct Split {
+template <int BN, bool GATHER> struct Split {
   static constexpr int kA = 128 * 128;
   static constexpr int kB = BN * 128;
   static constexpr int kStage = kA + kB;
-  // two CTAs per SM
-  static constexpr int kStages = 110 * 1024 / kStage;
-  static constexpr int kSmem = kStages * kStage + 2048;
+  // through TMA: two CTAs per SM; gathered: one, most of it blocks on their way as they lie in memory
+  static constexpr int kStages = GATHER ? (BN == 128 ? 2 : 3) : 110 * 1024 / kStage;
+  static constexpr int kRawStages = GATHER ? (BN == 128 ? 4 : 5) : 0;
+  static constexpr int kRaw = kRawStages * (128 + BN) * 144;
+  static constexpr int kSmem = kStages * kStage + kRaw + 2048;
   static constexpr int kCols = BN < 32 ? 32 : BN;
-  static_assert(kStages * kStage >= 128 * BN * 4, "the parts reuse the stages");
+  static_assert(kStages * kStage + kRaw >= 128 * BN * 4, "the parts reuse the stages");
 };
 
 template <typename T, int BN, bool GATHER>
 __global__ void __launch_bounds__(kThreads + (GATHER ? kGatherThreads : 0), GATHER ? 1 : 2)
     linear_split_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                         const LinearParams p, const int split) {
-  using S = Split<BN>;
+  using S = Split<BN, GATHER>;
   constexpr int NS = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;
-  uint64_t* full = reinterpret_cast<uint64_t*>(stages + NS * S::kStage);
+  uint8_t* raw = stages + NS * S::kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(raw + S::kRaw);
   uint64_t* empty = full + NS;
   uint64_t* done = empty + NS;
   uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -114,19 +117,37 @@ __global__ void __launch_bounds__(kThreads + (GATHER ? kGatherThreads : 0), GATH
       }
     }
   } else if (GATHER && warp >= 8) {
-    const int tid = threadIdx.x - kThreads;
+    using G = Gather<128, BN, kGatherThreads>;
+    constexpr int R = S::kRawStages > 1 ? S::kRawStages : 2;
+    G g;
+    g.a = G::side(p.w, p.ldw, p.n, p.k);
+    g.b = G::side(p.x, p.ldx, p.m, p.k);
+    g.a.r0 = j0, g.b.r0 = i0;
+    g.k = p.k, g.tid = threadIdx.x - kThreads;
+#pragma unroll
+    for (int q = 0; q < R - 1; ++q) {
+      if (first + q < last) g.issue(raw + q * G::kStage, (first + q) * kKB);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
     uint32_t s = 0, ph = 0;
+    int rs = 0;
+    bool ok = true;  // one thread's: all walk on together, as they share barriers
     for (int k = first; k < last; ++k) {
-      if (!mbar_wait_bounded(&empty[s], ph ^ 1, p.status, kErrTimeoutProducer)) break;
-      uint8_t* A = stages + s * S::kStage;
-      gather_tile<128, kGatherThreads>(A, p.w, p.ldw, p.n, p.k, j0, k * kKB, tid);
-      if constexpr (BN * 8 >= kGatherThreads) {
-        gather_tile<BN, kGatherThreads>(A + S::kA, p.x, p.ldx, p.m, p.k, i0, k * kKB, tid);
-      } else {
-        if (tid < BN * 8) gather_tile<BN, BN * 8>(A + S::kA, p.x, p.ldx, p.m, p.k, i0, k * kKB, tid);
+      asm volatile("cp.async.wait_group %0;" ::"n"(R - 2) : "memory");
+      // this block has landed for every thread, and every thread is done with
+      // the one whose place the next copies take
+      named_barrier_sync(3, kGatherThreads);
+      const int ahead = k + R - 1;
+      if (ahead < last) g.issue(raw + (rs == 0 ? R - 1 : rs - 1) * G::kStage, ahead * kKB);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (ok) ok = mbar_wait_bounded(&empty[s], ph ^ 1, p.status, kErrTimeoutProducer);
+      if (ok) {
+        uint8_t* A = stages + s * S::kStage;
+        g.place(raw + rs * G::kStage, A, A + S::kA, k * kKB);
+        fence_proxy_async_smem();
+        mbar_arrive(&full[s]);
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&full[s]);
+      if (++rs == R) rs = 0;
       if (++s == NS) s = 0, ph ^= 1;
     }
   }
@@ -173,7 +194,7 @@ __global__ void __launch_bounds__(kThreads + (GATHER ? kGatherThreads : 0), GATH
 
 template <typename T, int BN, bool GATHER>
 cudaError_t launch(const LinearTcLaunch& L, cudaStream_t stream) {
-  using S = Split<BN>;
+  using S = Split<BN, GATHER>;
   auto kernel = linear_split_kernel<T, BN, GATHER>;
   static SmemReady ready;
   const cudaError_t e = ready.ensure(kernel, S::kSmem, L.device);

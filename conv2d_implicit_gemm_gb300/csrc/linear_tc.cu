@@ -37,14 +37,15 @@ constexpr int kLinThreadsGather = kLinThreads + kGatherWarps * 32;
 constexpr int kStageOut = 4096;  // bytes of staging per epilogue warp
 constexpr int kRowGroup = 8;     // row blocks walked together
 
-template <int CG, int BN> struct Shape {
+template <int CG, int BN, bool GATHER> struct Shape {
   static constexpr int kA = 128 * 128;              // bytes of a CTA's x block
   static constexpr int kB = BN / CG * 128;          // bytes of its w block
   static constexpr int kStage = kA + kB;
-  static constexpr int kStages = (227 * 1024 - 2048 - kEpiWarps * kStageOut) / kStage < 8
-                                     ? (227 * 1024 - 2048 - kEpiWarps * kStageOut) / kStage
-                                     : 8;
-  static constexpr int kSmem = kStages * kStage + kEpiWarps * kStageOut + 2048;
+  static constexpr int kRawStages = GATHER ? 3 : 0;  // blocks on their way as they lie in memory
+  static constexpr int kRaw = kRawStages * (128 + BN) * 144;
+  static constexpr int kRoom = 227 * 1024 - 2048 - kEpiWarps * kStageOut - kRaw;
+  static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
+  static constexpr int kSmem = kStages * kStage + kEpiWarps * kStageOut + kRaw + 2048;
   static constexpr int kCols = 2 * BN < 32 ? 32 : 2 * BN;
 };
 
@@ -184,13 +185,14 @@ __global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                      const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_y,
                      const TcArgs a) {
-  using S = Shape<CG, BN>;
+  using S = Shape<CG, BN, GATHER>;
   constexpr int NS = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;  // every tile starts on 1024 bytes
   uint8_t* staging = stages + NS * S::kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStageOut);
+  uint8_t* raw = staging + kEpiWarps * kStageOut;
+  uint64_t* full = reinterpret_cast<uint64_t*>(raw + S::kRaw);
   uint64_t* empty = full + NS;
   uint64_t* tfull = empty + NS;    // [2]
   uint64_t* tempty = tfull + 2;    // [2]
@@ -318,22 +320,44 @@ __global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
     }
     if (lane == 0) bulk_wait_all();
   } else if (GATHER && warp >= kFirstEpi + kEpiWarps) {
-    const int tid = threadIdx.x - kLinThreads;
+    using G = Gather<128, BN, kGatherWarps * 32>;
+    constexpr int R = S::kRawStages > 1 ? S::kRawStages : 2;
+    G g;
+    g.a = G::side(p.x, p.ldx, p.m, p.k);
+    g.b = G::side(p.w, p.ldw, p.n, p.k);
+    g.k = p.k, g.tid = threadIdx.x - kLinThreads;
     uint32_t s = 0, ph = 0;
-    bool ok = true;
-    for (int t = walker; t < tiles && ok; t += walkers) {
+    bool ok = true;  // one thread's: all walk on together, as they share barriers
+    for (int t = walker; t < tiles; t += walkers) {
       int tm, tn;
       tile_of(a, t, &tm, &tn);
+      g.a.r0 = tm * 128, g.b.r0 = tn * BN;
+#pragma unroll
+      for (int k = 0; k < R - 1; ++k) {
+        if (k < kb) g.issue(raw + k * G::kStage, k * kKB);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+      int rs = 0;
       for (int k = 0; k < kb; ++k) {
-        ok = mbar_wait_bounded(&empty[s], ph ^ 1, p.status, kErrTimeoutProducer);
-        if (!ok) break;
-        uint8_t* A = stages + s * S::kStage;
-        gather_tile<128, kGatherWarps * 32>(A, p.x, p.ldx, p.m, p.k, tm * 128, k * kKB, tid);
-        gather_tile<BN, kGatherWarps * 32>(A + S::kA, p.w, p.ldw, p.n, p.k, tn * BN, k * kKB, tid);
-        fence_proxy_async_smem();
-        mbar_arrive(&full[s]);
+        asm volatile("cp.async.wait_group %0;" ::"n"(R - 2) : "memory");
+        // this block has landed for every thread, and every thread is done with
+        // the one whose place the next copies take
+        named_barrier_sync(3, kGatherWarps * 32);
+        const int ahead = k + R - 1;
+        if (ahead < kb) g.issue(raw + (rs == 0 ? R - 1 : rs - 1) * G::kStage, ahead * kKB);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (ok) ok = mbar_wait_bounded(&empty[s], ph ^ 1, p.status, kErrTimeoutProducer);
+        if (ok) {
+          uint8_t* A = stages + s * S::kStage;
+          g.place(raw + rs * G::kStage, A, A + S::kA, k * kKB);
+          fence_proxy_async_smem();
+          mbar_arrive(&full[s]);
+        }
+        if (++rs == R) rs = 0;
         if (++s == NS) s = 0, ph ^= 1;
       }
+      // the next tile's first copies must not overtake the last block's reads
+      named_barrier_sync(3, kGatherWarps * 32);
     }
   }
 
@@ -350,7 +374,7 @@ __global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
 
 template <typename T, int CG, int BN, bool GATHER>
 cudaError_t launch(const LinearTcLaunch& L, cudaStream_t stream) {
-  using S = Shape<CG, BN>;
+  using S = Shape<CG, BN, GATHER>;
   TcArgs a = {L.p, (L.p.m + 128 * CG - 1) / (128 * CG), (L.p.n + BN - 1) / BN, L.tma_out};
   auto kernel = linear_tc_kernel<T, CG, BN, GATHER>;
   static SmemReady ready;

@@ -124,6 +124,7 @@ struct NormParams {
   const int* slots;  // or null: row t
   int64_t cache_rows;
   int t, d, rot, interleaved;
+  int wide;  // vector form: 16-byte loads of 16-bit values (else 8-byte)
 };
 
 // ---------------------------------------------------------------- attention
@@ -167,7 +168,7 @@ __device__ __forceinline__ int attn_slot(const AttnParams& p, int pos) {
 
 cudaError_t launch_linear_tc(const LinearTcLaunch& L, bool bf16, cudaStream_t stream);
 cudaError_t launch_linear_split(const LinearTcLaunch& L, bool bf16, cudaStream_t stream);
-cudaError_t launch_norm_vec(const NormParams& p, int precision, cudaStream_t stream);
+cudaError_t launch_norm_vec(const NormParams& p, int precision, int sms, cudaStream_t stream);
 cudaError_t launch_norm_any(const NormParams& p, int precision, cudaStream_t stream);
 cudaError_t launch_attn_token(const AttnParams& p, bool bf16, int split, int device, cudaStream_t stream);
 struct AttnLaunch {

@@ -219,25 +219,34 @@ oidnx_status oidnx_qk_norm_rope(const void* q, long long q_st, long long q_sh, v
   const long long it[3] = {q_st, k_st, v_st}, ih[3] = {q_sh, k_sh, v_sh};
   const long long ot[3] = {qo_st, ko_st, vo_st}, oh[3] = {qo_sh, ko_sh, vo_sh};
   p.heads[0] = hq, p.heads[1] = hk, p.heads[2] = v ? hk : 0;
-  // Vector form: loads of four values (eight where pairs are adjacent), the
-  // rotated part and the rest both in whole groups of four pairs.
-  const int vec = static_cast<int>(interleaved ? 16 / size < 8 ? 4 : 8 : 4);
-  const size_t align = vec * size < 16 ? vec * size : 16;
-  bool fast = d % 8 == 0 && d <= 256 && rot % 8 == 0 && aligned(q_weight, align) && aligned(k_weight, align) &&
-              aligned(cos_table, 16) && aligned(sin_table, 16);
+  // Vector forms: heads in whole groups of four rotation pairs (eight: wide),
+  // the rotated part and the rest alike, everything aligned to four values
+  // (eight).  Values of 32 bits: four pairs and 16 bytes.
+  const auto fits = [&](int pairs) {
+    const size_t align = pairs * size;
+    bool ok = d % (2 * pairs) == 0 && d / (2 * pairs) <= 32 && rot % (2 * pairs) == 0 && aligned(q_weight, align) &&
+              aligned(k_weight, align) && aligned(cos_table, 16) && aligned(sin_table, 16);
+    for (int i = 0; i < 3; ++i)
+      if (p.heads[i])
+        ok = ok && aligned(in[i], align) && aligned(out[i], align) && it[i] % pairs == 0 && ih[i] % pairs == 0 &&
+             ot[i] % pairs == 0 && oh[i] % pairs == 0;
+    return ok;
+  };
   for (int i = 0; i < 3; ++i) {
     p.in[i] = in[i], p.out[i] = out[i];
     p.in_t[i] = it[i], p.in_h[i] = ih[i], p.out_t[i] = ot[i], p.out_h[i] = oh[i];
-    if (p.heads[i])
-      fast = fast && aligned(in[i], align) && aligned(out[i], align) && it[i] % vec == 0 && ih[i] % vec == 0 &&
-             ot[i] % vec == 0 && oh[i] % vec == 0;
   }
+  p.wide = size == 2 && fits(8);
+  const bool fast = p.wide || fits(4);
   p.weight[0] = q_weight, p.weight[1] = k_weight;
   p.eps = eps, p.cos_t = cos_table, p.sin_t = sin_table, p.table_rows = table_rows;
   p.positions = positions, p.slots = slots, p.cache_rows = cache_rows;
   p.t = t, p.d = d, p.rot = rot, p.interleaved = interleaved != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return finish(fast ? launch_norm_vec(p, precision, s) : launch_norm_any(p, precision, s), "qk_norm_rope");
+  int device, sms, *status;
+  cudaError_t e = token_device(&device, &sms, &status);
+  if (e == cudaSuccess) e = fast ? launch_norm_vec(p, precision, sms, s) : launch_norm_any(p, precision, s);
+  return finish(e, "qk_norm_rope");
 }
 
 oidnx_status oidnx_window_attention(const void* q, long long q_sb, long long q_st, long long q_sh, const void* k,
