@@ -16,16 +16,20 @@
 namespace oidnx {
 namespace {
 
-constexpr int kThreads = 256;  // warp 0 loads, warp 1 multiplies, warps 4-7 read the accumulator; all join the sums
-constexpr int kGatherThreads = 256;
+// Warp 0 loads, warp 1 multiplies, warps 4-7 read the accumulator, all join the
+// sums; gathered operands: warps 2, 3, 12 and 13 copy, warps 4-11 shift.
+constexpr int kThreads = 256;
+constexpr int kThreadsGather = 448;
 
 template <int BN, bool GATHER> struct Split {
   static constexpr int kA = 128 * 128;
   static constexpr int kB = BN * 128;
   static constexpr int kStage = kA + kB;
-  // through TMA: two CTAs per SM; gathered: one, most of it blocks on their way as they lie in memory
-  static constexpr int kStages = GATHER ? (BN == 128 ? 2 : 3) : 110 * 1024 / kStage;
-  static constexpr int kRawStages = GATHER ? (BN == 128 ? 4 : 5) : 0;
+  // two CTAs per SM, but for wide gathered tiles; most of a gathering CTA's
+  // room holds blocks on their way as they lie in memory
+  static constexpr int kCtas = GATHER && BN > 32 ? 1 : 2;
+  static constexpr int kStages = GATHER ? (BN == 64 ? 3 : 2) : 110 * 1024 / kStage;
+  static constexpr int kRawStages = GATHER ? (BN == 64 ? 5 : BN == 128 ? 4 : 3) : 0;
   static constexpr int kRaw = kRawStages * (128 + BN) * 144;
   static constexpr int kSmem = kStages * kStage + kRaw + 2048;
   static constexpr int kCols = BN < 32 ? 32 : BN;
@@ -33,7 +37,7 @@ template <int BN, bool GATHER> struct Split {
 };
 
 template <typename T, int BN, bool GATHER>
-__global__ void __launch_bounds__(kThreads + (GATHER ? kGatherThreads : 0), GATHER ? 1 : 2)
+__global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, Split<BN, GATHER>::kCtas)
     linear_split_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                         const LinearParams p, const int split) {
   using S = Split<BN, GATHER>;
@@ -45,7 +49,9 @@ __global__ void __launch_bounds__(kThreads + (GATHER ? kGatherThreads : 0), GATH
   uint64_t* full = reinterpret_cast<uint64_t*>(raw + S::kRaw);
   uint64_t* empty = full + NS;
   uint64_t* done = empty + NS;
-  uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* rawfull = done + 1;  // [RS]
+  uint64_t* rawempty = rawfull + S::kRawStages;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(rawempty + S::kRawStages);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int j0 = blockIdx.x / split * 128, i0 = blockIdx.y * BN;
@@ -55,10 +61,14 @@ __global__ void __launch_bounds__(kThreads + (GATHER ? kGatherThreads : 0), GATH
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], GATHER ? kGatherThreads : 1);
+      mbar_init(&full[s], GATHER ? kPlaceThreads / 32 : 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
+    for (int r = 0; r < S::kRawStages; ++r) {
+      mbar_init(&rawfull[r], 2 * kCopyThreads);
+      mbar_init(&rawempty[r], kPlaceThreads / 32);
+    }
     fence_mbarrier_init();
   }
   if (warp == 1) tmem_alloc(slot, S::kCols);
@@ -99,11 +109,42 @@ __global__ void __launch_bounds__(kThreads + (GATHER ? kGatherThreads : 0), GATH
       }
       mma_commit(done);
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp < 4 || warp >= 12) {
+    if constexpr (GATHER) {
+      Gather<128, BN> g;
+      g.matrices(p.w, p.ldw, p.n, p.x, p.ldx, p.m, p.k);
+      g.a.r0 = j0, g.b.r0 = i0;
+      int r = 0, ph = 0;
+      for (int k = first; k < last; ++k) {
+        if (!mbar_wait_bounded(&rawempty[r], ph ^ 1, p.status, kErrTimeoutProducer)) break;
+        g.copy_block(raw + r * g.kStage, &rawfull[r], k * kKB, warp < 4 ? threadIdx.x - 64 : threadIdx.x - 384 + 64);
+        if (++r == S::kRawStages) r = 0, ph ^= 1;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  } else {
+    if constexpr (GATHER) {
+      Gather<128, BN> g;
+      g.matrices(p.w, p.ldw, p.n, p.x, p.ldx, p.m, p.k);
+      g.a.r0 = j0, g.b.r0 = i0;
+      uint32_t s = 0, ph = 0, rs = 0, rph = 0;
+      for (int k = first; k < last; ++k) {
+        const bool ok = mbar_wait_bounded(&rawfull[rs], rph, p.status, kErrTimeoutProducer) &&
+                        mbar_wait_bounded(&empty[s], ph ^ 1, p.status, kErrTimeoutProducer);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        uint8_t* A = stages + s * S::kStage;
+        g.place(raw + rs * g.kStage, A, A + S::kA, p.k - k * kKB, threadIdx.x - 128);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]), mbar_arrive(&rawempty[rs]);
+        if (++s == NS) s = 0, ph ^= 1;
+        if (++rs == S::kRawStages) rs = 0, rph ^= 1;
+      }
+    }
     const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(done, 0, p.status, kErrTimeoutEpilogue));
     tc_fence_after();
     const int quarter = warp & 3;
-    if (ok) {
+    if (ok && warp < 8) {
 #pragma unroll 1
       for (int c = 0; c < BN; c += 16) {
         if (i0 + c >= p.m) break;
@@ -116,40 +157,6 @@ __global__ void __launch_bounds__(kThreads + (GATHER ? kGatherThreads : 0), GATH
           sums[(c + i) * 128 + quarter * 32 + lane] = last > first ? __uint_as_float(raw[i]) : 0.f;
       }
     }
-  } else if (GATHER && warp >= 8) {
-    using G = Gather<128, BN, kGatherThreads>;
-    constexpr int R = S::kRawStages > 1 ? S::kRawStages : 2;
-    G g;
-    g.a = G::side(p.w, p.ldw, p.n, p.k);
-    g.b = G::side(p.x, p.ldx, p.m, p.k);
-    g.a.r0 = j0, g.b.r0 = i0;
-    g.k = p.k, g.tid = threadIdx.x - kThreads;
-#pragma unroll
-    for (int q = 0; q < R - 1; ++q) {
-      if (first + q < last) g.issue(raw + q * G::kStage, (first + q) * kKB);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    uint32_t s = 0, ph = 0;
-    int rs = 0;
-    bool ok = true;  // one thread's: all walk on together, as they share barriers
-    for (int k = first; k < last; ++k) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(R - 2) : "memory");
-      // this block has landed for every thread, and every thread is done with
-      // the one whose place the next copies take
-      named_barrier_sync(3, kGatherThreads);
-      const int ahead = k + R - 1;
-      if (ahead < last) g.issue(raw + (rs == 0 ? R - 1 : rs - 1) * G::kStage, ahead * kKB);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (ok) ok = mbar_wait_bounded(&empty[s], ph ^ 1, p.status, kErrTimeoutProducer);
-      if (ok) {
-        uint8_t* A = stages + s * S::kStage;
-        g.place(raw + rs * G::kStage, A, A + S::kA, k * kKB);
-        fence_proxy_async_smem();
-        mbar_arrive(&full[s]);
-      }
-      if (++rs == R) rs = 0;
-      if (++s == NS) s = 0, ph ^= 1;
-    }
   }
 
   __syncwarp();
@@ -161,30 +168,62 @@ __global__ void __launch_bounds__(kThreads + (GATHER ? kGatherThreads : 0), GATH
     tmem_dealloc(tmem, S::kCols);
   }
 
-  // this CTA's rows of the tile, for all its tokens
+  // This CTA's rows of the tile, for all its tokens: four rows a thread, the
+  // loads of two such pieces before the first store (y may be the residual).
   const int rows = 128 / split, r0 = part * rows;
   const int tokens = min(BN, p.m - i0);
-  for (int e = threadIdx.x; e < rows * tokens; e += blockDim.x) {
-    const int i = e / rows, r = r0 + e % rows;
-    const int j = j0 + r;
-    if (j >= p.n) continue;
-    float z;
-    if (split == 1) {
-      z = sums[i * 128 + r];
-    } else {
-      float v[8];
+  const int items = rows / 4 * tokens, threads = blockDim.x;
+  uint32_t at[8];
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-        v[s] = s < split ? ld_cluster_f32(map_to_rank(sums + i * 128 + r, s)) : 0.f;
-      z = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+  for (int s = 0; s < 8; ++s) at[s] = split > 1 && s < split ? map_to_rank(sums, s) : smem_u32(sums);
+  for (int e0 = threadIdx.x; e0 < items; e0 += 2 * threads) {
+    float4 z[2];
+    float res[2][4], bias[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int e = e0 + h * threads;
+      if (e >= items) break;
+      const int i = e / (rows / 4), r = r0 + e % (rows / 4) * 4, j = j0 + r;
+      const uint32_t off = (i * 128 + r) * 4;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t row = i0 + i;
+        bias[h][q] = p.bias && j + q < p.n ? to_f32<T>(static_cast<const T*>(p.bias)[j + q]) : 0.f;
+        res[h][q] =
+            p.residual && j + q < p.n ? to_f32<T>(static_cast<const T*>(p.residual)[row * p.ldr + j + q]) : 0.f;
+      }
+      if (split == 1) {
+        z[h] = *reinterpret_cast<const float4*>(sums + i * 128 + r);
+      } else {
+        float4 v[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) v[s] = s < split ? ld_cluster_f4(at[s] + off) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 4; w > 0; w >>= 1)
+#pragma unroll
+          for (int s = 0; s < w; ++s)
+            v[s].x += v[s + w].x, v[s].y += v[s + w].y, v[s].z += v[s + w].z, v[s].w += v[s + w].w;
+        z[h] = v[0];
+      }
     }
-    if (p.bias) z += to_f32<T>(static_cast<const T*>(p.bias)[j]);
-    float one[1] = {z};
-    activate_all(one, p.act);
-    z = one[0];
-    const int64_t row = i0 + i;
-    if (p.residual) z += to_f32<T>(static_cast<const T*>(p.residual)[row * p.ldr + j]);
-    static_cast<T*>(p.y)[row * p.ldy + j] = from_f32<T>(z);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int e = e0 + h * threads;
+      if (e >= items) break;
+      const int i = e / (rows / 4), j = j0 + r0 + e % (rows / 4) * 4;
+      float f[4] = {z[h].x + bias[h][0], z[h].y + bias[h][1], z[h].z + bias[h][2], z[h].w + bias[h][3]};
+      activate_all(f, p.act);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f[q] += res[h][q];
+      T* y = static_cast<T*>(p.y) + static_cast<int64_t>(i0 + i) * p.ldy + j;
+      if (j + 4 <= p.n && (reinterpret_cast<uintptr_t>(y) & 7) == 0) {
+        *reinterpret_cast<uint2*>(y) = make_uint2(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]));
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (j + q < p.n) y[q] = from_f32<T>(f[q]);
+      }
+    }
   }
   if (split > 1) {
     __syncwarp();
@@ -201,7 +240,7 @@ cudaError_t launch(const LinearTcLaunch& L, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((L.p.n + 127) / 128 * L.split, (L.p.m + BN - 1) / BN);
-  cfg.blockDim = dim3(kThreads + (GATHER ? kGatherThreads : 0));
+  cfg.blockDim = dim3(GATHER ? kThreadsGather : kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute at[2];

@@ -7,8 +7,8 @@
 //    products.  Persistent CTAs walk the tiles in groups of 8 row blocks, so
 //    that the tiles in flight share their operands in L2.
 //  * K in blocks of 64 values: one 128-byte swizzled TMA box per operand and
-//    block.  Matrices whose rows do not start on 16 bytes are gathered by
-//    eight more warps into the same layout.
+//    block.  Matrices whose rows do not start on 16 bytes are gathered into the
+//    same layout by four warps that copy and the epilogue's, which shift.
 //  * Epilogue: eight warps, each 32 rows x half the columns, through 32 x 64
 //    tiles of 16-bit values that TMA stores (and, for the residual, loads
 //    first); outputs that TMA cannot store go through 32 x 32 fp32 tiles and
@@ -30,10 +30,9 @@ namespace oidnx {
 namespace {
 
 constexpr int kEpiWarps = 8;
-constexpr int kGatherWarps = 8;
-constexpr int kFirstEpi = 4;  // warp 0 loads, warp 1 multiplies, 2 and 3 rest
+constexpr int kFirstEpi = 4;  // warp 0 loads, warp 1 multiplies; gathered operands: 2, 3 and two more copy
 constexpr int kLinThreads = (kFirstEpi + kEpiWarps) * 32;
-constexpr int kLinThreadsGather = kLinThreads + kGatherWarps * 32;
+constexpr int kLinThreadsGather = kLinThreads + 64;
 constexpr int kStageOut = 4096;  // bytes of staging per epilogue warp
 constexpr int kRowGroup = 8;     // row blocks walked together
 
@@ -84,7 +83,19 @@ __device__ __forceinline__ void add_bias(const LinearParams& p, int c0, float (&
   }
 }
 
-// Columns [c0, c0 + COLS) of 32 rows from r0 on, accumulators at `tmem` (lane
+// One lane: once the store before has left the staging tile, the residual's
+// tile into it.
+template <int W>
+__device__ __forceinline__ void fetch_residual(const LinearParams& p, const CUtensorMap* map_r, uint8_t* stage,
+                                               uint64_t* bar, int r0, int c0) {
+  bulk_wait_read<0>();
+  if (!p.residual) return;
+  mbar_arrive_expect_tx(bar, 32 * W * 2);
+  tma_load_2d(stage, map_r, bar, c0, r0, l2_evict_first());
+}
+
+// Columns [c0, c0 + COLS) of 32 rows from r0 on (the first tile's residual
+// fetched by the caller), accumulators at `tmem` (lane
 // = row), through the warp's staging tile.  `bar`/`phase`: residual loads.
 template <typename T, int COLS>
 __device__ __forceinline__ bool epilogue_tma(const TcArgs& a, const CUtensorMap* map_y, const CUtensorMap* map_r,
@@ -95,14 +106,10 @@ __device__ __forceinline__ bool epilogue_tma(const TcArgs& a, const CUtensorMap*
 #pragma unroll 1
   for (int c = 0; c < COLS; c += W) {
     if (c0 + c >= p.n) break;
-    if (lane == 0) {
-      bulk_wait_read<0>();  // the store before has left the tile
-      if (p.residual) {
-        mbar_arrive_expect_tx(bar, 32 * W * 2);
-        tma_load_2d(stage, map_r, bar, c0 + c, r0, l2_evict_first());
-      }
+    if (c > 0) {
+      if (lane == 0) fetch_residual<W>(p, map_r, stage, bar, r0, c0 + c);
+      __syncwarp();
     }
-    __syncwarp();
     if (p.residual) {
       const bool landed = mbar_wait_bounded(bar, *phase, p.status, kErrTimeoutEpilogue);
       *phase ^= 1;
@@ -169,12 +176,16 @@ __device__ __forceinline__ void epilogue_any(const TcArgs& a, uint32_t tmem, int
     if (col < p.n) {
       T* y = static_cast<T*>(p.y) + r0 * p.ldy + col;
       const T* res = static_cast<const T*>(p.residual) + r0 * p.ldr + col;
-#pragma unroll 8
-      for (int r = 0; r < rows; ++r) {
-        float z = tile[r * 32 + (lane ^ r)];
-        if (p.residual) z += to_f32<T>(res[r * p.ldr]);
-        y[r * p.ldy] = from_f32<T>(z);
+      // all loads before the first store: y may be the residual, so the compiler
+      // keeps a load behind every earlier store
+      T z[32];
+      if (p.residual) {
+#pragma unroll
+        for (int r = 0; r < 32; ++r) z[r] = r < rows ? res[r * p.ldr] : T(0.f);
       }
+#pragma unroll
+      for (int r = 0; r < 32; ++r)
+        if (r < rows) y[r * p.ldy] = from_f32<T>(tile[r * 32 + (lane ^ r)] + (p.residual ? to_f32<T>(z[r]) : 0.f));
     }
     __syncwarp();
   }
@@ -197,7 +208,9 @@ __global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
   uint64_t* tfull = empty + NS;    // [2]
   uint64_t* tempty = tfull + 2;    // [2]
   uint64_t* rbar = tempty + 2;     // [kEpiWarps] residual tiles
-  uint32_t* slot = reinterpret_cast<uint32_t*>(rbar + kEpiWarps);
+  uint64_t* rawfull = rbar + kEpiWarps;       // [RS]
+  uint64_t* rawempty = rawfull + S::kRawStages;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(rawempty + S::kRawStages);
   const LinearParams& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
@@ -207,7 +220,7 @@ __global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], GATHER ? kGatherWarps * 32 : 1);
+      mbar_init(&full[s], GATHER ? kEpiWarps : 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -215,6 +228,10 @@ __global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
       mbar_init(&tempty[b], CG * kEpiWarps);
     }
     for (int w = 0; w < kEpiWarps; ++w) mbar_init(&rbar[w], 1);
+    for (int r = 0; r < S::kRawStages; ++r) {
+      mbar_init(&rawfull[r], 2 * kCopyThreads);
+      mbar_init(&rawempty[r], kEpiWarps);
+    }
     fence_mbarrier_init();
   }
   if (warp == 1) {
@@ -289,20 +306,63 @@ __global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
         else mma_commit(&tfull[b]);
       }
     }
-  } else if (warp >= kFirstEpi && warp < kFirstEpi + kEpiWarps) {
+  } else if (warp < kFirstEpi || warp >= kFirstEpi + kEpiWarps) {
+    if constexpr (GATHER) {
+      const int tid = warp < kFirstEpi ? threadIdx.x - 64 : threadIdx.x - kLinThreads + 64;
+      Gather<128, BN> g;
+      g.matrices(p.x, p.ldx, p.m, p.w, p.ldw, p.n, p.k);
+      int r = 0, ph = 0;
+      bool ok = true;
+      for (int t = walker; t < tiles && ok; t += walkers) {
+        int tm, tn;
+        tile_of(a, t, &tm, &tn);
+        g.a.r0 = tm * 128, g.b.r0 = tn * BN;
+        for (int k = 0; k < kb; ++k) {
+          ok = mbar_wait_bounded(&rawempty[r], ph ^ 1, p.status, kErrTimeoutProducer);
+          if (!ok) break;
+          g.copy_block(raw + r * g.kStage, &rawfull[r], k * kKB, tid);
+          if (++r == S::kRawStages) r = 0, ph ^= 1;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  } else {
     const int e = warp - kFirstEpi;
     const int quarter = warp & 3, half = e >> 2;  // the TMEM lanes a warp may read; its columns
     uint8_t* stage = staging + e * kStageOut;
     uint32_t rphase = 0;
     int n = 0;
+    [[maybe_unused]] uint32_t s = 0, ph = 0, rs = 0, rph = 0;  // gathered operands
     for (int t = walker; t < tiles; t += walkers, ++n) {
       const int b = n & 1;
       int tm, tn;
       tile_of(a, t, &tm, &tn);
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[b], (n >> 1) & 1, p.status, kErrTimeoutEpilogue))) break;
-      tc_fence_after();
+      if constexpr (GATHER) {
+        Gather<128, BN> g;
+        g.matrices(p.x, p.ldx, p.m, p.w, p.ldw, p.n, p.k);
+        g.a.r0 = tm * 128, g.b.r0 = tn * BN;
+        bool ok = true;
+        for (int k = 0; k < kb; ++k) {
+          ok = mbar_wait_bounded(&rawfull[rs], rph, p.status, kErrTimeoutProducer) &&
+               mbar_wait_bounded(&empty[s], ph ^ 1, p.status, kErrTimeoutProducer);
+          if (!__all_sync(0xFFFFFFFFu, ok)) break;
+          uint8_t* A = stages + s * S::kStage;
+          g.place(raw + rs * g.kStage, A, A + S::kA, p.k - k * kKB, threadIdx.x - kFirstEpi * 32);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]), mbar_arrive(&rawempty[rs]);
+          if (++s == NS) s = 0, ph ^= 1;
+          if (++rs == S::kRawStages) rs = 0, rph ^= 1;
+        }
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      }
       const int r0 = (tm * CG + static_cast<int>(rank)) * 128 + quarter * 32;
       const int c0 = tn * BN + half * (BN / 2);
+      if (a.tma_out && lane == 0 && r0 < p.m && c0 < p.n)
+        fetch_residual<BN / 2 < 64 ? BN / 2 : 64>(p, &map_r, stage, &rbar[e], r0, c0);
+      __syncwarp();
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[b], (n >> 1) & 1, p.status, kErrTimeoutEpilogue))) break;
+      tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * BN + half * (BN / 2);
       if (r0 < p.m) {
         if (a.tma_out) {
@@ -318,47 +378,7 @@ __global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
         else mbar_arrive(&tempty[b]);
       }
     }
-    if (lane == 0) bulk_wait_all();
-  } else if (GATHER && warp >= kFirstEpi + kEpiWarps) {
-    using G = Gather<128, BN, kGatherWarps * 32>;
-    constexpr int R = S::kRawStages > 1 ? S::kRawStages : 2;
-    G g;
-    g.a = G::side(p.x, p.ldx, p.m, p.k);
-    g.b = G::side(p.w, p.ldw, p.n, p.k);
-    g.k = p.k, g.tid = threadIdx.x - kLinThreads;
-    uint32_t s = 0, ph = 0;
-    bool ok = true;  // one thread's: all walk on together, as they share barriers
-    for (int t = walker; t < tiles; t += walkers) {
-      int tm, tn;
-      tile_of(a, t, &tm, &tn);
-      g.a.r0 = tm * 128, g.b.r0 = tn * BN;
-#pragma unroll
-      for (int k = 0; k < R - 1; ++k) {
-        if (k < kb) g.issue(raw + k * G::kStage, k * kKB);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      }
-      int rs = 0;
-      for (int k = 0; k < kb; ++k) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(R - 2) : "memory");
-        // this block has landed for every thread, and every thread is done with
-        // the one whose place the next copies take
-        named_barrier_sync(3, kGatherWarps * 32);
-        const int ahead = k + R - 1;
-        if (ahead < kb) g.issue(raw + (rs == 0 ? R - 1 : rs - 1) * G::kStage, ahead * kKB);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (ok) ok = mbar_wait_bounded(&empty[s], ph ^ 1, p.status, kErrTimeoutProducer);
-        if (ok) {
-          uint8_t* A = stages + s * S::kStage;
-          g.place(raw + rs * G::kStage, A, A + S::kA, k * kKB);
-          fence_proxy_async_smem();
-          mbar_arrive(&full[s]);
-        }
-        if (++rs == R) rs = 0;
-        if (++s == NS) s = 0, ph ^= 1;
-      }
-      // the next tile's first copies must not overtake the last block's reads
-      named_barrier_sync(3, kGatherWarps * 32);
-    }
+    if (lane == 0) bulk_wait_read<0>();  // the staging tiles must outlive their stores
   }
 
   __syncwarp();
