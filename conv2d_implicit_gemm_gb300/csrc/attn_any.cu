@@ -22,19 +22,25 @@ __global__ void __launch_bounds__(kWarps * 32) attn_any_kernel(const AttnParams 
   attend_row<T, NR>(p, b, i, h, lane);
 }
 
-template <typename T>
-cudaError_t launch_t(const AttnParams& p, cudaStream_t stream) {
+template <typename T, int NR>
+cudaError_t launch(const AttnParams& p, int device, cudaStream_t stream) {
   const int64_t items = static_cast<int64_t>(p.b) * p.hq * p.tq;
-  const dim3 grid(static_cast<unsigned>((items + kWarps - 1) / kWarps)), block(kWarps * 32);
-  if (p.d <= 64) return launch_pdl(attn_any_kernel<T, 2>, grid, block, 0, stream, p);
-  if (p.d <= 128) return launch_pdl(attn_any_kernel<T, 4>, grid, block, 0, stream, p);
-  return launch_pdl(attn_any_kernel<T, 8>, grid, block, 0, stream, p);
+  static Kernel handle;
+  return handle.launch(attn_any_kernel<T, NR>, device, dim3(static_cast<unsigned>((items + kWarps - 1) / kWarps)),
+                       kWarps * 32, 0, 1, stream, p);
+}
+
+template <typename T>
+cudaError_t launch_t(const AttnParams& p, int device, cudaStream_t stream) {
+  if (p.d <= 64) return launch<T, 2>(p, device, stream);
+  if (p.d <= 128) return launch<T, 4>(p, device, stream);
+  return launch<T, 8>(p, device, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_any(const AttnParams& p, int precision, cudaStream_t stream) {
-  return precision == OIDNX_PRECISION_BF16 ? launch_t<__nv_bfloat16>(p, stream) : launch_t<__half>(p, stream);
+cudaError_t launch_attn_any(const AttnParams& p, int precision, int device, cudaStream_t stream) {
+  return precision == OIDNX_PRECISION_BF16 ? launch_t<__nv_bfloat16>(p, device, stream) : launch_t<__half>(p, device, stream);
 }
 
 }  // namespace oidnx

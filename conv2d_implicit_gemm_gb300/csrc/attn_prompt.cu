@@ -513,10 +513,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename T, int DB>
 cudaError_t launch(const AttnLaunch& L, cudaStream_t stream) {
   auto kernel = attn_prompt_kernel<T, DB>;
-  static SmemReady ready;
-  const cudaError_t e = ready.ensure(kernel, Pr<DB>::kSmem, L.device);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(L.grid), dim3(kThreads), Pr<DB>::kSmem, stream, L.map_q, L.map_k, L.map_v, L.map_o, L.p);
+  static Kernel handle;
+  return handle.launch(kernel, L.device, dim3(L.grid), kThreads, Pr<DB>::kSmem, 1, stream, L.map_q, L.map_k, L.map_v,
+                       L.map_o, L.p);
 }
 
 }  // namespace

@@ -409,23 +409,9 @@ template <typename T, int DP, int MT>
 cudaError_t launch(const AttnParams& p, int split, int device, cudaStream_t stream) {
   using C = Tok<DP, MT>;
   auto kernel = attn_token_kernel<T, DP, MT>;
-  static SmemReady ready;
-  const cudaError_t e = ready.ensure(kernel, C::kSmem, device);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.b * p.hk * split, (p.tq * (p.hq / p.hk) + C::kRows - 1) / C::kRows);
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = split;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, split);
+  static Kernel handle;
+  return handle.launch(kernel, device, dim3(p.b * p.hk * split, (p.tq * (p.hq / p.hk) + C::kRows - 1) / C::kRows),
+                       kWarps * 32, C::kSmem, split, stream, p, split);
 }
 
 template <typename T>

@@ -235,23 +235,9 @@ template <typename T, int BN, bool GATHER>
 cudaError_t launch(const LinearTcLaunch& L, cudaStream_t stream) {
   using S = Split<BN, GATHER>;
   auto kernel = linear_split_kernel<T, BN, GATHER>;
-  static SmemReady ready;
-  const cudaError_t e = ready.ensure(kernel, S::kSmem, L.device);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((L.p.n + 127) / 128 * L.split, (L.p.m + BN - 1) / BN);
-  cfg.blockDim = dim3(GATHER ? kThreadsGather : kThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = L.split;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = L.split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, L.map_x, L.map_w, L.p, L.split);
+  static Kernel handle;
+  return handle.launch(kernel, L.device, dim3((L.p.n + 127) / 128 * L.split, (L.p.m + BN - 1) / BN),
+                       GATHER ? kThreadsGather : kThreads, S::kSmem, L.split, stream, L.map_x, L.map_w, L.p, L.split);
 }
 
 template <typename T, bool GATHER>

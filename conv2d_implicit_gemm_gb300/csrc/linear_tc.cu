@@ -397,26 +397,12 @@ cudaError_t launch(const LinearTcLaunch& L, cudaStream_t stream) {
   using S = Shape<CG, BN, GATHER>;
   TcArgs a = {L.p, (L.p.m + 128 * CG - 1) / (128 * CG), (L.p.n + BN - 1) / BN, L.tma_out};
   auto kernel = linear_tc_kernel<T, CG, BN, GATHER>;
-  static SmemReady ready;
-  const cudaError_t e = ready.ensure(kernel, S::kSmem, L.device);
-  if (e != cudaSuccess) return e;
+  static Kernel handle;
   const long long tiles = static_cast<long long>(a.tiles_m) * a.tiles_n;
   if (tiles > INT_MAX) return cudaErrorInvalidValue;
   const int walkers = static_cast<int>(tiles < L.sms / CG ? tiles : L.sms / CG);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(walkers * CG);
-  cfg.blockDim = dim3(GATHER ? kLinThreadsGather : kLinThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = CG;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, L.map_x, L.map_w, L.map_r, L.map_y, a);
+  return handle.launch(kernel, L.device, dim3(walkers * CG), GATHER ? kLinThreadsGather : kLinThreads, S::kSmem, CG,
+                       stream, L.map_x, L.map_w, L.map_r, L.map_y, a);
 }
 
 template <typename T>

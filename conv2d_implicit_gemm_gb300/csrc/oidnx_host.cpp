@@ -2277,6 +2277,8 @@ oidnx_status report_error(oidnx_status status, const char* message) {
   return fail(status, "%s", message);
 }
 
+oidnx_status report_ok() { return ok(); }
+
 // Plan the network for a w x h input with every intermediate activation
 // placed in `arena` (cap bytes) by the same liveness best-fit rule as the
 // plan cache, the input read from `in` and the output written to `out`, then

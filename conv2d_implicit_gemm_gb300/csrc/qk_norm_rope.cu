@@ -318,19 +318,21 @@ __global__ void __launch_bounds__(kAnyThreads) qk_norm_rope_any_kernel(const Nor
 }
 
 template <typename T, int P, int LPH, int NT>
-cudaError_t launch_vec(const NormParams& p, int gy, int sms, cudaStream_t stream) {
+cudaError_t launch_vec(const NormParams& p, int gy, int device, int sms, cudaStream_t stream) {
   const int total = p.heads[0] + p.heads[1] + p.heads[2];
   const int tokens = NT / 32 * (32 / (LPH ? LPH : p.d / (2 * P))) / ((total + gy - 1) / gy);
   const int most = (kCtasPerSm * sms + gy - 1) / gy;  // resident together
   const dim3 grid(std::min((p.t + tokens - 1) / tokens, most), gy);
-  return p.interleaved ? launch_pdl(qk_norm_rope_vec_kernel<T, P, LPH, NT, true>, grid, dim3(NT), 0, stream, p)
-                       : launch_pdl(qk_norm_rope_vec_kernel<T, P, LPH, NT, false>, grid, dim3(NT), 0, stream, p);
+  static Kernel adjacent, halves;
+  return p.interleaved
+             ? adjacent.launch(qk_norm_rope_vec_kernel<T, P, LPH, NT, true>, device, grid, NT, 0, 1, stream, p)
+             : halves.launch(qk_norm_rope_vec_kernel<T, P, LPH, NT, false>, device, grid, NT, 0, 1, stream, p);
 }
 
 // 8 or 12 warps, whichever leaves fewer lane groups without a head; a token
 // with more heads is split over CTA rows.
 template <typename T, int P, int LPH>
-cudaError_t launch_heads(const NormParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_heads(const NormParams& p, int device, int sms, cudaStream_t stream) {
   const int total = p.heads[0] + p.heads[1] + p.heads[2], per_warp = 32 / (LPH ? LPH : p.d / (2 * P));
   const auto busy = [&](int warps, int* gy) {
     const int groups = warps * per_warp;
@@ -340,40 +342,41 @@ cudaError_t launch_heads(const NormParams& p, int sms, cudaStream_t stream) {
   };
   int gy8, gy12;
   const float b8 = busy(8, &gy8), b12 = busy(12, &gy12);
-  return b12 > b8 ? launch_vec<T, P, LPH, 384>(p, gy12, sms, stream) : launch_vec<T, P, LPH, 256>(p, gy8, sms, stream);
+  return b12 > b8 ? launch_vec<T, P, LPH, 384>(p, gy12, device, sms, stream) : launch_vec<T, P, LPH, 256>(p, gy8, device, sms, stream);
 }
 
 template <typename T>
-cudaError_t launch_vec_t(const NormParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_vec_t(const NormParams& p, int device, int sms, cudaStream_t stream) {
   if constexpr (sizeof(T) == 2) {
-    if (p.wide && p.d == 64) return launch_heads<T, 8, 4>(p, sms, stream);
-    if (p.wide && p.d == 128) return launch_heads<T, 8, 8>(p, sms, stream);
-    if (p.wide) return launch_heads<T, 8, 0>(p, sms, stream);
+    if (p.wide && p.d == 64) return launch_heads<T, 8, 4>(p, device, sms, stream);
+    if (p.wide && p.d == 128) return launch_heads<T, 8, 8>(p, device, sms, stream);
+    if (p.wide) return launch_heads<T, 8, 0>(p, device, sms, stream);
   } else {
-    if (p.d == 64) return launch_heads<T, 4, 8>(p, sms, stream);
-    if (p.d == 128) return launch_heads<T, 4, 16>(p, sms, stream);
+    if (p.d == 64) return launch_heads<T, 4, 8>(p, device, sms, stream);
+    if (p.d == 128) return launch_heads<T, 4, 16>(p, device, sms, stream);
   }
-  return launch_heads<T, 4, 0>(p, sms, stream);
+  return launch_heads<T, 4, 0>(p, device, sms, stream);
 }
 
 template <typename T>
-cudaError_t launch_any_t(const NormParams& p, cudaStream_t stream) {
+cudaError_t launch_any_t(const NormParams& p, int device, cudaStream_t stream) {
   const int total = p.heads[0] + p.heads[1] + p.heads[2], per = kAnyThreads / 32;
-  return launch_pdl(qk_norm_rope_any_kernel<T>, dim3(p.t, (total + per - 1) / per), dim3(kAnyThreads), 0, stream, p);
+  static Kernel handle;
+  return handle.launch(qk_norm_rope_any_kernel<T>, device, dim3(p.t, (total + per - 1) / per), kAnyThreads, 0, 1, stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_norm_vec(const NormParams& p, int precision, int sms, cudaStream_t stream) {
-  if (precision == OIDNX_PRECISION_FP32) return launch_vec_t<float>(p, sms, stream);
-  if (precision == OIDNX_PRECISION_BF16) return launch_vec_t<__nv_bfloat16>(p, sms, stream);
-  return launch_vec_t<__half>(p, sms, stream);
+cudaError_t launch_norm_vec(const NormParams& p, int precision, int device, int sms, cudaStream_t stream) {
+  if (precision == OIDNX_PRECISION_FP32) return launch_vec_t<float>(p, device, sms, stream);
+  if (precision == OIDNX_PRECISION_BF16) return launch_vec_t<__nv_bfloat16>(p, device, sms, stream);
+  return launch_vec_t<__half>(p, device, sms, stream);
 }
 
-cudaError_t launch_norm_any(const NormParams& p, int precision, cudaStream_t stream) {
-  if (precision == OIDNX_PRECISION_FP32) return launch_any_t<float>(p, stream);
-  if (precision == OIDNX_PRECISION_BF16) return launch_any_t<__nv_bfloat16>(p, stream);
-  return launch_any_t<__half>(p, stream);
+cudaError_t launch_norm_any(const NormParams& p, int precision, int device, cudaStream_t stream) {
+  if (precision == OIDNX_PRECISION_FP32) return launch_any_t<float>(p, device, stream);
+  if (precision == OIDNX_PRECISION_BF16) return launch_any_t<__nv_bfloat16>(p, device, stream);
+  return launch_any_t<__half>(p, device, stream);
 }
 
 }  // namespace oidnx

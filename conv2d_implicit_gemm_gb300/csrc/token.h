@@ -4,6 +4,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -95,17 +96,30 @@ struct LinearTcLaunch {
   int split;    // split form: CTAs of a cluster along K
 };
 
-// Which devices a kernel's shared-memory limit has been raised on.
-struct SmemReady {
-  std::atomic<uint64_t> done{0};
-  template <typename K> cudaError_t ensure(K kernel, int bytes, int device) {
-    const uint64_t bit = uint64_t(1) << device;  // devices 0 to 63
-    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-    const cudaError_t e =
-        cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-    return e;
+// A kernel of the token operators, launched through the driver's call: a
+// single-token step is bound by the host, and the runtime's launch (symbol
+// look-up, configuration) is most of what this library adds to it.
+struct Kernel {
+  std::atomic<CUfunction> fn[64] = {};  // by device
+
+  template <typename... KArgs, typename... Args>
+  cudaError_t launch(void (*kernel)(KArgs...), int device, dim3 grid, int threads, int smem, int cluster,
+                     cudaStream_t stream, const Args&... args) {
+    CUfunction f = fn[device].load(std::memory_order_acquire);
+    if (!f) {
+      const cudaError_t e = find(reinterpret_cast<const void*>(kernel), smem, device, &f);
+      if (e != cudaSuccess) return e;
+    }
+    void* params[] = {const_cast<void*>(static_cast<const void*>(&args))...};
+    static_assert(sizeof...(KArgs) == sizeof...(Args), "one value a parameter");
+    static_assert((std::is_same<KArgs, Args>::value && ...), "of its type");
+    return launch_found(f, grid, threads, smem, cluster, stream, params);
   }
+
+ private:
+  cudaError_t find(const void* kernel, int smem, int device, CUfunction* f);
+  static cudaError_t launch_found(CUfunction f, dim3 grid, int threads, int smem, int cluster, cudaStream_t stream,
+                                  void** params);
 };
 
 // ---------------------------------------------------------------- norm and rotation
@@ -168,8 +182,8 @@ __device__ __forceinline__ int attn_slot(const AttnParams& p, int pos) {
 
 cudaError_t launch_linear_tc(const LinearTcLaunch& L, bool bf16, cudaStream_t stream);
 cudaError_t launch_linear_split(const LinearTcLaunch& L, bool bf16, cudaStream_t stream);
-cudaError_t launch_norm_vec(const NormParams& p, int precision, int sms, cudaStream_t stream);
-cudaError_t launch_norm_any(const NormParams& p, int precision, cudaStream_t stream);
+cudaError_t launch_norm_vec(const NormParams& p, int precision, int device, int sms, cudaStream_t stream);
+cudaError_t launch_norm_any(const NormParams& p, int precision, int device, cudaStream_t stream);
 cudaError_t launch_attn_token(const AttnParams& p, bool bf16, int split, int device, cudaStream_t stream);
 struct AttnLaunch {
   AttnParams p;
@@ -178,6 +192,6 @@ struct AttnLaunch {
   unsigned grid;
 };
 cudaError_t launch_attn_prompt(const AttnLaunch& L, bool bf16, cudaStream_t stream);
-cudaError_t launch_attn_any(const AttnParams& p, int precision, cudaStream_t stream);
+cudaError_t launch_attn_any(const AttnParams& p, int precision, int device, cudaStream_t stream);
 
 }  // namespace oidnx

@@ -13,6 +13,7 @@
 
 namespace oidnx {
 oidnx_status report_error(oidnx_status status, const char* message);
+oidnx_status report_ok();
 cudaError_t token_device(int* device, int* sms, int** status);
 cudaError_t token_status_take(int* word, cudaStream_t stream);
 }  // namespace oidnx
@@ -35,8 +36,16 @@ oidnx_status finish(cudaError_t e, const char* call) {
     return fail(e == cudaErrorMemoryAllocation ? OIDNX_ERR_OUT_OF_MEMORY : OIDNX_ERR_CUDA, "%s: %s", call,
                 cudaGetErrorString(e));
   }
-  report_error(OIDNX_OK, "");
-  return OIDNX_OK;
+  return report_ok();
+}
+
+template <typename F> F driver_call(const char* name) {
+  void* ptr = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  return cudaGetDriverEntryPointByVersion(name, &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                 q == cudaDriverEntryPointSuccess
+             ? reinterpret_cast<F>(ptr)
+             : F(nullptr);
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -46,25 +55,13 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-                   q == cudaDriverEntryPointSuccess
-               ? reinterpret_cast<EncodeFn>(ptr)
-               : EncodeFn(nullptr);
-  }();
-  return fn;
-}
-
 // A matrix of rows x cols 16-bit values with row stride ld, in boxes of
 // box_cols (64: 128-byte rows, 32: 64-byte rows) x box_rows, swizzled.
 bool matrix_map(CUtensorMap* map, bool bf16, const void* base, int64_t ld, int rows, int cols, int box_rows, int box_cols) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
-  const EncodeFn fn = encode_fn();
+  static const EncodeFn fn = driver_call<EncodeFn>("cuTensorMapEncodeTiled");
   return fn && fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                   const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -119,7 +116,7 @@ bool heads_map(CUtensorMap* map, bool bf16, const void* base, int d, int n1, int
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2,
                                  static_cast<cuuint64_t>(s3) * 2};
   const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2), 1}, step[4] = {1, 1, 1, 1};
-  const EncodeFn fn = encode_fn();
+  static const EncodeFn fn = driver_call<EncodeFn>("cuTensorMapEncodeTiled");
   return fn && fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                   const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -158,7 +155,7 @@ cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
         heads_map(&L.map_v, bf16, p.v, p.d, p.cap, p.v_s[1], p.hk, p.v_s[2], p.b, p.v_s[0], 128, 1))
       return launch_attn_prompt(L, bf16, stream);
   }
-  return launch_attn_any(p, precision, stream);
+  return launch_attn_any(p, precision, device, stream);
 }
 
 }  // namespace
@@ -245,7 +242,7 @@ oidnx_status oidnx_qk_norm_rope(const void* q, long long q_st, long long q_sh, v
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int device, sms, *status;
   cudaError_t e = token_device(&device, &sms, &status);
-  if (e == cudaSuccess) e = fast ? launch_norm_vec(p, precision, sms, s) : launch_norm_any(p, precision, s);
+  if (e == cudaSuccess) e = fast ? launch_norm_vec(p, precision, device, sms, s) : launch_norm_any(p, precision, device, s);
   return finish(e, "qk_norm_rope");
 }
 
@@ -292,6 +289,41 @@ oidnx_status oidnx_token_sync_status(void* stream) {
 
 }  // extern "C"
 
+// ---------------------------------------------------------------- launches
+cudaError_t oidnx::Kernel::find(const void* kernel, int smem, int device, CUfunction* f) {
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaFunction_t found = nullptr;
+  if (e == cudaSuccess) e = cudaGetFuncBySymbol(&found, kernel);
+  if (e != cudaSuccess) return e;
+  fn[device].store(found, std::memory_order_release);
+  *f = found;
+  return cudaSuccess;
+}
+
+// Each kernel may start its prologue under the one before it in the stream
+// (it waits for that one's results itself).
+cudaError_t oidnx::Kernel::launch_found(CUfunction f, dim3 grid, int threads, int smem, int cluster,
+                                        cudaStream_t stream, void** params) {
+  static const auto call = driver_call<CUresult (*)(const CUlaunchConfig*, CUfunction, void**, void**)>("cuLaunchKernelEx");
+  if (!call) return cudaErrorNotSupported;
+  CUlaunchAttribute at[2] = {};
+  at[0].id = CU_LAUNCH_ATTRIBUTE_PROGRAMMATIC_STREAM_SERIALIZATION;
+  at[0].value.programmaticStreamSerializationAllowed = 1;
+  at[1].id = CU_LAUNCH_ATTRIBUTE_CLUSTER_DIMENSION;
+  at[1].value.clusterDim.x = cluster;
+  at[1].value.clusterDim.y = at[1].value.clusterDim.z = 1;
+  CUlaunchConfig cfg = {};
+  cfg.gridDimX = grid.x, cfg.gridDimY = grid.y, cfg.gridDimZ = grid.z;
+  cfg.blockDimX = threads, cfg.blockDimY = cfg.blockDimZ = 1;
+  cfg.sharedMemBytes = smem;
+  cfg.hStream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return static_cast<cudaError_t>(call(&cfg, f, params, nullptr));  // the two share their codes
+}
+
 // ---------------------------------------------------------------- error word
 namespace {
 __device__ int g_token_status;
@@ -310,6 +342,14 @@ cudaError_t oidnx::token_device(int* device, int* sms, int** status) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  // The driver's calls need the device's context on the calling thread, which
+  // the runtime binds at a thread's first call that needs it.
+  static thread_local int bound = -1;
+  if (bound != dev) {
+    e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return e;
+    bound = dev;
+  }
   std::lock_guard<std::mutex> lock(g_device_mutex);
   DeviceInfo& d = g_devices[dev];
   if (!d.status) {

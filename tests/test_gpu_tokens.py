@@ -406,3 +406,27 @@ def test_calls_can_be_captured_into_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, ref[0]) and torch.equal(o, ref[1])
+
+
+def test_calls_from_a_thread_of_its_own():
+    import threading
+    x, w = strided((9, 256), "bf16", 1), strided((64, 256), "bf16", 2)
+    y = torch.empty(9, 64, dtype=torch.bfloat16, device="cuda")
+    ref = torch.empty_like(y)
+    linear(x, w, None, None, ref, "none", "bf16")
+    done()
+    args = (x.data_ptr(), 256, w.data_ptr(), 256, 0, 0, 0, y.data_ptr(), 64, 9, 64, 256, ox.ACT_NONE, ox.PRECISION_BF16,
+            torch.cuda.current_stream().cuda_stream)
+    failed = []
+
+    def work():
+        try:
+            ox.oidnx_linear(*args)
+        except Exception as e:
+            failed.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    done()
+    assert not failed and torch.equal(y, ref)
