@@ -6,6 +6,10 @@ and streams are plain integers (e.g. ``tensor.data_ptr()`` and
 ``torch.cuda.current_stream().cuda_stream``).  A non-OK status raises
 ``OidnxError`` carrying the status code and ``oidnx_last_error()``.
 
+The calls made once a token (oidnx_linear, oidnx_qk_norm_rope,
+oidnx_window_attention) go through a small extension module, _calls, as
+converting their many arguments in ctypes takes longer than the launch.
+
 Importing fails loudly when the library has not been built (there is no
 fallback): build it with ``python conv2d_implicit_gemm_gb300/build.py``.
 """
@@ -23,6 +27,12 @@ if not os.path.exists(_LIB_PATH):
         f"{_LIB_PATH} is missing: build the CUDA library first "
         "(python conv2d_implicit_gemm_gb300/build.py)")
 _lib = ctypes.CDLL(_LIB_PATH)
+try:
+    from . import _calls
+except ImportError as e:
+    raise ImportError(
+        f"{os.path.join(os.path.dirname(_LIB_PATH), '_calls.so')} is missing or unusable ({e}): "
+        "build it with the library (python conv2d_implicit_gemm_gb300/build.py)") from e
 
 OK = 0
 ERR_INVALID_ARGUMENT = 1
@@ -83,14 +93,6 @@ _sig("oidnx_filter_release", None, _vp)
 _sig("oidnx_conv_create", _st, _vp, _vp, _i, _i, _i, ctypes.POINTER(_vp))
 _sig("oidnx_conv_execute", _st, _vp, _vp, _vp, _i, _i, _i, _vp)
 _sig("oidnx_conv_release", None, _vp)
-_ll = ctypes.c_longlong
-_fl = ctypes.c_float
-_view = (_vp, _ll, _ll)
-_sig("oidnx_linear", _st, _vp, _ll, _vp, _ll, _vp, _vp, _ll, _vp, _ll, _i, _i, _i, _i, _i, _vp)
-_sig("oidnx_qk_norm_rope", _st, *_view * 6, _vp, _vp, _fl, _vp, _vp, _ll, _vp, _vp, _ll,
-     _i, _i, _i, _i, _i, _i, _i, _vp)
-_sig("oidnx_window_attention", _st, *(_vp, _ll, _ll, _ll) * 4, _vp, _vp, _vp,
-     _i, _i, _i, _i, _i, _i, _i, _i, _fl, _i, _vp)
 _sig("oidnx_token_sync_status", _st, _vp)
 _sig("oidnx_plan_tiles", _st, _i, _i, _i, _i, ctypes.POINTER(_i), _i, ctypes.POINTER(_i))
 _sig("oidnx_default_overlap", _i)
@@ -256,7 +258,7 @@ def oidnx_conv_release(c):
 
 def oidnx_linear(x, ldx, w, ldw, bias, residual, ldr, y, ldy, m, n, k, act, precision, stream=0):
     """y = act(x w^T + bias) + residual; bias and residual may be 0."""
-    _check(_lib.oidnx_linear(x, ldx, w, ldw, bias, residual, ldr, y, ldy, m, n, k, act, precision,
+    _check(_calls.oidnx_linear(x, ldx, w, ldw, bias, residual, ldr, y, ldy, m, n, k, act, precision,
                              stream))
 
 
@@ -266,7 +268,7 @@ def oidnx_qk_norm_rope(q, q_st, q_sh, q_out, qo_st, qo_sh, k, k_st, k_sh, k_out,
                        interleaved, precision, stream=0):
     """Norm and rotation of query and key heads, keys and values appended at
     their slots; q_weight, k_weight, slots and the pair v, v_out may be 0."""
-    _check(_lib.oidnx_qk_norm_rope(q, q_st, q_sh, q_out, qo_st, qo_sh, k, k_st, k_sh, k_out, ko_st,
+    _check(_calls.oidnx_qk_norm_rope(q, q_st, q_sh, q_out, qo_st, qo_sh, k, k_st, k_sh, k_out, ko_st,
                                    ko_sh, v, v_st, v_sh, v_out, vo_st, vo_sh, q_weight, k_weight,
                                    eps, cos_table, sin_table, table_rows, positions, slots,
                                    cache_rows, t, hq, hk, d, rot, interleaved, precision, stream))
@@ -277,7 +279,7 @@ def oidnx_window_attention(q, q_sb, q_st, q_sh, k, k_sb, k_st, k_sh, v, v_sb, v_
                            window, sinks, scale, precision, stream=0):
     """Attention with a sliding window and sinks over a linear or ring cache;
     lse, q_lens and kv_lens may be 0."""
-    _check(_lib.oidnx_window_attention(q, q_sb, q_st, q_sh, k, k_sb, k_st, k_sh, v, v_sb, v_st,
+    _check(_calls.oidnx_window_attention(q, q_sb, q_st, q_sh, k, k_sb, k_st, k_sh, v, v_sb, v_st,
                                        v_sh, o, o_sb, o_st, o_sh, lse, q_lens, kv_lens, b, tq, cap,
                                        hq, hk, d, window, sinks, scale, precision, stream))
 

@@ -1,4 +1,5 @@
-"""Build liboidnx.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Build liboidnx.so (the C-ABI library) in-tree with nvcc for sm_103a, and
+_calls.so, the binding's entry of the per-token calls.
 
 Usage: python conv2d_implicit_gemm_gb300/build.py   (run as a script: importing the
 package would load the library it is about to rebuild)
@@ -11,12 +12,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liboidnx.so")
+CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["oidnx_host.cpp", "conv_tc.cu", "conv_pair.cu", "conv_final.cu", "conv_tail.cu",
            "conv_head.cu", "io_passes.cu", "noalloc.cu", "token_host.cpp", "linear_tc.cu", "linear_split.cu",
            "qk_norm_rope.cu", "attn_any.cu", "attn_token.cu", "attn_prompt.cu"]
@@ -55,12 +58,24 @@ def build(verbose=False):
             sys.stderr.write(log)
     objs = [o for o, _ in results]
     tmp = LIB + ".tmp"
-    cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
+    cmd = [_nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=liboidnx.so", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
+    _build_calls()
     return LIB
+
+
+def _build_calls():
+    """_calls.so: the Python entry of the per-token calls, linked to the library beside it."""
+    tmp = CALLS + ".tmp"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "calls.c"), "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"building {CALLS} failed:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, CALLS)
 
 
 if __name__ == "__main__":
