@@ -18,7 +18,7 @@
 namespace oidnx {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 constexpr int kChunk = 16;   // keys of one step of a warp
 constexpr int kStages = 3;
 
@@ -83,7 +83,7 @@ struct Keys {
   int slot0;  // slot of position `begin`
 };
 template <typename T, int DP, int MT>
-__global__ void __launch_bounds__(kWarps * 32, 2) attn_token_kernel(const AttnParams p, const int split) {
+__global__ void __launch_bounds__(kWarps * 32, 1) attn_token_kernel(const AttnParams p, const int split) {
   using C = Tok<DP, MT>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -365,32 +365,38 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_token_kernel(const AttnPa
   const int items = rows * (p.d / 8);
   for (int e = part * kWarps * 32 + threadIdx.x; e < items; e += split * kWarps * 32) {
     const int r = e / (p.d / 8), c = e % (p.d / 8);
-    float m = -INFINITY;
-    for (int s = 0; s < split; ++s) {
-      const float x = split > 1 ? ld_cluster_f32(map_to_rank(&stats[kWarps * C::kRows + r], s))
-                                : stats[kWarps * C::kRows + r].x;
-      m = fmaxf(m, x);
+    const float* at = part_o + r * DP + c * 8;
+    const float2* st_at = &stats[kWarps * C::kRows + r];
+    // every part's loads before the first use (a remote load takes 0.7 us)
+    float2 st[8];
+    float4 u[8], v[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      st[s] = make_float2(-INFINITY, 0.f);
+      u[s] = v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s >= split) continue;
+      if (split > 1) {
+        const uint32_t sa = map_to_rank(st_at, s), oa = map_to_rank(at, s);
+        st[s].x = ld_cluster_f32(sa), st[s].y = ld_cluster_f32(sa + 4);
+        u[s] = ld_cluster_f4(oa), v[s] = ld_cluster_f4(oa + 16);
+      } else {
+        st[s] = *st_at;
+        u[s] = *reinterpret_cast<const float4*>(at), v[s] = *reinterpret_cast<const float4*>(at + 4);
+      }
     }
+    float m = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) m = fmaxf(m, st[s].x);
     const float base = m == -INFINITY ? 0.f : m;
     float acc[8] = {}, l = 0.f;
-    for (int s = 0; s < split; ++s) {
-      float2 st;
-      float4 u, v;
-      const float* at = part_o + r * DP + c * 8;
-      if (split > 1) {
-        const uint32_t sa = map_to_rank(&stats[kWarps * C::kRows + r], s), oa = map_to_rank(at, s);
-        st.x = ld_cluster_f32(sa), st.y = ld_cluster_f32(sa + 4);
-        u = ld_cluster_f4(oa), v = ld_cluster_f4(oa + 16);
-      } else {
-        st = stats[kWarps * C::kRows + r];
-        u = *reinterpret_cast<const float4*>(at), v = *reinterpret_cast<const float4*>(at + 4);
-      }
-      const float f = exp2_fast(st.x - base);
-      l = fmaf(st.y, f, l);
-      acc[0] = fmaf(u.x, f, acc[0]), acc[1] = fmaf(u.y, f, acc[1]);
-      acc[2] = fmaf(u.z, f, acc[2]), acc[3] = fmaf(u.w, f, acc[3]);
-      acc[4] = fmaf(v.x, f, acc[4]), acc[5] = fmaf(v.y, f, acc[5]);
-      acc[6] = fmaf(v.z, f, acc[6]), acc[7] = fmaf(v.w, f, acc[7]);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const float f = exp2_fast(st[s].x - base);
+      l = fmaf(st[s].y, f, l);
+      acc[0] = fmaf(u[s].x, f, acc[0]), acc[1] = fmaf(u[s].y, f, acc[1]);
+      acc[2] = fmaf(u[s].z, f, acc[2]), acc[3] = fmaf(u[s].w, f, acc[3]);
+      acc[4] = fmaf(v[s].x, f, acc[4]), acc[5] = fmaf(v[s].y, f, acc[5]);
+      acc[6] = fmaf(v[s].z, f, acc[6]), acc[7] = fmaf(v[s].w, f, acc[7]);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: zeros
 #pragma unroll

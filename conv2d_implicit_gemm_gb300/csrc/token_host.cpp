@@ -136,8 +136,17 @@ cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
     // the most keys that a query tile can see
     int64_t keys = p.cap;
     if (p.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(p.window) + p.held_sinks + p.tq - 1);
+    // Rounds of resident CTAs (one an SM, two with heads of up to 64 values)
+    // times a CTA's keys; its start and the joining cost as much as about 900
+    // keys (64 ragged streams of 8 key heads, up to 4100 keys: 134 us unsplit,
+    // 197 in four; one stream: 12 us in eight, 38 in two).
+    const int64_t slots = static_cast<int64_t>(sms) * (p.d <= 64 ? 2 : 1);
     int split = 1;
-    while (split < 8 && units * split < 2 * sms && keys / (2 * split) >= 128) split *= 2;
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= 8; s *= 2) {
+      const int64_t cost = (units * s + slots - 1) / slots * (keys / s + 900);
+      if (cost < best) best = cost, split = s;
+    }
     return launch_attn_token(p, precision == OIDNX_PRECISION_BF16, split, device, stream);
   }
   bool tiles = pieces && group <= 128 && p.scale > 0.f && p.cap > 0;
