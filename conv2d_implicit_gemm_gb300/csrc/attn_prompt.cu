@@ -63,6 +63,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -92,6 +97,9 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void*
 struct Tile {
   int slot, pos, count;
 };
+
+// The lowest n of 32 bits (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
 // What a CTA works on; every role computes the same.
 struct Plan {
@@ -192,8 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* vfull = kempty + NS;
   uint64_t* vempty = vfull + NS;
   uint64_t* sfull = vempty + NS;  // [2]
-  uint64_t* pfull = sfull + 2;    // [2]
-  uint64_t* odone = pfull + 2;    // [2]
+  uint64_t* pfull = sfull + 2;    // [2 row tiles][2 halves of the keys]
+  uint64_t* odone = pfull + 4;    // [2]
   uint64_t* vclean = odone + 2;   // [NS]
   uint32_t* slot = reinterpret_cast<uint32_t*>(vclean + NS);
   int* odd = reinterpret_cast<int*>(slot + 1);
@@ -210,7 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&qfull[t], 1);
       mbar_init(&sfull[t], 1);
-      mbar_init(&pfull[t], 128);
+      mbar_init(&pfull[2 * t], 128);
+      mbar_init(&pfull[2 * t + 1], 128);
       mbar_init(&odone[t], 1);
     }
     *odd = 0;
@@ -238,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < w.tiles && ok; ++j) {
           const Tile k = w.tile(p, j);
           const int s = j % NS, ph = (j / NS) & 1;
-          ok = mbar_wait_bounded(&kempty[s], ph ^ 1, p.status, kErrTimeoutProducer);
+          ok = mbar_wait_soon(&kempty[s], ph ^ 1, p.status, kErrTimeoutProducer);
           if (!ok) break;
           mbar_arrive_expect_tx(&kfull[s], C::kTile);
 #pragma unroll
@@ -253,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_4d(Q + t * C::kTile + d * 16384, &map_q, &qfull[t], d * 64, w.kvh * w.group, w.i0(t), w.b, pol);
             }
           }
-          ok = mbar_wait_bounded(&vempty[s], ph ^ 1, p.status, kErrTimeoutProducer);
+          ok = mbar_wait_soon(&vempty[s], ph ^ 1, p.status, kErrTimeoutProducer);
           if (!ok) break;
           mbar_arrive_expect_tx(&vfull[s], C::kTile);
 #pragma unroll
@@ -279,10 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (w.tiles > 0) {
           const Tile k = w.tile(p, 0);
-          ok = mbar_wait_bounded(&kfull[0], 0, p.status, kErrTimeoutMma);
+          ok = mbar_wait_soon(&kfull[0], 0, p.status, kErrTimeoutMma);
           for (int t = 0; t < 2 && ok; ++t) {
             if (!w.active(t)) continue;
-            ok = mbar_wait_bounded(&qfull[t], 0, p.status, kErrTimeoutMma);
+            ok = mbar_wait_soon(&qfull[t], 0, p.status, kErrTimeoutMma);
             tc_fence_after();
             if (ok && w.seen(p, t, k)) score(t, 0, k);
           }
@@ -293,9 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = j % NS;
           const bool more = j + 1 < w.tiles;
           const Tile kn = w.tile(p, more ? j + 1 : j);
-          ok = mbar_wait_bounded(&vfull[s], (j / NS) & 1, p.status, kErrTimeoutMma);
+          ok = mbar_wait_soon(&vfull[s], (j / NS) & 1, p.status, kErrTimeoutMma);
           if (ok && w.looked_over(p, k)) {
-            ok = mbar_wait_bounded(&vclean[s], clean >> s & 1, p.status, kErrTimeoutMma);
+            ok = mbar_wait_soon(&vclean[s], clean >> s & 1, p.status, kErrTimeoutMma);
             clean ^= 1u << s;
           }
           bool next_ready = false;
@@ -304,18 +313,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < 2; ++t) {
             if (!ok) break;
             if (w.seen(p, t, k)) {
-              ok = mbar_wait_bounded(&pfull[t], n_p[t] & 1, p.status, kErrTimeoutMma);
-              if (!ok) break;
-              tc_fence_after();
               const int steps = (k.count + 15) / 16;
-              for (int i = 0; i < steps; ++i)
-                mma_ts(o_col(t), s_col(t) + i * 8, value_desc(va + i * 2048), id_pv, n_p[t] > 0 || i > 0);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (ok) ok = mbar_wait_soon(&pfull[2 * t + h], n_p[t] & 1, p.status, kErrTimeoutMma);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 4 * h; i < 4 * h + 4; ++i)
+                  if (i < steps)
+                    mma_ts(o_col(t), s_col(t) + i * 8, value_desc(va + i * 2048), id_pv, n_p[t] > 0 || i > 0);
+              }
+              if (!ok) break;
               mma_commit(&odone[t]);
               ++n_p[t];
             }
             if (more && w.seen(p, t, kn)) {
               if (!next_ready) {
-                ok = mbar_wait_bounded(&kfull[(j + 1) % NS], ((j + 1) / NS) & 1, p.status, kErrTimeoutMma);
+                ok = mbar_wait_soon(&kfull[(j + 1) % NS], ((j + 1) / NS) & 1, p.status, kErrTimeoutMma);
                 if (!ok) break;
                 tc_fence_after();
                 next_ready = true;
@@ -334,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Tile k = w.tile(p, j);
         if (!w.looked_over(p, k)) continue;
         const int s = j % NS;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&vfull[s], (j / NS) & 1, p.status, kErrTimeoutProducer))) break;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_soon(&vfull[s], (j / NS) & 1, p.status, kErrTimeoutProducer))) break;
         uint8_t* V = Vs + s * C::kTile;
         const int rows = (k.count + 15) / 16 * 16;
         bool found = false;
@@ -373,42 +388,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; j < w.tiles && ok; ++j) {
       const Tile k = w.tile(p, j);
       if (!w.seen(p, t, k)) continue;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sfull[t], n & 1, p.status, kErrTimeoutEpilogue));
+      const bool whole = w.whole(p, t, k);
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&sfull[t], n & 1, p.status, kErrTimeoutEpilogue));
       if (!ok) break;
       tc_fence_after();
+      // S from tensor memory; the second half's columns are on their way while
+      // the first's are looked at
       uint32_t raw[4][32];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (q * 32 < k.count) {
-          tmem_ld32_nowait(s_col(t) + lanes + q * 32, raw[q]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) raw[q][e] = 0xFF800000u;
-        }
-      }
+      tmem_ld32_nowait(s_col(t) + lanes, raw[0]);
+      tmem_ld32_nowait(s_col(t) + lanes + 32, raw[1]);
       tmem_wait_ld();
-      if (!w.whole(p, t, k)) {
-        const int hi = min(k.count - 1, pos - k.pos);  // columns lo .. hi, and the sinks
-        const int lo = p.window > 0 ? pos - p.window + 1 - k.pos : 0;
-        const int sk = min(p.sinks - k.pos, hi + 1);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int x = q * 32 + e;
-            if (!((x >= lo && x <= hi) || x < sk)) raw[q][e] = 0xFF800000u;
-          }
-      }
+      tmem_ld32_nowait(s_col(t) + lanes + 64, raw[2]);
+      tmem_ld32_nowait(s_col(t) + lanes + 96, raw[3]);
       float m4[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        m4[q] = __uint_as_float(raw[q][0]);
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1) tmem_wait_ld();
+        if (!whole) {
+          // columns lo .. hi, and the sinks
+          const int hi = min(k.count - 1, pos - k.pos) - h * 64;
+          const int lo = (p.window == 0 ? 0 : max(pos - p.window + 1 - k.pos, 0)) - h * 64;
+          const int sk = min(p.sinks - k.pos - h * 64, hi + 1);
 #pragma unroll
-        for (int e = 1; e < 31; e += 2)
-          m4[q] = fmaxf(m4[q], fmaxf(__uint_as_float(raw[q][e]), __uint_as_float(raw[q][e + 1])));
-        m4[q] = fmaxf(m4[q], __uint_as_float(raw[q][31]));
+          for (int q = 2 * h; q < 2 * h + 2; ++q) {
+            const int o = (q & 1) * 32;
+            const uint32_t bits = (below(hi + 1 - o) & ~below(lo - o)) | below(sk - o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) raw[q][e] = bits >> e & 1u ? raw[q][e] : 0xFF800000u;
+          }
+        }
+#pragma unroll
+        for (int q = 2 * h; q < 2 * h + 2; ++q) {
+          m4[q] = fmaxf(__uint_as_float(raw[q][0]), __uint_as_float(raw[q][1]));
+#pragma unroll
+          for (int e = 2; e < 32; e += 2) m4[q] = max3(m4[q], __uint_as_float(raw[q][e]), __uint_as_float(raw[q][e + 1]));
+        }
       }
-      const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      const float m = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
       const bool rise = (m - top) * c > 8.f;
       if (__any_sync(0xFFFFFFFFu, rise)) {
         const float up = fmaxf(m, top);
@@ -416,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         top = up;
         sum *= f;
         if (n > 0) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&odone[t], (n - 1) & 1, p.status, kErrTimeoutEpilogue));
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&odone[t], (n - 1) & 1, p.status, kErrTimeoutEpilogue));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -435,26 +451,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (q * 32 >= k.count) continue;
-        uint32_t pk[16];
+        if (q * 32 < k.count) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 x = f2_of(fma2(f2(__uint_as_float(raw[q][e]), __uint_as_float(raw[q][e + 1])), c2, b2));
-          const float u = exp2_fast(x.x), v = exp2_fast(x.y);
-          acc[(e >> 1) & 1] = add2(acc[(e >> 1) & 1], f2(u, v));
-          pk[e / 2] = pack2<T>(u, v);
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = f2_of(fma2(f2(__uint_as_float(raw[q][e]), __uint_as_float(raw[q][e + 1])), c2, b2));
+            const float u = exp2_fast(x.x), v = exp2_fast(x.y);
+            acc[(e >> 1) & 1] = add2(acc[(e >> 1) & 1], f2(u, v));
+            pk[e / 2] = pack2<T>(u, v);
+          }
+          tmem_st16(s_col(t) + lanes + q * 16, pk);
         }
-        tmem_st16(s_col(t) + lanes + q * 16, pk);
+        if (q & 1) {  // half of the keys: their product may start
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&pfull[2 * t + (q >> 1)]);
+        }
       }
       const float2 a = f2_of(add2(acc[0], acc[1]));
       sum += a.x + a.y;
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&pfull[t]);
       ++n;
     }
     if (n > 0 && ok) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&odone[t], (n - 1) & 1, p.status, kErrTimeoutEpilogue));
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&odone[t], (n - 1) & 1, p.status, kErrTimeoutEpilogue));
       tc_fence_after();
     }
     // output: through the row tile's query tile, which no product reads any more

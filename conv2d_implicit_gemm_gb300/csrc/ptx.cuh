@@ -94,6 +94,15 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   return false;
 }
 
+// The same with a few tries before the clock is first read: for waits on the
+// critical path of short steps.
+__device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, int* status, int code) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_bounded(bar, parity, status, code);
+}
+
 // ---------------------------------------------------------------- grid dependencies
 // Programmatic dependent launch: the next kernel in the stream may start its
 // independent prologue early; griddep_wait() blocks until the preceding grid
