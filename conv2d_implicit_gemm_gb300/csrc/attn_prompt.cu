@@ -19,12 +19,13 @@
 //    over the keys.  The sum of the weights is taken before the rounding.
 //  * Tiles that every row sees whole skip the mask.  In the others a value
 //    that is no number must not reach rows that do not see it (0 x NaN):
-//    two warps look the tile's values over first, clear what lies past the
+//    a warp looks the tile's values over first, clears what lies past the
 //    keys, and where a key itself holds such a value the CTA's rows are done
 //    again one by one.
 //
 // Warps 0-3 and 4-7: softmax of row tile 0 and 1, rescaling, output; warp 8
-// loads (TMA), warp 9 multiplies, warps 10 and 11 look values over.
+// loads (TMA), warps 9 and 10 issue the products of a row tile each (one thread
+// for both was the bound), warp 11 looks values over.
 #include <type_traits>
 
 #include "attn_row.cuh"
@@ -34,7 +35,9 @@
 namespace oidnx {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kSoftWarps = 8;
+constexpr int kThreads = (kSoftWarps + 4) * 32;
+constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kLookWarp = kSoftWarps + 3;
 constexpr int kTileKeys = 128;
 
 template <int DB> struct Pr {  // DB: 64-value blocks of a head (1 or 2)
@@ -84,6 +87,8 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 // Value operand: rows of 64 values (128 bytes, swizzled) a key, 8 keys 1024
 // bytes apart, 64-value blocks 16384 bytes apart; values contiguous (N-major).
+// An operand's descriptors differ in their start address only (16-byte units in
+// the low bits, which do not overflow), so the issuing thread adds constants.
 __device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
   return smem_desc_sw128(saddr) | (static_cast<uint64_t>(16384u >> 4) << 16);
 }
@@ -92,6 +97,16 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void*
                    reinterpret_cast<uint64_t>(map)),
                "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(src))
                : "memory");
+}
+
+// sum + 0 v of pairs: zeros of either sign while every v is a number.
+template <typename T> __device__ __forceinline__ uint32_t add_nulls(uint32_t sum, uint32_t v) {
+  uint32_t r;
+  if constexpr (std::is_same<T, __half>::value)
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0u), "r"(sum));
+  else
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0u), "r"(sum));
+  return r;
 }
 
 struct Tile {
@@ -109,7 +124,9 @@ struct Plan {
   int sinks, n_sinks;                  // keys and tiles of the sinks' run
   int begin, slot0, len_a, n_a, len_b; // the window: up to the ring's end, and from its start on
   int tiles;
+  int plain_lo, plain_hi;  // tiles of 128 keys that every row of both row tiles sees whole, as far as they are in one run
 
+  __device__ __forceinline__ bool plain(int j) const { return j >= plain_lo && j < plain_hi; }
   __device__ __forceinline__ Tile tile(const AttnParams& p, int j) const {
     Tile t;
     if (j < n_sinks) {
@@ -161,7 +178,7 @@ __device__ __forceinline__ Plan make_plan(const AttnParams& p) {
   w.max1 = w.pq + min(w.i00 + 2 * w.per, w.nq) - 1;
   const bool on0 = w.active(0), on1 = w.active(1);
   const int lo = on0 ? w.min0 : w.min1, hi = on1 ? w.max1 : on0 ? w.max0 : -1;
-  w.sinks = w.n_sinks = w.begin = w.slot0 = w.len_a = w.n_a = w.len_b = w.tiles = 0;
+  w.sinks = w.n_sinks = w.begin = w.slot0 = w.len_a = w.n_a = w.len_b = w.tiles = w.plain_lo = w.plain_hi = 0;
   if (hi < 0) return w;
   w.sinks = min(min(p.held_sinks, w.n), hi + 1);
   w.begin = attn_ring_begin(p, w.n);
@@ -179,6 +196,12 @@ __device__ __forceinline__ Plan make_plan(const AttnParams& p) {
   w.n_sinks = (w.sinks + kTileKeys - 1) / kTileKeys;
   w.n_a = (w.len_a + kTileKeys - 1) / kTileKeys;
   w.tiles = w.n_sinks + w.n_a + (w.len_b + kTileKeys - 1) / kTileKeys;
+  // whole: the last key at or before the first row's position, the first key in
+  // the last row's window
+  const int past = p.window > 0 ? hi - p.window - w.begin : -1;
+  const int room = lo + 1 - w.begin;
+  w.plain_lo = w.n_sinks + (past >= 0 ? past / kTileKeys + 1 : 0);
+  w.plain_hi = w.n_sinks + min(w.len_a, max(room, 0)) / kTileKeys;
   return w;
 }
 
@@ -210,10 +233,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 1);
+      mbar_init(&kempty[s], 2);  // both row tiles' products
       mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], 1);
-      mbar_init(&vclean[s], 64);
+      mbar_init(&vempty[s], 2);
+      mbar_init(&vclean[s], 32);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&qfull[t], 1);
@@ -225,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *odd = 0;
     fence_mbarrier_init();
   }
-  if (warp == 9) tmem_alloc(slot, 512);
+  if (warp == kMmaWarp) tmem_alloc(slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -238,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto s_col = [tmem](int t) { return tmem + t * 128; };
   const auto o_col = [tmem](int t) { return tmem + 256 + t * 64 * DB; };
 
-  if (warp >= 8) {
-    if (warp == 8) {
+  if (warp >= kSoftWarps) {
+    if (warp == kLoadWarp) {
       if (lane == 0) {
         const uint64_t pol = l2_evict_normal();
         const int q_bytes = w.per * w.group * 128;
@@ -270,102 +293,119 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d(Vs + s * C::kTile + d * 16384, &map_v, &vfull[s], d * 64, k.slot, w.kvh, w.b, pol);
         }
       }
-    } else if (warp == 9) {
+    } else if (warp < kLookWarp) {
+      // one warp a row tile; each waits for every key tile, also those that its
+      // rows do not see, so that its arrivals stay in step with the ring
+      const int t = warp - kMmaWarp;
       if (elect_one()) {
         constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-        const uint32_t id_pv = idesc_16(bf, 128, kd * 16, true);
-        int n_p[2] = {0, 0};
+        const uint32_t id_s = idesc_16(bf, 128, kTileKeys), id_pv = idesc_16(bf, 128, kd * 16, true);
+        const uint64_t qd = smem_desc_sw128(smem_u32(Q + t * C::kTile));
+        const uint64_t kd0 = smem_desc_sw128(smem_u32(Ks)), vd0 = value_desc(smem_u32(Vs));
+        const uint32_t s_at = s_col(t), o_at = o_col(t);
+        int n = 0;
         uint32_t clean = 0;  // phase of each stage's looked-over barrier
         bool ok = true;
-        auto score = [&](int t, int j, const Tile& k) {  // S of row tile t and key tile j
-          const uint32_t id = idesc_16(bf, 128, (k.count + 15) / 16 * 16);
-          const uint32_t qa = smem_u32(Q + t * C::kTile), ka = smem_u32(Ks + (j % NS) * C::kTile);
-          for (int i = 0; i < kd; ++i) {
-            const uint32_t off = (i >> 2) * 16384 + (i & 3) * 32;
-            mma_f16_ss(s_col(t), smem_desc_sw128(qa + off), smem_desc_sw128(ka + off), id, i > 0);
+        const auto score = [&](uint64_t kt, int count) {  // S of the key tile at kt
+          const uint32_t id = count == kTileKeys ? id_s : idesc_16(bf, 128, (count + 15) / 16 * 16);
+#pragma unroll
+          for (int i = 0; i < 4 * DB; ++i) {
+            const uint32_t off = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
+            if (i < kd) mma_f16_ss(s_at, qd + off, kt + off, id, i > 0);
           }
           mma_commit(&sfull[t]);
         };
         if (w.tiles > 0) {
           const Tile k = w.tile(p, 0);
           ok = mbar_wait_soon(&kfull[0], 0, p.status, kErrTimeoutMma);
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (!w.active(t)) continue;
+          if (ok && w.active(t)) {
             ok = mbar_wait_soon(&qfull[t], 0, p.status, kErrTimeoutMma);
             tc_fence_after();
-            if (ok && w.seen(p, t, k)) score(t, 0, k);
+            if (ok && w.seen(p, t, k)) score(kd0, k.count);
           }
           mma_commit(&kempty[0]);
         }
+        int s = 0, ph = 0;
         for (int j = 0; j < w.tiles && ok; ++j) {
-          const Tile k = w.tile(p, j);
-          const int s = j % NS;
-          const bool more = j + 1 < w.tiles;
-          const Tile kn = w.tile(p, more ? j + 1 : j);
-          ok = mbar_wait_soon(&vfull[s], (j / NS) & 1, p.status, kErrTimeoutMma);
-          if (ok && w.looked_over(p, k)) {
+          const int s1 = s + 1 == NS ? 0 : s + 1, ph1 = s + 1 == NS ? ph ^ 1 : ph;
+          bool see = w.active(t), look = false;
+          int steps = kTileKeys / 16;
+          if (!w.plain(j)) {
+            const Tile k = w.tile(p, j);
+            see = w.seen(p, t, k), look = w.looked_over(p, k);
+            steps = (k.count + 15) / 16;
+          }
+          bool see1 = j + 1 < w.tiles && w.active(t);
+          int count1 = kTileKeys;
+          if (see1 && !w.plain(j + 1)) {
+            const Tile k = w.tile(p, j + 1);
+            see1 = w.seen(p, t, k);
+            count1 = k.count;
+          }
+          ok = mbar_wait_soon(&vfull[s], ph, p.status, kErrTimeoutMma);
+          if (ok && look) {
             ok = mbar_wait_soon(&vclean[s], clean >> s & 1, p.status, kErrTimeoutMma);
             clean ^= 1u << s;
           }
-          bool next_ready = false;
-          const uint32_t va = smem_u32(Vs + s * C::kTile);
+          if (see) {
+            const uint64_t vt = vd0 + s * (C::kTile >> 4);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!ok) break;
-            if (w.seen(p, t, k)) {
-              const int steps = (k.count + 15) / 16;
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if (ok) ok = mbar_wait_soon(&pfull[2 * t + h], n_p[t] & 1, p.status, kErrTimeoutMma);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int i = 4 * h; i < 4 * h + 4; ++i)
-                  if (i < steps)
-                    mma_ts(o_col(t), s_col(t) + i * 8, value_desc(va + i * 2048), id_pv, n_p[t] > 0 || i > 0);
-              }
+            for (int h = 0; h < 2; ++h) {
+              if (ok) ok = mbar_wait_soon(&pfull[2 * t + h], n & 1, p.status, kErrTimeoutMma);
               if (!ok) break;
-              mma_commit(&odone[t]);
-              ++n_p[t];
+              tc_fence_after();
+#pragma unroll
+              for (int i = 4 * h; i < 4 * h + 4; ++i)
+                if (i < steps) mma_ts(o_at, s_at + i * 8, vt + i * (2048 >> 4), id_pv, n > 0 || i > 0);
             }
-            if (more && w.seen(p, t, kn)) {
-              if (!next_ready) {
-                ok = mbar_wait_soon(&kfull[(j + 1) % NS], ((j + 1) / NS) & 1, p.status, kErrTimeoutMma);
-                if (!ok) break;
-                tc_fence_after();
-                next_ready = true;
-              }
-              score(t, j + 1, kn);
-            }
+            if (!ok) break;
+            mma_commit(&odone[t]);
+            ++n;
           }
+          if (!ok) break;
           mma_commit(&vempty[s]);
-          if (more) mma_commit(&kempty[(j + 1) % NS]);
+          if (j + 1 < w.tiles) {
+            ok = mbar_wait_soon(&kfull[s1], ph1, p.status, kErrTimeoutMma);
+            if (!ok) break;
+            tc_fence_after();
+            if (see1) score(kd0 + s1 * (C::kTile >> 4), count1);
+            mma_commit(&kempty[s1]);
+          }
+          s = s1, ph = ph1;
         }
       }
     } else {
       // look over the values of tiles that some row does not see whole
-      const int tid = threadIdx.x - 320;
-      for (int j = 0; j < w.tiles; ++j) {
+            for (int j = 0; j < w.tiles; ++j) {
+        if (w.plain(j)) {
+          j = w.plain_hi - 1;
+          continue;
+        }
         const Tile k = w.tile(p, j);
         if (!w.looked_over(p, k)) continue;
         const int s = j % NS;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_soon(&vfull[s], (j / NS) & 1, p.status, kErrTimeoutProducer))) break;
         uint8_t* V = Vs + s * C::kTile;
         const int rows = (k.count + 15) / 16 * 16;
+        // 0 x v is NaN where v is none: a sum of them tells in one instruction a pair
+        uint32_t sum[2] = {0u, 0u};
+#pragma unroll 8
+        for (int e = lane; e < rows * 8 * DB; e += 32) {
+          const int block = e / (rows * 8);  // any order of a row's pieces will do
+          const uint4 v = *reinterpret_cast<const uint4*>(V + block * 16384 + (e - block * rows * 8) * 16);
+          sum[0] = add_nulls<T>(add_nulls<T>(sum[0], v.x), v.y);
+          sum[1] = add_nulls<T>(add_nulls<T>(sum[1], v.z), v.w);
+        }
         bool found = false;
-#pragma unroll 4
-        for (int e = tid; e < rows * 8 * DB; e += 64) {
-          const int block = e / (rows * 8), r = e / 8 % rows;  // any order of a row's pieces will do
-          uint4* at = reinterpret_cast<uint4*>(V + block * 16384 + r * 128 + (e % 8) * 16);
-          const uint4 v = *at;
-          const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-          constexpr uint32_t x = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
-          bool bad = false;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) bad |= (q[i] & x) == x || (q[i] & (x << 16)) == (x << 16);
-          if (bad) {
-            if (r >= k.count) *at = make_uint4(0u, 0u, 0u, 0u);
-            else found = true;
+        if (__any_sync(0xFFFFFFFFu, (sum[0] | sum[1]) & 0x7FFF7FFFu)) {
+          for (int e = lane; e < rows * 8 * DB; e += 32) {
+            const int block = e / (rows * 8), r = (e - block * rows * 8) / 8;
+            uint4* at = reinterpret_cast<uint4*>(V + block * 16384 + (e - block * rows * 8) * 16);
+            const uint4 v = *at;
+            if ((add_nulls<T>(add_nulls<T>(0u, v.x), v.y) | add_nulls<T>(add_nulls<T>(0u, v.z), v.w)) & 0x7FFF7FFFu) {
+              if (r >= k.count) *at = make_uint4(0u, 0u, 0u, 0u);
+              else found = true;
+            }
           }
         }
         if (found) *odd = 1;
@@ -385,10 +425,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     float sum = 0.f;
     int n = 0;
     bool ok = true;
-    for (int j = 0; j < w.tiles && ok; ++j) {
-      const Tile k = w.tile(p, j);
-      if (!w.seen(p, t, k)) continue;
-      const bool whole = w.whole(p, t, k);
+    const int tiles = w.active(t) ? w.tiles : 0;
+    for (int j = 0; j < tiles && ok; ++j) {
+      Tile k;
+      k.count = kTileKeys;
+      bool whole = true;
+      if (!w.plain(j)) {
+        k = w.tile(p, j);
+        if (!w.seen(p, t, k)) continue;
+        whole = w.whole(p, t, k);
+      }
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&sfull[t], n & 1, p.status, kErrTimeoutEpilogue));
       if (!ok) break;
       tc_fence_after();
@@ -516,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
