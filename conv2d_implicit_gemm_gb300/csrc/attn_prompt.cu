@@ -294,8 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp < kLookWarp) {
-      // one warp a row tile; each waits for every key tile, also those that its
-      // rows do not see, so that its arrivals stay in step with the ring
+      // One warp a row tile.  Its thread only issues: a commit covers all the
+      // thread's earlier products, so the scores of key tile j landing tells the
+      // softmax warps that P V of the tile before is done too, and they hand the
+      // stages back (keys of j, values of j - 1).  What its rows do not see the
+      // thread hands back itself, in step with the ring.
       const int t = warp - kMmaWarp;
       if (elect_one()) {
         constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
@@ -315,28 +318,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mma_commit(&sfull[t]);
         };
+        bool see = false;
         if (w.tiles > 0) {
           const Tile k = w.tile(p, 0);
+          see = w.seen(p, t, k);
           ok = mbar_wait_soon(&kfull[0], 0, p.status, kErrTimeoutMma);
-          if (ok && w.active(t)) {
-            ok = mbar_wait_soon(&qfull[t], 0, p.status, kErrTimeoutMma);
-            tc_fence_after();
-            if (ok && w.seen(p, t, k)) score(kd0, k.count);
-          }
-          mma_commit(&kempty[0]);
+          if (ok && see) ok = mbar_wait_soon(&qfull[t], 0, p.status, kErrTimeoutMma);
+          tc_fence_after();
+          if (ok && see) score(kd0, k.count);
+          else mbar_arrive(&kempty[0]);
         }
         int s = 0, ph = 0;
         for (int j = 0; j < w.tiles && ok; ++j) {
           const int s1 = s + 1 == NS ? 0 : s + 1, ph1 = s + 1 == NS ? ph ^ 1 : ph;
-          bool see = w.active(t), look = false;
-          int steps = kTileKeys / 16;
+          bool look = false, see1 = j + 1 < w.tiles && w.active(t);
+          int steps = kTileKeys / 16, count1 = kTileKeys;
           if (!w.plain(j)) {
             const Tile k = w.tile(p, j);
-            see = w.seen(p, t, k), look = w.looked_over(p, k);
+            look = w.looked_over(p, k);
             steps = (k.count + 15) / 16;
           }
-          bool see1 = j + 1 < w.tiles && w.active(t);
-          int count1 = kTileKeys;
           if (see1 && !w.plain(j + 1)) {
             const Tile k = w.tile(p, j + 1);
             see1 = w.seen(p, t, k);
@@ -347,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait_soon(&vclean[s], clean >> s & 1, p.status, kErrTimeoutMma);
             clean ^= 1u << s;
           }
+          if (ok && j + 1 < w.tiles) ok = mbar_wait_soon(&kfull[s1], ph1, p.status, kErrTimeoutMma);
           if (see) {
             const uint64_t vt = vd0 + s * (C::kTile >> 4);
 #pragma unroll
@@ -358,21 +360,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 4 * h; i < 4 * h + 4; ++i)
                 if (i < steps) mma_ts(o_at, s_at + i * 8, vt + i * (2048 >> 4), id_pv, n > 0 || i > 0);
             }
-            if (!ok) break;
-            mma_commit(&odone[t]);
             ++n;
           }
           if (!ok) break;
-          mma_commit(&vempty[s]);
-          if (j + 1 < w.tiles) {
-            ok = mbar_wait_soon(&kfull[s1], ph1, p.status, kErrTimeoutMma);
-            if (!ok) break;
-            tc_fence_after();
-            if (see1) score(kd0 + s1 * (C::kTile >> 4), count1);
-            mma_commit(&kempty[s1]);
+          if (see1) {
+            score(kd0 + s1 * (C::kTile >> 4), count1);
+          } else if (j + 1 < w.tiles) {
+            mma_commit(&vempty[s]);
+            mbar_arrive(&kempty[s1]);
           }
+          see = see1;
           s = s1, ph = ph1;
         }
+        mma_commit(&odone[t]);
       }
     } else {
       // look over the values of tiles that some row does not see whole
@@ -438,6 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&sfull[t], n & 1, p.status, kErrTimeoutEpilogue));
       if (!ok) break;
       tc_fence_after();
+      if (r == 0) {
+        mbar_arrive(&kempty[j % NS]);
+        if (j > 0) mbar_arrive(&vempty[(j - 1) % NS]);
+      }
       // S from tensor memory; the second half's columns are on their way while
       // the first's are looked at
       uint32_t raw[4][32];
@@ -477,10 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f = up == -INFINITY ? 1.f : exp2_fast((top - up) * c);
         top = up;
         sum *= f;
-        if (n > 0) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&odone[t], (n - 1) & 1, p.status, kErrTimeoutEpilogue));
-          if (!ok) break;
-          tc_fence_after();
+        if (n > 0) {  // (the last P V is done: these scores were committed behind it)
 #pragma unroll 1
           for (int x = 0; x < kd * 16; x += 16) {
             uint32_t o[16];
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n;
     }
     if (n > 0 && ok) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&odone[t], (n - 1) & 1, p.status, kErrTimeoutEpilogue));
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&odone[t], 0, p.status, kErrTimeoutEpilogue));
       tc_fence_after();
     }
     // output: through the row tile's query tile, which no product reads any more
