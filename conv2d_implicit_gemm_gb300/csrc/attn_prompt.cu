@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&kfull[s], 1);
       mbar_init(&kempty[s], 2);  // both row tiles' products
       mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], 2);
+      mbar_init(&vempty[s], 3);  // and the looking warp
       mbar_init(&vclean[s], 32);
     }
     for (int t = 0; t < 2; ++t) {
@@ -375,16 +375,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(&odone[t]);
       }
     } else {
-      // look over the values of tiles that some row does not see whole
-            for (int j = 0; j < w.tiles; ++j) {
-        if (w.plain(j)) {
-          j = w.plain_hi - 1;
-          continue;
-        }
-        const Tile k = w.tile(p, j);
-        if (!w.looked_over(p, k)) continue;
+      // look over the values of tiles that some row does not see whole; every
+      // tile is waited for and handed back, so that the phases stay in step
+      for (int j = 0; j < w.tiles; ++j) {
         const int s = j % NS;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_soon(&vfull[s], (j / NS) & 1, p.status, kErrTimeoutProducer))) break;
+        const Tile k = w.tile(p, j);
+        if (w.plain(j) || !w.looked_over(p, k)) {
+          if (lane == 0) mbar_arrive(&vempty[s]);
+          continue;
+        }
         uint8_t* V = Vs + s * C::kTile;
         const int rows = (k.count + 15) / 16 * 16;
         // 0 x v is NaN where v is none: a sum of them tells in one instruction a pair
@@ -411,6 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (found) *odd = 1;
         fence_proxy_async_smem();
         mbar_arrive(&vclean[s]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&vempty[s]);
       }
     }
   } else {

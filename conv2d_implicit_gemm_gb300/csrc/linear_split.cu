@@ -25,11 +25,10 @@ template <int BN, bool GATHER> struct Split {
   static constexpr int kA = 128 * 128;
   static constexpr int kB = BN * 128;
   static constexpr int kStage = kA + kB;
-  // two CTAs per SM, but for wide gathered tiles; most of a gathering CTA's
-  // room holds blocks on their way as they lie in memory
-  static constexpr int kCtas = GATHER && BN > 32 ? 1 : 2;
-  static constexpr int kStages = GATHER ? (BN == 64 ? 3 : 2) : 110 * 1024 / kStage;
-  static constexpr int kRawStages = GATHER ? (BN == 64 ? 5 : BN == 128 ? 4 : 3) : 0;
+  // two CTAs per SM; a gathering one's room holds blocks on their way as they
+  // lie in memory as well
+  static constexpr int kStages = GATHER ? 2 : 110 * 1024 / kStage;
+  static constexpr int kRawStages = GATHER ? 3 : 0;
   static constexpr int kRaw = kRawStages * (128 + BN) * 144;
   static constexpr int kSmem = kStages * kStage + kRaw + 2048;
   static constexpr int kCols = BN < 32 ? 32 : BN;
@@ -37,7 +36,7 @@ template <int BN, bool GATHER> struct Split {
 };
 
 template <typename T, int BN, bool GATHER>
-__global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, Split<BN, GATHER>::kCtas)
+__global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 2)
     linear_split_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                         const LinearParams p, const int split) {
   using S = Split<BN, GATHER>;
@@ -240,20 +239,19 @@ cudaError_t launch(const LinearTcLaunch& L, cudaStream_t stream) {
                        GATHER ? kThreadsGather : kThreads, S::kSmem, L.split, stream, L.map_x, L.map_w, L.p, L.split);
 }
 
-template <typename T, bool GATHER>
-cudaError_t launch_bn(const LinearTcLaunch& L, cudaStream_t stream) {
-  if (L.bn <= 16) return launch<T, 16, GATHER>(L, stream);
-  if (L.bn <= 32) return launch<T, 32, GATHER>(L, stream);
-  if (L.bn <= 64) return launch<T, 64, GATHER>(L, stream);
-  return launch<T, 128, GATHER>(L, stream);
+template <typename T>
+cudaError_t launch_t(const LinearTcLaunch& L, cudaStream_t stream) {
+  if (L.gather) return L.bn <= 16 ? launch<T, 16, true>(L, stream) : launch<T, 32, true>(L, stream);
+  if (L.bn <= 16) return launch<T, 16, false>(L, stream);
+  if (L.bn <= 32) return launch<T, 32, false>(L, stream);
+  if (L.bn <= 64) return launch<T, 64, false>(L, stream);
+  return launch<T, 128, false>(L, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_split(const LinearTcLaunch& L, bool bf16, cudaStream_t stream) {
-  if (bf16)
-    return L.gather ? launch_bn<__nv_bfloat16, true>(L, stream) : launch_bn<__nv_bfloat16, false>(L, stream);
-  return L.gather ? launch_bn<__half, true>(L, stream) : launch_bn<__half, false>(L, stream);
+  return bf16 ? launch_t<__nv_bfloat16>(L, stream) : launch_t<__half>(L, stream);
 }
 
 }  // namespace oidnx

@@ -1,14 +1,14 @@
 // Linear layer on the 5th-generation tensor cores: y = act(x w^T + bias) + residual.
 //
-//  * Output tiles of 128 x BN per CTA, or 256 x 256 per CTA pair
+//  * Output tiles of 128 x BN per CTA, or 256 x BN per CTA pair
 //    (cta_group::2: each CTA holds its 128 rows of x and half of the tile's
 //    rows of w, and the pair reads both), fp32 accumulators in tensor memory,
 //    two of them, so that one tile's epilogue runs under the next tile's
 //    products.  Persistent CTAs walk the tiles in groups of 8 row blocks, so
 //    that the tiles in flight share their operands in L2.
 //  * K in blocks of 64 values: one 128-byte swizzled TMA box per operand and
-//    block.  Matrices whose rows do not start on 16 bytes are gathered into the
-//    same layout by four warps that copy and the epilogue's, which shift.
+//    block.  (Matrices whose rows do not start on 16 bytes are laid out anew
+//    before, by linear_align.cu.)
 //  * Epilogue: eight warps, each 32 rows x half the columns, through 32 x 64
 //    tiles of 16-bit values that TMA stores (and, for the residual, loads
 //    first); outputs that TMA cannot store go through 32 x 32 fp32 tiles and
@@ -21,7 +21,6 @@
 #include <climits>
 #include <type_traits>
 
-#include "linear_load.cuh"
 #include "ptx.cuh"
 #include "token.h"
 #include "token_math.cuh"
@@ -30,21 +29,19 @@ namespace oidnx {
 namespace {
 
 constexpr int kEpiWarps = 8;
-constexpr int kFirstEpi = 4;  // warp 0 loads, warp 1 multiplies; gathered operands: 2, 3 and two more copy
+constexpr int kFirstEpi = 4;  // warp 0 loads, warp 1 multiplies, 2 and 3 rest
 constexpr int kLinThreads = (kFirstEpi + kEpiWarps) * 32;
-constexpr int kLinThreadsGather = kLinThreads + 64;
 constexpr int kStageOut = 4096;  // bytes of staging per epilogue warp
+constexpr int kKB = 64;          // values of one K block: one 128-byte row of a tile
 constexpr int kRowGroup = 8;     // row blocks walked together
 
-template <int CG, int BN, bool GATHER> struct Shape {
+template <int CG, int BN> struct Shape {
   static constexpr int kA = 128 * 128;              // bytes of a CTA's x block
   static constexpr int kB = BN / CG * 128;          // bytes of its w block
   static constexpr int kStage = kA + kB;
-  static constexpr int kRawStages = GATHER ? 3 : 0;  // blocks on their way as they lie in memory
-  static constexpr int kRaw = kRawStages * (128 + BN) * 144;
-  static constexpr int kRoom = 227 * 1024 - 2048 - kEpiWarps * kStageOut - kRaw;
+  static constexpr int kRoom = 227 * 1024 - 2048 - kEpiWarps * kStageOut;
   static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
-  static constexpr int kSmem = kStages * kStage + kEpiWarps * kStageOut + kRaw + 2048;
+  static constexpr int kSmem = kStages * kStage + kEpiWarps * kStageOut + 2048;
   static constexpr int kCols = 2 * BN < 32 ? 32 : 2 * BN;
 };
 
@@ -191,36 +188,33 @@ __device__ __forceinline__ void epilogue_any(const TcArgs& a, uint32_t tmem, int
   }
 }
 
-template <typename T, int CG, int BN, bool GATHER>
-__global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
+template <typename T, int CG, int BN>
+__global__ void __launch_bounds__(kLinThreads, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                      const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_y,
                      const TcArgs a) {
-  using S = Shape<CG, BN, GATHER>;
+  using S = Shape<CG, BN>;
   constexpr int NS = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;  // every tile starts on 1024 bytes
   uint8_t* staging = stages + NS * S::kStage;
-  uint8_t* raw = staging + kEpiWarps * kStageOut;
-  uint64_t* full = reinterpret_cast<uint64_t*>(raw + S::kRaw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStageOut);
   uint64_t* empty = full + NS;
   uint64_t* tfull = empty + NS;    // [2]
   uint64_t* tempty = tfull + 2;    // [2]
   uint64_t* rbar = tempty + 2;     // [kEpiWarps] residual tiles
-  uint64_t* rawfull = rbar + kEpiWarps;       // [RS]
-  uint64_t* rawempty = rawfull + S::kRawStages;
-  uint32_t* slot = reinterpret_cast<uint32_t*>(rawempty + S::kRawStages);
+  uint32_t* slot = reinterpret_cast<uint32_t*>(rbar + kEpiWarps);
   const LinearParams& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
-  const int kb = p.k > 0 ? (p.k + kKB - 1) / kKB : 1;  // k = 0: one block of zeros
+  const int kb = (p.k + kKB - 1) / kKB;
   const int tiles = a.tiles_m * a.tiles_n;
   const int walker = blockIdx.x / CG, walkers = gridDim.x / CG;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], GATHER ? kEpiWarps : 1);
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -228,10 +222,6 @@ __global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
       mbar_init(&tempty[b], CG * kEpiWarps);
     }
     for (int w = 0; w < kEpiWarps; ++w) mbar_init(&rbar[w], 1);
-    for (int r = 0; r < S::kRawStages; ++r) {
-      mbar_init(&rawfull[r], 2 * kCopyThreads);
-      mbar_init(&rawempty[r], kEpiWarps);
-    }
     fence_mbarrier_init();
   }
   if (warp == 1) {
@@ -247,7 +237,7 @@ __global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
   griddep_wait();
 
   if (warp == 0) {
-    if (!GATHER && lane == 0) {
+    if (lane == 0) {
       prefetch_tmap(&map_x);
       prefetch_tmap(&map_w);
       const uint64_t pol = l2_evict_normal();
@@ -306,56 +296,16 @@ __global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
         else mma_commit(&tfull[b]);
       }
     }
-  } else if (warp < kFirstEpi || warp >= kFirstEpi + kEpiWarps) {
-    if constexpr (GATHER) {
-      const int tid = warp < kFirstEpi ? threadIdx.x - 64 : threadIdx.x - kLinThreads + 64;
-      Gather<128, BN> g;
-      g.matrices(p.x, p.ldx, p.m, p.w, p.ldw, p.n, p.k);
-      int r = 0, ph = 0;
-      bool ok = true;
-      for (int t = walker; t < tiles && ok; t += walkers) {
-        int tm, tn;
-        tile_of(a, t, &tm, &tn);
-        g.a.r0 = tm * 128, g.b.r0 = tn * BN;
-        for (int k = 0; k < kb; ++k) {
-          ok = mbar_wait_bounded(&rawempty[r], ph ^ 1, p.status, kErrTimeoutProducer);
-          if (!ok) break;
-          g.copy_block(raw + r * g.kStage, &rawfull[r], k * kKB, tid);
-          if (++r == S::kRawStages) r = 0, ph ^= 1;
-        }
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-    }
-  } else {
+  } else if (warp >= kFirstEpi) {
     const int e = warp - kFirstEpi;
     const int quarter = warp & 3, half = e >> 2;  // the TMEM lanes a warp may read; its columns
     uint8_t* stage = staging + e * kStageOut;
     uint32_t rphase = 0;
     int n = 0;
-    [[maybe_unused]] uint32_t s = 0, ph = 0, rs = 0, rph = 0;  // gathered operands
     for (int t = walker; t < tiles; t += walkers, ++n) {
       const int b = n & 1;
       int tm, tn;
       tile_of(a, t, &tm, &tn);
-      if constexpr (GATHER) {
-        Gather<128, BN> g;
-        g.matrices(p.x, p.ldx, p.m, p.w, p.ldw, p.n, p.k);
-        g.a.r0 = tm * 128, g.b.r0 = tn * BN;
-        bool ok = true;
-        for (int k = 0; k < kb; ++k) {
-          ok = mbar_wait_bounded(&rawfull[rs], rph, p.status, kErrTimeoutProducer) &&
-               mbar_wait_bounded(&empty[s], ph ^ 1, p.status, kErrTimeoutProducer);
-          if (!__all_sync(0xFFFFFFFFu, ok)) break;
-          uint8_t* A = stages + s * S::kStage;
-          g.place(raw + rs * g.kStage, A, A + S::kA, p.k - k * kKB, threadIdx.x - kFirstEpi * 32);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[s]), mbar_arrive(&rawempty[rs]);
-          if (++s == NS) s = 0, ph ^= 1;
-          if (++rs == S::kRawStages) rs = 0, rph ^= 1;
-        }
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      }
       const int r0 = (tm * CG + static_cast<int>(rank)) * 128 + quarter * 32;
       const int c0 = tn * BN + half * (BN / 2);
       if (a.tma_out && lane == 0 && r0 < p.m && c0 < p.n)
@@ -392,28 +342,24 @@ __global__ void __launch_bounds__(GATHER ? kLinThreadsGather : kLinThreads, 1)
   }
 }
 
-template <typename T, int CG, int BN, bool GATHER>
+template <typename T, int CG, int BN>
 cudaError_t launch(const LinearTcLaunch& L, cudaStream_t stream) {
-  using S = Shape<CG, BN, GATHER>;
+  using S = Shape<CG, BN>;
   TcArgs a = {L.p, (L.p.m + 128 * CG - 1) / (128 * CG), (L.p.n + BN - 1) / BN, L.tma_out};
-  auto kernel = linear_tc_kernel<T, CG, BN, GATHER>;
+  auto kernel = linear_tc_kernel<T, CG, BN>;
   static Kernel handle;
   const long long tiles = static_cast<long long>(a.tiles_m) * a.tiles_n;
   if (tiles > INT_MAX) return cudaErrorInvalidValue;
   const int walkers = static_cast<int>(tiles < L.sms / CG ? tiles : L.sms / CG);
-  return handle.launch(kernel, L.device, dim3(walkers * CG), GATHER ? kLinThreadsGather : kLinThreads, S::kSmem, CG,
+  return handle.launch(kernel, L.device, dim3(walkers * CG), kLinThreads, S::kSmem, CG,
                        stream, L.map_x, L.map_w, L.map_r, L.map_y, a);
 }
 
 template <typename T>
 cudaError_t launch_t(const LinearTcLaunch& L, cudaStream_t stream) {
-  if (L.gather) {
-    if (L.bn == 64) return launch<T, 1, 64, true>(L, stream);
-    return launch<T, 1, 128, true>(L, stream);
-  }
-  if (L.pair) return launch<T, 2, 256, false>(L, stream);
-  if (L.bn == 64) return launch<T, 1, 64, false>(L, stream);
-  return launch<T, 1, 128, false>(L, stream);
+  if (L.pair) return L.bn == 256 ? launch<T, 2, 256>(L, stream) : launch<T, 2, 128>(L, stream);
+  if (L.bn == 64) return launch<T, 1, 64>(L, stream);
+  return launch<T, 1, 128>(L, stream);
 }
 
 }  // namespace

@@ -84,14 +84,24 @@ struct LinearParams {
   int* status;
 };
 
+// Matrices of k values a row to be copied to rows that start on 16 bytes.
+struct AlignParams {
+  struct Matrix {
+    const void* from;
+    void* to;
+    int64_t ld, ld_to, rows;
+  } matrix[2];
+  int k;
+};
+
 // Launch of a tensor-core form; maps that a form does not use are zero.
 struct LinearTcLaunch {
   LinearParams p;
   CUtensorMap map_x, map_w, map_r, map_y;
   int device, sms;
-  int bn;       // columns per tile: 64 or 128 (pair: 256); split form: tokens per tile
-  int pair;     // CTA pairs on 256 x 256 tiles
-  int gather;   // x and w through plain loads
+  int bn;       // columns per tile: 64 or 128 (pair: 128 or 256); split form: tokens per tile
+  int pair;     // CTA pairs on tiles of 256 rows
+  int gather;   // split form: x and w through plain loads
   int tma_out;  // y and residual through TMA
   int split;    // split form: CTAs of a cluster along K
 };
@@ -181,6 +191,7 @@ __device__ __forceinline__ int attn_slot(const AttnParams& p, int pos) {
 }
 
 cudaError_t launch_linear_tc(const LinearTcLaunch& L, bool bf16, cudaStream_t stream);
+cudaError_t launch_align_rows(const AlignParams& p, int count, int device, int sms, cudaStream_t stream);
 cudaError_t launch_linear_split(const LinearTcLaunch& L, bool bf16, cudaStream_t stream);
 cudaError_t launch_norm_vec(const NormParams& p, int precision, int device, int sms, cudaStream_t stream);
 cudaError_t launch_norm_any(const NormParams& p, int precision, int device, cudaStream_t stream);

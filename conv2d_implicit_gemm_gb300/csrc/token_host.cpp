@@ -72,37 +72,111 @@ bool matrix_map(CUtensorMap* map, bool bf16, const void* base, int64_t ld, int r
 bool tma_rows(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0 && ld < (int64_t(1) << 38); }
 
 // ---------------------------------------------------------------- linear: choice of form
+// Memory of one call, ordered on its stream, from a pool of the library's own
+// that keeps what it has been given (the default pool hands it back to the
+// system at every synchronisation).
+cudaError_t scratch_pool(int device, cudaMemPool_t* out) {
+  static std::mutex mutex;
+  static cudaMemPool_t pools[64] = {};
+  std::lock_guard<std::mutex> lock(mutex);
+  if (!pools[device]) {
+    cudaMemPoolProps props = {};
+    props.allocType = cudaMemAllocationTypePinned;
+    props.location.type = cudaMemLocationTypeDevice;
+    props.location.id = device;
+    cudaMemPool_t pool;
+    cudaError_t e = cudaMemPoolCreate(&pool, &props);
+    if (e != cudaSuccess) return e;
+    uint64_t keep = UINT64_MAX;
+    e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    if (e != cudaSuccess) return e;
+    pools[device] = pool;
+  }
+  *out = pools[device];
+  return cudaSuccess;
+}
+
+// Few rows: K split over clusters, tokens as the narrow operand.
+cudaError_t run_split(LinearTcLaunch& L, bool bf16, cudaStream_t stream) {
+  const LinearParams& p = L.p;
+  L.gather = p.k == 0 || !tma_rows(p.x, p.ldx) || !tma_rows(p.w, p.ldw);
+  L.bn = p.m <= 16 ? 16 : p.m <= 32 || L.gather ? 32 : p.m <= 64 ? 64 : 128;
+  const int64_t tiles = int64_t((p.n + 127) / 128) * ((p.m + L.bn - 1) / L.bn), blocks = (p.k + 63) / 64;
+  L.split = 1;
+  while (L.split < 8 && tiles * L.split <= L.sms && blocks / (L.split * 2) >= 4) L.split *= 2;
+  if (!L.gather && !(matrix_map(&L.map_x, bf16, p.x, p.ldx, p.m, p.k, L.bn, 64) &&
+                     matrix_map(&L.map_w, bf16, p.w, p.ldw, p.n, p.k, 128, 64)))
+    return cudaErrorInvalidValue;
+  return launch_linear_split(L, bf16, stream);
+}
+
+// Many rows, x and w with rows that TMA can address.
+cudaError_t run_tiles(LinearTcLaunch& L, bool bf16, cudaStream_t stream) {
+  const LinearParams& p = L.p;
+  // Cycles of a tile shape: rounds of resident tiles times their K blocks, each
+  // bound by its operands' way into the SM (64 bytes a cycle: 384 for 128 x 64
+  // and for half a pair's 256 x 128, 512 for 128 x 128 and half of 256 x 256),
+  // plus the last tile's epilogue, 28 a column, and a pair's start.  Measured for
+  // the shapes in this order, us: 512 x 2048 x 2048: 10.6, 12.1, 11.6, 15.8;
+  // 2000 x 1000 x 4000: 33, 20, 24, 24; 8192 x 512 x 4096: 55, 33, 37, 26;
+  // 8192 x 256 x 256: 5.7, 6.4, 5.7, 7.9.
+  struct Form {
+    int rows, cols, pair, block;
+  };
+  static const Form forms[] = {{128, 64, 0, 384}, {256, 128, 1, 384}, {128, 128, 0, 512}, {256, 256, 1, 512}};
+  const int64_t blocks = (p.k + 63) / 64;
+  int64_t best = INT64_MAX;
+  for (const Form& f : forms) {
+    const int64_t tiles = int64_t((p.m + f.rows - 1) / f.rows) * ((p.n + f.cols - 1) / f.cols);
+    const int64_t slots = f.pair ? L.sms / 2 : L.sms;
+    const int64_t cost = (tiles + slots - 1) / slots * (blocks * f.block + 1500) + 28 * f.cols + 1200 * f.pair;
+    if (cost < best) best = cost, L.pair = f.pair, L.bn = f.cols;
+  }
+  L.tma_out = tma_rows(p.y, p.ldy) && (!p.residual || tma_rows(p.residual, p.ldr));
+  const int cols = L.bn == 64 ? 32 : 64;
+  const bool ok = matrix_map(&L.map_x, bf16, p.x, p.ldx, p.m, p.k, 128, 64) &&
+                  matrix_map(&L.map_w, bf16, p.w, p.ldw, p.n, p.k, L.pair ? L.bn / 2 : L.bn, 64) &&
+                  (!L.tma_out || matrix_map(&L.map_y, bf16, p.y, p.ldy, p.m, p.n, 32, cols)) &&
+                  (!L.tma_out || !p.residual || matrix_map(&L.map_r, bf16, p.residual, p.ldr, p.m, p.n, 32, cols));
+  return ok ? launch_linear_tc(L, bf16, stream) : cudaErrorInvalidValue;
+}
+
 cudaError_t run_linear(const LinearParams& params, bool bf16, cudaStream_t stream) {
   LinearTcLaunch L = {};
   L.p = params;
   LinearParams& p = L.p;
   cudaError_t e = token_device(&L.device, &L.sms, &p.status);
   if (e != cudaSuccess) return e;
-  L.gather = p.k == 0 || !tma_rows(p.x, p.ldx) || !tma_rows(p.w, p.ldw);
-  bool ok = true;
-  if (p.m <= 128) {
-    L.bn = p.m <= 16 ? 16 : p.m <= 32 ? 32 : p.m <= 64 ? 64 : 128;
-    const int tiles = (p.n + 127) / 128 * ((p.m + L.bn - 1) / L.bn), blocks = (p.k + 63) / 64;
-    L.split = 1;
-    while (L.split < 8 && tiles * L.split * 2 <= 2 * L.sms && blocks / (L.split * 2) >= 4) L.split *= 2;
-    if (!L.gather)
-      ok = matrix_map(&L.map_x, bf16, p.x, p.ldx, p.m, p.k, L.bn, 64) &&
-           matrix_map(&L.map_w, bf16, p.w, p.ldw, p.n, p.k, 128, 64);
-    return ok ? launch_linear_split(L, bf16, stream) : cudaErrorInvalidValue;
+  const bool x_fits = tma_rows(p.x, p.ldx), w_fits = tma_rows(p.w, p.ldw);
+  // Few rows read the weight once, so they gather it as it lies (16 x 4000 x
+  // 3501: 15 us, laid out anew first: 22); from 33 rows on, with one gathering
+  // CTA an SM, its copying bounds it (64 rows: 34 and 26).  k = 0 has nothing to
+  // fetch, which the gathering form's cleared blocks serve.
+  if (p.m <= 32 || p.k == 0 || (p.m <= 128 && x_fits && w_fits)) return run_split(L, bf16, stream);
+  if (x_fits && w_fits) return run_tiles(L, bf16, stream);
+  const int64_t ld = (static_cast<int64_t>(p.k) + 7) / 8 * 8;
+  const int64_t x_bytes = x_fits ? 0 : ld * p.m * 2, w_bytes = w_fits ? 0 : ld * p.n * 2;
+  cudaMemPool_t pool;
+  void* scratch = nullptr;
+  e = scratch_pool(L.device, &pool);
+  if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&scratch, x_bytes + w_bytes, pool, stream);
+  if (e != cudaSuccess) return e;
+  AlignParams a = {};
+  a.k = p.k;
+  int count = 0;
+  if (!x_fits) {
+    a.matrix[count++] = {p.x, scratch, p.ldx, ld, p.m};
+    p.x = scratch, p.ldx = ld;
   }
-  const auto tiles = [&](int rows, int cols) { return int64_t((p.m + rows - 1) / rows) * ((p.n + cols - 1) / cols); };
-  L.pair = !L.gather && tiles(256, 256) >= L.sms / 2 - 8;
-  L.bn = L.pair ? 256 : tiles(128, 128) * 2 <= L.sms ? 64 : 128;
-  L.tma_out = tma_rows(p.y, p.ldy) && (!p.residual || tma_rows(p.residual, p.ldr));
-  if (!L.gather)
-    ok = matrix_map(&L.map_x, bf16, p.x, p.ldx, p.m, p.k, 128, 64) &&
-         matrix_map(&L.map_w, bf16, p.w, p.ldw, p.n, p.k, L.pair ? 128 : L.bn, 64);
-  if (L.tma_out) {
-    const int cols = L.bn == 64 ? 32 : 64;
-    ok = ok && matrix_map(&L.map_y, bf16, p.y, p.ldy, p.m, p.n, 32, cols) &&
-         (!p.residual || matrix_map(&L.map_r, bf16, p.residual, p.ldr, p.m, p.n, 32, cols));
+  if (!w_fits) {
+    void* to = static_cast<uint8_t*>(scratch) + x_bytes;
+    a.matrix[count++] = {p.w, to, p.ldw, ld, p.n};
+    p.w = to, p.ldw = ld;
   }
-  return ok ? launch_linear_tc(L, bf16, stream) : cudaErrorInvalidValue;
+  e = launch_align_rows(a, count, L.device, L.sms, stream);
+  if (e == cudaSuccess) e = p.m <= 128 ? run_split(L, bf16, stream) : run_tiles(L, bf16, stream);
+  const cudaError_t freed = cudaFreeAsync(scratch, stream);
+  return e != cudaSuccess ? e : freed;
 }
 
 // ---------------------------------------------------------------- attention: choice of form

@@ -297,6 +297,15 @@ def test_attention_ring_cache(tq, cap, sinks, window):
                     kv_lens=[cap, cap + 1, 3 * cap + 17, 1000003], seed=cap)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tq,cap,kv,window,sinks", [
+    (300, 2500, 2390, 900, 4), (200, 3000, 2871, 0, 0), (600, 1500, 1500, 700, 130), (150, 1400, 5000, 1200, 7),
+    (90, 4000, 3980, 3000, 1)])
+def test_attention_many_key_tiles(tq, cap, kv, window, sinks, d):
+    """Long caches with partly written last tiles: first and last tiles masked, many whole ones between."""
+    check_attention(2, tq, cap, 2, 1, d, window, sinks, "bf16", kv_lens=[kv, min(kv, cap) - 131], seed=kv)
+
+
 @pytest.mark.parametrize("pad,shift", [(8, 0), (8, 8), (3, 0), (0, 1), (8, 4)])
 @pytest.mark.parametrize("tq", [1, 70])
 def test_attention_strides_and_alignment(tq, pad, shift):
