@@ -439,3 +439,18 @@ def test_calls_from_a_thread_of_its_own():
     t.join()
     done()
     assert not failed and torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_stream_in_steps_over_a_ring_equals_one_pass(dtype):
+    """The example's block: prompt steps, then single tokens, over a ring, against one call over a cache of everything.
+    The two round the same intermediate values to 16 bits in places that differ by what fp32 sums in another order give:
+    a few units of the storage type through six roundings."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_stream.py")
+    spec = importlib.util.spec_from_file_location("attention_stream", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    off = example.run(tokens=450, prompt_step=48, singles=12, streams=3, window=100, dtype=dtype, channels=256)
+    assert off <= 6 * UNIT["fp16" if dtype == torch.float16 else "bf16"]
