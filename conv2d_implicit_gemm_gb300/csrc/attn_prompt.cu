@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&kfull[s], C::kTile);
 #pragma unroll
           for (int d = 0; d < DB; ++d)
-            tma_load_4d(Ks + s * C::kTile + d * 16384, &map_k, &kfull[s], d * 64, k.slot, w.kvh, w.b, pol);
+            tma_load_4d(Ks + s * C::kTile + d * 16384, &map_k, &kfull[s], d * 64, k.slot, p.k_s[2] ? w.kvh : 0, p.k_s[0] ? w.b : 0, pol);
           if (j == 0) {
             for (int t = 0; t < 2; ++t) {
               if (!w.active(t)) continue;
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&vfull[s], C::kTile);
 #pragma unroll
           for (int d = 0; d < DB; ++d)
-            tma_load_4d(Vs + s * C::kTile + d * 16384, &map_v, &vfull[s], d * 64, k.slot, w.kvh, w.b, pol);
+            tma_load_4d(Vs + s * C::kTile + d * 16384, &map_v, &vfull[s], d * 64, k.slot, p.v_s[2] ? w.kvh : 0, p.v_s[0] ? w.b : 0, pol);
         }
       }
     } else if (warp < kLookWarp) {

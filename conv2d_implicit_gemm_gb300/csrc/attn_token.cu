@@ -411,26 +411,39 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_token_kernel(const AttnPa
   if (split > 1) cluster_sync();  // a part stays until everyone has read it
 }
 
+// slots: only count the CTAs that the device holds at once.
 template <typename T, int DP, int MT>
-cudaError_t launch(const AttnParams& p, int split, int device, cudaStream_t stream) {
+cudaError_t launch(const AttnParams& p, int split, int device, cudaStream_t stream, int* slots) {
   using C = Tok<DP, MT>;
   auto kernel = attn_token_kernel<T, DP, MT>;
   static Kernel handle;
+  if (slots) {
+    *slots = handle.clusters(kernel, device, kWarps * 32, C::kSmem, split) * split;
+    return cudaSuccess;
+  }
   return handle.launch(kernel, device, dim3(p.b * p.hk * split, (p.tq * (p.hq / p.hk) + C::kRows - 1) / C::kRows),
                        kWarps * 32, C::kSmem, split, stream, p, split);
 }
 
 template <typename T>
-cudaError_t launch_t(const AttnParams& p, int split, int device, cudaStream_t stream) {
+cudaError_t launch_t(const AttnParams& p, int split, int device, cudaStream_t stream, int* slots) {
   const bool two = p.tq * (p.hq / p.hk) > 16;
-  if (p.d <= 64) return two ? launch<T, 64, 2>(p, split, device, stream) : launch<T, 64, 1>(p, split, device, stream);
-  return two ? launch<T, 128, 2>(p, split, device, stream) : launch<T, 128, 1>(p, split, device, stream);
+  if (p.d <= 64)
+    return two ? launch<T, 64, 2>(p, split, device, stream, slots) : launch<T, 64, 1>(p, split, device, stream, slots);
+  return two ? launch<T, 128, 2>(p, split, device, stream, slots) : launch<T, 128, 1>(p, split, device, stream, slots);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_token(const AttnParams& p, bool bf16, int split, int device, cudaStream_t stream) {
-  return bf16 ? launch_t<__nv_bfloat16>(p, split, device, stream) : launch_t<__half>(p, split, device, stream);
+  return bf16 ? launch_t<__nv_bfloat16>(p, split, device, stream, nullptr)
+              : launch_t<__half>(p, split, device, stream, nullptr);
+}
+
+int attn_token_slots(const AttnParams& p, bool bf16, int split, int device) {
+  int slots = 0;
+  bf16 ? launch_t<__nv_bfloat16>(p, split, device, nullptr, &slots) : launch_t<__half>(p, split, device, nullptr, &slots);
+  return slots;
 }
 
 }  // namespace oidnx

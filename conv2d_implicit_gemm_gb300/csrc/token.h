@@ -125,8 +125,15 @@ struct Kernel {
     static_assert((std::is_same<KArgs, Args>::value && ...), "of its type");
     return launch_found(f, grid, threads, smem, cluster, stream, params);
   }
+  // Clusters that the device holds at once (by its GPCs: 15 of eight CTAs of one
+  // an SM, not 152 / 8).
+  template <typename K> int clusters(K kernel, int device, int threads, int smem, int cluster) {
+    return count_clusters(reinterpret_cast<const void*>(kernel), device, threads, smem, cluster);
+  }
 
  private:
+  std::atomic<int> held[4][64] = {};  // by log2 of the cluster, device
+  int count_clusters(const void* kernel, int device, int threads, int smem, int cluster);
   cudaError_t find(const void* kernel, int smem, int device, CUfunction* f);
   static cudaError_t launch_found(CUfunction f, dim3 grid, int threads, int smem, int cluster, cudaStream_t stream,
                                   void** params);
@@ -196,6 +203,8 @@ cudaError_t launch_linear_split(const LinearTcLaunch& L, bool bf16, cudaStream_t
 cudaError_t launch_norm_vec(const NormParams& p, int precision, int device, int sms, cudaStream_t stream);
 cudaError_t launch_norm_any(const NormParams& p, int precision, int device, cudaStream_t stream);
 cudaError_t launch_attn_token(const AttnParams& p, bool bf16, int split, int device, cudaStream_t stream);
+// CTAs in clusters of `split` that the device holds at once.
+int attn_token_slots(const AttnParams& p, bool bf16, int split, int device);
 struct AttnLaunch {
   AttnParams p;
   CUtensorMap map_q, map_k, map_v, map_o;

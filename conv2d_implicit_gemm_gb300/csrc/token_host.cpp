@@ -202,40 +202,73 @@ cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
   const cudaError_t e = token_device(&device, &sms, &p.status);
   if (e != cudaSuccess) return e;
   const int group = p.hq / p.hk;
+  // the stride of a dimension of one element says nothing
+  const int64_t any = (static_cast<int64_t>(p.d) + 7) / 8 * 8;
+  if (p.b == 1) p.q_s[0] = p.k_s[0] = p.v_s[0] = p.o_s[0] = any;
+  if (p.tq == 1) p.q_s[1] = p.o_s[1] = any;
+  if (p.cap == 1) p.k_s[1] = p.v_s[1] = any;
+  if (p.hq == 1) p.q_s[2] = p.o_s[2] = any;
+  if (p.hk == 1) p.k_s[2] = p.v_s[2] = any;
   bool pieces = p.d % 8 == 0 && p.d <= 128 && aligned(p.q, 16) && aligned(p.k, 16) && aligned(p.v, 16) && aligned(p.o, 16);
   for (int i = 0; i < 3; ++i)
     pieces = pieces && p.q_s[i] % 8 == 0 && p.k_s[i] % 8 == 0 && p.v_s[i] % 8 == 0 && p.o_s[i] % 8 == 0;
-  const int64_t rows = static_cast<int64_t>(p.tq) * group, units = static_cast<int64_t>(p.b) * p.hk * ((rows + 31) / 32);
-  if (pieces && rows <= 64 && units < (1 << 27)) {
-    // the most keys that a query tile can see
-    int64_t keys = p.cap;
-    if (p.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(p.window) + p.held_sinks + p.tq - 1);
-    // Rounds of resident CTAs (one an SM, two with heads of up to 64 values)
-    // times a CTA's keys; its start and the joining cost as much as about 900
-    // keys (64 ragged streams of 8 key heads, up to 4100 keys: 134 us unsplit,
-    // 197 in four; one stream: 12 us in eight, 38 in two).
-    const int64_t slots = static_cast<int64_t>(sms) * (p.d <= 64 ? 2 : 1);
-    int split = 1;
-    int64_t best = INT64_MAX;
+  const bool bf16 = precision == OIDNX_PRECISION_BF16;
+  const int64_t rows = static_cast<int64_t>(p.tq) * group, row_tiles = (rows + 31) / 32, heads = static_cast<int64_t>(p.b) * p.hk;
+  const int64_t units = heads * row_tiles;
+  // Keys that a tile of some queries sees, at most and on average.
+  const auto keys = [&](int64_t queries, bool mean) {
+    const double all = mean ? p.cap - std::min(p.tq, p.cap) / 2.0 : p.cap;
+    return p.window > 0 ? std::min(all, static_cast<double>(p.window) + p.held_sinks + queries) : all;
+  };
+
+  // Few queries: rounds of resident CTAs times a CTA's keys (9 ns each with 16
+  // rows, 12.6 with 32), plus its start and the joining, 6 us and 9 (10 and 13
+  // where rounds follow one another and share the memory).  Measured,
+  // us: 16 rows of one head over 8192 keys 17.3 in eight parts, 2300 keys 10.6;
+  // 32 rows 24.4 and 15; 128 tiles of 32 rows over 2300 keys, unsplit, 40; 64
+  // ragged single tokens of 8 heads, up to 4100 keys, unsplit 134, in four 197.
+  double token_cost = INFINITY;
+  int split = 1;
+  if (pieces && row_tiles <= 65535 && units < (1 << 27)) {
+    const double key = rows <= 16 ? 9.1 : 12.6, start = rows <= 16 ? 6000 : 9000;
+    const double seen = keys((31 + group) / group, units > sms);
     for (int s = 1; s <= 8; s *= 2) {
-      const int64_t cost = (units * s + slots - 1) / slots * (keys / s + 900);
-      if (cost < best) best = cost, split = s;
+      const int slots = attn_token_slots(p, bf16, s, device);
+      if (slots <= 0) continue;
+      const double rounds = std::ceil(static_cast<double>(units) * s / slots);
+      const double cost = rounds * (seen / s * key + start + (rounds > 1 ? 4000 : 0));
+      if (cost < token_cost) token_cost = cost, split = s;
     }
-    return launch_attn_token(p, precision == OIDNX_PRECISION_BF16, split, device, stream);
   }
   bool tiles = pieces && group <= 128 && p.scale > 0.f && p.cap > 0;
-  for (int i = 0; i < 3; ++i)
-    for (const int64_t s : {p.q_s[i], p.k_s[i], p.v_s[i], p.o_s[i]}) tiles = tiles && s > 0 && s < (int64_t(1) << 38);
-  const int per = 128 / group;  // queries of a row tile
+  const int64_t far = int64_t(1) << 38;
+  for (int i = 0; i < 3; ++i) {
+    tiles = tiles && p.q_s[i] > 0 && p.q_s[i] < far && p.o_s[i] > 0 && p.o_s[i] < far;
+    // keys and values may be shared by sequences and heads (stride 0)
+    for (const int64_t s : {p.k_s[i], p.v_s[i]}) tiles = tiles && s < far && (i == 1 ? s > 0 : s >= 0);
+  }
+  const int per = group <= 128 ? 128 / group : 1;  // queries of a row tile
   const int64_t grid = (static_cast<int64_t>(p.tq) + 2 * per - 1) / (2 * per) * p.b * p.hk;
+  // Many queries: a key tile of 128 takes a CTA 1.4 us with one row tile, 1.95
+  // with two (2300 keys, us: 29.4 and 41; 8192: 90 and 131), its ends 5; the
+  // longest CTA or the mean over the SMs, whichever is more.
+  const double tile = p.tq <= per ? 1360 : 1950;
+  const double longest = std::ceil(keys(2 * per, false) / 128 + 1) * tile;
+  const double prompt_cost =
+      5000 + std::max(longest, std::ceil(static_cast<double>(grid) / sms) * std::ceil(keys(2 * per, true) / 128 + 1) * tile);
+  if (token_cost < INFINITY && (!tiles || grid > INT_MAX || token_cost <= prompt_cost))
+    return launch_attn_token(p, bf16, split, device, stream);
   if (tiles && grid <= INT_MAX) {
+    // a shared dimension has one element, which the kernel reads for all
+    const auto cache_map = [&](CUtensorMap* map, const void* base, const int64_t* s) {
+      return heads_map(map, bf16, base, p.d, p.cap, s[1], s[2] ? p.hk : 1, s[2] ? s[2] : any, s[0] ? p.b : 1,
+                       s[0] ? s[0] : any, 128, 1);
+    };
     AttnLaunch L = {};
     L.p = p, L.device = device, L.grid = static_cast<unsigned>(grid);
-    const bool bf16 = precision == OIDNX_PRECISION_BF16;
     if (heads_map(&L.map_q, bf16, p.q, p.d, p.hq, p.q_s[2], p.tq, p.q_s[1], p.b, p.q_s[0], group, per) &&
         heads_map(&L.map_o, bf16, p.o, p.d, p.hq, p.o_s[2], p.tq, p.o_s[1], p.b, p.o_s[0], group, per) &&
-        heads_map(&L.map_k, bf16, p.k, p.d, p.cap, p.k_s[1], p.hk, p.k_s[2], p.b, p.k_s[0], 128, 1) &&
-        heads_map(&L.map_v, bf16, p.v, p.d, p.cap, p.v_s[1], p.hk, p.v_s[2], p.b, p.v_s[0], 128, 1))
+        cache_map(&L.map_k, p.k, p.k_s) && cache_map(&L.map_v, p.v, p.v_s))
       return launch_attn_prompt(L, bf16, stream);
   }
   return launch_attn_any(p, precision, device, stream);
@@ -383,6 +416,30 @@ cudaError_t oidnx::Kernel::find(const void* kernel, int smem, int device, CUfunc
   fn[device].store(found, std::memory_order_release);
   *f = found;
   return cudaSuccess;
+}
+
+int oidnx::Kernel::count_clusters(const void* kernel, int device, int threads, int smem, int cluster) {
+  const int at = cluster == 1 ? 0 : cluster == 2 ? 1 : cluster == 4 ? 2 : 3;
+  int n = held[at][device].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  CUfunction f = fn[device].load(std::memory_order_acquire);
+  if (!f && find(kernel, smem, device, &f) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeClusterDimension;
+  a[0].val.clusterDim.x = cluster;
+  a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  held[at][device].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 // Each kernel may start its prologue under the one before it in the stream

@@ -352,6 +352,25 @@ def test_attention_keys_that_are_no_numbers(tq):
                   (UNIT["fp16"] * np.abs(ref) + TINY["fp16"] * 600 + (2 * UNIT["fp16"] + 2.0 ** -14) * mag)[0][~sees])
 
 
+@pytest.mark.parametrize("tq", [1, 90])
+def test_attention_shared_keys_and_strides_of_single_elements(tq):
+    """Keys and values broadcast over sequences and heads; dimensions of one element with strides that mean nothing."""
+    q = strided((3, tq, 4, 64), "bf16", 1)
+    k, v = (strided((1, 200, 1, 64), "bf16", i).expand(3, 200, 2, 64) for i in (2, 3))
+    o, lse = torch.empty_like(q), torch.empty(3, 4, tq, device="cuda")
+    attention(q, k, v, o, lse, None, None, 40, 2, 0.125, "bf16")
+    done()
+    ref, ref_lse, mag, dots = tokens.window_attention(f64(q), f64(k), f64(v), [tq] * 3, [200] * 3, 40, 2, 0.125)
+    assert_within(f64(o), ref, UNIT["bf16"] * np.abs(ref) + (2 * UNIT["bf16"] + 2.0 ** -14) * mag)
+    q1, k1, v1 = q[:1, :, :1], k[:1, :, :1].contiguous(), v[:1, :, :1].contiguous()
+    o1 = torch.zeros(1, tq, 1, 64, dtype=torch.bfloat16, device="cuda")
+    ox.oidnx_window_attention(q1.data_ptr(), 3, q1.stride(1), 5, k1.data_ptr(), 0, k1.stride(1), 1, v1.data_ptr(), -7,
+                              v1.stride(1), 9, o1.data_ptr(), 11, o1.stride(1), 13, 0, 0, 0, 1, tq, 200, 1, 1, 64, 40, 2,
+                              0.125, ox.PRECISION_BF16, torch.cuda.current_stream().cuda_stream)
+    done()
+    assert_within(f64(o1), ref[:1, :, :1], (UNIT["bf16"] * np.abs(ref) + (2 * UNIT["bf16"] + 2.0 ** -14) * mag)[:1, :, :1])
+
+
 def test_attention_many_sequences_of_single_tokens():
     rng = np.random.default_rng(4)
     check_attention(90, 1, 260, 8, 2, 128, 100, 4, "bf16", kv_lens=rng.integers(0, 600, 90), seed=6)
@@ -398,23 +417,27 @@ def test_results_do_not_depend_on_the_stream_or_on_what_ran_before():
 
 def test_calls_can_be_captured_into_a_graph():
     x, w = strided((9, 256), "bf16", 1), strided((256, 256), "bf16", 2)
+    xo, wo = strided((200, 255), "bf16", 5), strided((64, 255), "bf16", 6)  # laid out anew in memory of the call
+    yo = torch.empty(200, 64, dtype=torch.bfloat16, device="cuda")
     q, k = strided((1, 1, 8, 64), "bf16", 3), strided((1, 900, 2, 64), "bf16", 4)
     y, o = torch.empty(9, 256, dtype=torch.bfloat16, device="cuda"), torch.empty_like(q)
 
     def step():
         linear(x, w, None, None, y, "silu", "bf16")
+        linear(xo, wo, None, None, yo, "none", "bf16")
         attention(q, k, k, o, None, None, None, 300, 4, 0.125, "bf16")
 
     step()
     done()
-    ref = [y.clone(), o.clone()]
+    ref = [y.clone(), o.clone(), yo.clone()]
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         step()
-    y.zero_(), o.zero_()
-    g.replay()
+    y.zero_(), o.zero_(), yo.zero_()
+    for _ in range(3):
+        g.replay()
     torch.cuda.synchronize()
-    assert torch.equal(y, ref[0]) and torch.equal(o, ref[1])
+    assert torch.equal(y, ref[0]) and torch.equal(o, ref[1]) and torch.equal(yo, ref[2])
 
 
 def test_calls_from_a_thread_of_its_own():
