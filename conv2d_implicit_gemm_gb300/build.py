@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "liboidnx.so")
 CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["oidnx_host.cpp", "conv_tc.cu", "conv_pair.cu", "conv_final.cu", "conv_tail.cu",
            "conv_head.cu", "io_passes.cu", "noalloc.cu", "token_host.cpp", "linear_tc.cu", "linear_split.cu", "linear_align.cu",
-           "qk_norm_rope.cu", "attn_any.cu", "attn_token.cu", "attn_prompt.cu"]
+           "qk_norm_rope.cu", "attn_any.cu", "attn_token.cu", "attn_prompt.cu", "attn_prompt64.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

@@ -211,7 +211,8 @@ struct AttnLaunch {
   int device;
   unsigned grid;
 };
-cudaError_t launch_attn_prompt(const AttnLaunch& L, bool bf16, cudaStream_t stream);
+cudaError_t launch_attn_prompt(const AttnLaunch& L, bool bf16, cudaStream_t stream);    // heads of over 64 values
+cudaError_t launch_attn_prompt64(const AttnLaunch& L, bool bf16, cudaStream_t stream);  // of up to 64
 cudaError_t launch_attn_any(const AttnParams& p, int precision, int device, cudaStream_t stream);
 
 }  // namespace oidnx

@@ -269,7 +269,7 @@ cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
     if (heads_map(&L.map_q, bf16, p.q, p.d, p.hq, p.q_s[2], p.tq, p.q_s[1], p.b, p.q_s[0], group, per) &&
         heads_map(&L.map_o, bf16, p.o, p.d, p.hq, p.o_s[2], p.tq, p.o_s[1], p.b, p.o_s[0], group, per) &&
         cache_map(&L.map_k, p.k, p.k_s) && cache_map(&L.map_v, p.v, p.v_s))
-      return launch_attn_prompt(L, bf16, stream);
+      return p.d <= 64 ? launch_attn_prompt64(L, bf16, stream) : launch_attn_prompt(L, bf16, stream);
   }
   return launch_attn_any(p, precision, device, stream);
 }
