@@ -221,16 +221,18 @@ cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
     return p.window > 0 ? std::min(all, static_cast<double>(p.window) + p.held_sinks + queries) : all;
   };
 
-  // Few queries: rounds of resident CTAs times a CTA's keys (9 ns each with 16
-  // rows, 12.6 with 32), plus its start and the joining, 6 us and 9 (10 and 13
-  // where rounds follow one another and share the memory).  Measured,
-  // us: 16 rows of one head over 8192 keys 17.3 in eight parts, 2300 keys 10.6;
-  // 32 rows 24.4 and 15; 128 tiles of 32 rows over 2300 keys, unsplit, 40; 64
-  // ragged single tokens of 8 heads, up to 4100 keys, unsplit 134, in four 197.
+  // Few queries: rounds of resident CTAs times a CTA's keys, plus its start and
+  // the joining, 4 us more where rounds follow one another and share the memory.
+  // Measured, us, one head of 128 values in eight parts: 16 rows over 600, 2300
+  // and 8192 keys 8.7, 10.6, 17.3; 32 rows 12.5, 15, 24.4; of 64 values 6.1, 7.4,
+  // 11.4 and 8.9, 10.5, 16.4.  64 ragged single tokens of 8 heads, up to 4100
+  // keys: unsplit 134, in four 197.
   double token_cost = INFINITY;
   int split = 1;
   if (pieces && row_tiles <= 65535 && units < (1 << 27)) {
-    const double key = rows <= 16 ? 9.1 : 12.6, start = rows <= 16 ? 6000 : 9000;
+    const bool few = rows <= 16, small = p.d <= 64;
+    const double key = few ? (small ? 5.6 : 9.1) : small ? 7.9 : 12.6;
+    const double start = few ? (small ? 4000 : 6000) : small ? 6500 : 10000;
     const double seen = keys((31 + group) / group, units > sms);
     for (int s = 1; s <= 8; s *= 2) {
       const int slots = attn_token_slots(p, bf16, s, device);
@@ -249,14 +251,19 @@ cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
   }
   const int per = group <= 128 ? 128 / group : 1;  // queries of a row tile
   const int64_t grid = (static_cast<int64_t>(p.tq) + 2 * per - 1) / (2 * per) * p.b * p.hk;
-  // Many queries: a key tile of 128 takes a CTA 1.4 us with one row tile, 1.95
-  // with two (2300 keys, us: 29.4 and 41; 8192: 90 and 131), its ends 5; the
-  // longest CTA or the mean over the SMs, whichever is more.
-  const double tile = p.tq <= per ? 1360 : 1950;
-  const double longest = std::ceil(keys(2 * per, false) / 128 + 1) * tile;
-  const double prompt_cost =
-      5000 + std::max(longest, std::ceil(static_cast<double>(grid) / sms) * std::ceil(keys(2 * per, true) / 128 + 1) * tile);
-  if (token_cost < INFINITY && (!tiles || grid > INT_MAX || token_cost <= prompt_cost))
+  // Many queries: key tiles of 128, with one row tile and two, us: heads of 128
+  // values 1.36 and 1.95 (8192 keys 90 and 131), of 64 1.0 and 1.2 (66 and 80);
+  // 4 for a CTA's ends.  The longest CTA or the mean over the SMs, whichever is
+  // more.
+  const bool one = p.tq <= per;
+  const double tile = p.d <= 64 ? (one ? 1000 : 1200) : one ? 1360 : 1950;
+  const int extra = p.window > 0 ? 1 : 0;
+  const double longest = (std::ceil(keys(2 * per, false) / 128) + extra) * tile;
+  const double mean = (std::ceil(keys(2 * per, true) / 128) + extra) * tile;
+  const double prompt_cost = 4000 + std::max(longest, std::ceil(static_cast<double>(grid) / sms) * mean);
+  // (a row tile of 128 with 16 rows or fewer has to win clearly: lengths are
+  // upper bounds, and short sequences free a CTA of few queries sooner)
+  if (token_cost < INFINITY && (!tiles || grid > INT_MAX || token_cost * (rows <= 16 ? 0.8 : 1.0) <= prompt_cost))
     return launch_attn_token(p, bf16, split, device, stream);
   if (tiles && grid <= INT_MAX) {
     // a shared dimension has one element, which the kernel reads for all
