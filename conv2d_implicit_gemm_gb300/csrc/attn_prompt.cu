@@ -23,6 +23,14 @@
 //    keys, and where a key itself holds such a value the CTA's rows are done
 //    again one by one.
 //
+// Bound by the latency of a row tile's chain (scores, softmax, products, the next
+// scores: some 3000 cycles for 128 keys, of which the products take 1024), two
+// of which are in flight: tensor memory has no room for a third with 128 output
+// values a row.  8192 tokens, window 2048, 16 heads of 128 over 4: 128 us, 943
+// TFLOP/s of visible pairs, the tensor pipe active 42% of the time.  Sixteen
+// softmax warps (two threads a row, exchanging maxima) took 141 us, one product
+// warp for both row tiles 135.
+//
 // Warps 0-3 and 4-7: softmax of row tile 0 and 1, rescaling, output; warp 8
 // loads (TMA), warps 9 and 10 issue the products of a row tile each (one thread
 // for both was the bound), warp 11 looks values over.

@@ -7,7 +7,9 @@
 // took as long per key tile as heads of 128 with twice the products.  Here
 // tensor memory has room for a chain per row tile and half of each key tile: 64
 // columns of scores and 64 of output each.  The halves of a row keep their own
-// maximum, sum and output and are joined at the end.
+// maximum, sum and output and are joined at the end.  2 x 4096 causal, 8 heads of
+// 64: 46 us (two chains: 54), 740 TFLOP/s of visible pairs; the longest CTA's 32
+// key tiles are what remains.
 //
 // Warps 4 c .. 4 c + 3: softmax of chain c = 2 (row tile) + (half of the keys),
 // one thread a row; warp 16 loads, 17 and 18 issue the products of a row tile's

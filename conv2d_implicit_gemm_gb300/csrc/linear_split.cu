@@ -6,6 +6,10 @@
 // 128 x BN tile in its shared memory; after a cluster barrier every CTA sums
 // 128 / split rows over the parts (always in the same order) and applies the
 // epilogue.
+//
+// 1 x 4096 x 4096: 9.7 us on the device (3.9 of them at any size: launch, first
+// loads, joining; the rest streams the weight at 5.8 TB/s); 1 x 8192 x 8192: 24 us,
+// 5.6 TB/s.  Rows that do not start on 16 bytes: 15.4 us for 1 x 4096 x 4095.
 #include <type_traits>
 
 #include "linear_load.cuh"

@@ -15,6 +15,9 @@
 //    single values, coalesced along the row.
 //  * The MMA warp overwrites the accumulator with its first product and adds
 //    the others; products outside the matrix are zeros that TMA fills in.
+// 8192 x 8192 x 4096, bf16, gelu_tanh: 295 us alone (1865 TFLOP/s, the tensor pipe
+// active 90% of the time), 315 to 343 among others, where the power limit lowers
+// the clock (the measured library rates are 1898 in a burst and 1702 sustained).
 //  * Every wait is bounded.  A role that gives up records it and leaves its
 //    loop; its own loads were issued before that wait of two seconds and have
 //    landed, and the other roles give up in turn, so the block ends together.

@@ -5,7 +5,10 @@
 //   pairs (a, b) of the first rot values: (a c - b s, b c + a s)
 //
 // with c, s the table rows of the token's position.  Each value is read and
-// written once, so the bound is memory; everything between is fp32.
+// written once, so the bound is memory; everything between is fp32.  16384 tokens
+// x 48 heads x 128 in bf16: 90 us, 4.6 TB/s, 68% of the measured copy rate: with
+// 78 registers 24 warps an SM do not quite cover the rotation's and the sums'
+// latency (issue slots 49% busy).  One token: 2.2 us on the device.
 #include <algorithm>
 #include <climits>
 #include <type_traits>

@@ -351,7 +351,10 @@ void oidnx_conv_release(oidnx_conv* c);
  * no counterpart of these calls; they are an addition of this library.
  *
  * For all of them: direct calls on device pointers, enqueued on `stream`;
- * nothing is allocated, and nothing is kept from one call for the next.
+ * nothing is kept from one call for the next.  Nothing is allocated either,
+ * but for linear layers of over 32 rows whose x or w has rows that do not start
+ * on 16 bytes: these take memory for copies with rows that do, ordered on the
+ * stream, from a pool of the library's own that keeps it for later calls.
  * Strides and row lengths count elements.  Pointers need the alignment of
  * their elements only; 16-byte aligned pointers and strides of whole 16
  * bytes run the fast forms.  Sums, norms and softmax statistics are fp32 and
@@ -373,7 +376,7 @@ enum { OIDNX_ACT_NONE = 0, OIDNX_ACT_RELU = 1, OIDNX_ACT_GELU = 2 /* erf */,
  * act(bias) + residual.
  * Errors: INVALID_ARGUMENT (NULL, negative sizes, strides shorter than
  * rows, misaligned pointers, unknown act or precision), UNSUPPORTED (fp32),
- * CUDA.  */
+ * OUT_OF_MEMORY, CUDA.  */
 oidnx_status oidnx_linear(const void* x, long long ldx, const void* w, long long ldw, const void* bias,
                           const void* residual, long long ldr, void* y, long long ldy, int m, int n,
                           int k, int act, int precision, void* stream);
@@ -420,7 +423,7 @@ oidnx_status oidnx_qk_norm_rope(const void* q, long long q_st, long long q_sh, v
  * the d values of a head are contiguous.  lse (fp32 [b][hq][tq]) may be NULL;
  * q_lens and kv_lens are device arrays.  o overlaps no input.
  * precision: OIDNX_PRECISION_FP16 or _BF16.  d <= 256; heads of up to 128
- * values in whole 16-byte pieces run on the tensor cores.
+ * values in whole 16-byte pieces run on the tensor cores, others a warp a row.
  * Errors: INVALID_ARGUMENT (NULL, sizes, hq not a multiple of hk, scale,
  * misaligned pointers, unknown precision), UNSUPPORTED (fp32, d > 256, over
  * 4e9 query heads), CUDA.  */
