@@ -43,25 +43,22 @@ constexpr int kSoftWarps = 8;
 constexpr int kThreads = (kSoftWarps + 4) * 32;
 constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kLookWarp = kSoftWarps + 3;
 
-template <int DB> struct Pr {  // DB: 64-value blocks of a head (1 or 2)
-  static constexpr int kTile = DB * 16384;  // 128 rows
-  static constexpr int kStages = DB == 2 ? 2 : 4;
-  static constexpr int kSmem = (2 + 2 * kStages) * kTile + 1024 + 512;
-};
+constexpr int DB = 2;              // 64-value blocks of a head
+constexpr int kTile = DB * 16384;  // 128 rows
+constexpr int NS = 2;              // key tiles (and value tiles) in flight
+constexpr int kSmem = (2 + 2 * NS) * kTile + 1024 + 512;
 
-template <typename T, int DB>
+template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
                        const AttnParams p) {
-  using C = Pr<DB>;
-  constexpr int NS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* Q = smem_raw + pad;  // [2 row tiles]; the output tiles at the end
-  uint8_t* Ks = Q + 2 * C::kTile;
-  uint8_t* Vs = Ks + NS * C::kTile;
-  uint64_t* qfull = reinterpret_cast<uint64_t*>(Vs + NS * C::kTile);  // [2]
+  uint8_t* Ks = Q + 2 * kTile;
+  uint8_t* Vs = Ks + NS * kTile;
+  uint64_t* qfull = reinterpret_cast<uint64_t*>(Vs + NS * kTile);  // [2]
   uint64_t* kfull = qfull + 2;    // [NS]
   uint64_t* kempty = kfull + NS;
   uint64_t* vfull = kempty + NS;
@@ -116,25 +113,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = j % NS, ph = (j / NS) & 1;
           ok = mbar_wait_soon(&kempty[s], ph ^ 1, p.status, kErrTimeoutProducer);
           if (!ok) break;
-          mbar_arrive_expect_tx(&kfull[s], C::kTile);
+          mbar_arrive_expect_tx(&kfull[s], kTile);
 #pragma unroll
           for (int d = 0; d < DB; ++d)
-            tma_load_4d(Ks + s * C::kTile + d * 16384, &map_k, &kfull[s], d * 64, k.slot, p.k_s[2] ? w.kvh : 0, p.k_s[0] ? w.b : 0, pol);
+            tma_load_4d(Ks + s * kTile + d * 16384, &map_k, &kfull[s], d * 64, k.slot, p.k_s[2] ? w.kvh : 0, p.k_s[0] ? w.b : 0, pol);
           if (j == 0) {
             for (int t = 0; t < 2; ++t) {
               if (!w.active(t)) continue;
               mbar_arrive_expect_tx(&qfull[t], DB * q_bytes);
 #pragma unroll
               for (int d = 0; d < DB; ++d)
-                tma_load_4d(Q + t * C::kTile + d * 16384, &map_q, &qfull[t], d * 64, w.kvh * w.group, w.i0(t), w.b, pol);
+                tma_load_4d(Q + t * kTile + d * 16384, &map_q, &qfull[t], d * 64, w.kvh * w.group, w.i0(t), w.b, pol);
             }
           }
           ok = mbar_wait_soon(&vempty[s], ph ^ 1, p.status, kErrTimeoutProducer);
           if (!ok) break;
-          mbar_arrive_expect_tx(&vfull[s], C::kTile);
+          mbar_arrive_expect_tx(&vfull[s], kTile);
 #pragma unroll
           for (int d = 0; d < DB; ++d)
-            tma_load_4d(Vs + s * C::kTile + d * 16384, &map_v, &vfull[s], d * 64, k.slot, p.v_s[2] ? w.kvh : 0, p.v_s[0] ? w.b : 0, pol);
+            tma_load_4d(Vs + s * kTile + d * 16384, &map_v, &vfull[s], d * 64, k.slot, p.v_s[2] ? w.kvh : 0, p.v_s[0] ? w.b : 0, pol);
         }
       }
     } else if (warp < kLookWarp) {
@@ -147,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) {
         constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
         const uint32_t id_s = idesc_16(bf, 128, kTileKeys), id_pv = idesc_16(bf, 128, kd * 16, true);
-        const uint64_t qd = smem_desc_sw128(smem_u32(Q + t * C::kTile));
+        const uint64_t qd = smem_desc_sw128(smem_u32(Q + t * kTile));
         const uint64_t kd0 = smem_desc_sw128(smem_u32(Ks)), vd0 = value_desc(smem_u32(Vs));
         const uint32_t s_at = s_col(t), o_at = o_col(t);
         int n = 0;
@@ -194,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (ok && j + 1 < w.tiles) ok = mbar_wait_soon(&kfull[s1], ph1, p.status, kErrTimeoutMma);
           if (see) {
-            const uint64_t vt = vd0 + s * (C::kTile >> 4);
+            const uint64_t vt = vd0 + s * (kTile >> 4);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               if (ok) ok = mbar_wait_soon(&pfull[2 * t + h], n & 1, p.status, kErrTimeoutMma);
@@ -208,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
           if (see1) {
-            score(kd0 + s1 * (C::kTile >> 4), count1);
+            score(kd0 + s1 * (kTile >> 4), count1);
           } else if (j + 1 < w.tiles) {
             mma_commit(&vempty[s]);
             mbar_arrive(&kempty[s1]);
@@ -229,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&vempty[s]);
           continue;
         }
-        if (look_over<T, DB>(Vs + s * C::kTile, k.count, lane)) *odd = 1;
+        if (look_over<T, DB>(Vs + s * kTile, k.count, lane)) *odd = 1;
         fence_proxy_async_smem();
         mbar_arrive(&vclean[s]);
         __syncwarp();
@@ -349,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // output: through the row tile's query tile, which no product reads any more
     const bool some = valid && n > 0 && !(sum == 0.f);
     const float inv = some ? 1.f / sum : 0.f;
-    uint8_t* out = Q + t * C::kTile;
+    uint8_t* out = Q + t * kTile;
 #pragma unroll 1
     for (int x = 0; x < DB * 64; x += 32) {
       if (x >= p.d) break;
@@ -379,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int d = 0; d < DB; ++d)
         if (d * 64 < p.d) tma_store_4d(&map_o, out + d * 16384, d * 64, w.kvh * w.group, w.i0(t), w.b);
       bulk_commit();
-      bulk_wait_all();
+      bulk_wait_read<0>();  // the tile must outlive the store's reads
     }
   }
 
@@ -391,7 +388,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
   if (*odd) {
-    // a key's value is no number: every row again, on its own
+    // a key's value is no number: every row again, on its own, over what the
+    // stores have written
+    bulk_wait_all();
+    __syncthreads();
     for (int r = warp; r < 2 * w.per * w.group; r += kThreads / 32) {
       const int i = w.i00 + r / w.group;
       if (i < p.tq) attend_row<T, 2 * DB>(p, w.b, i, w.kvh * w.group + r % w.group, lane);
@@ -399,19 +399,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename T, int DB>
-cudaError_t launch(const AttnLaunch& L, cudaStream_t stream) {
-  auto kernel = attn_prompt_kernel<T, DB>;
+template <typename T> cudaError_t launch(const AttnLaunch& L, cudaStream_t stream) {
   static Kernel handle;
-  return handle.launch(kernel, L.device, dim3(L.grid), kThreads, Pr<DB>::kSmem, 1, stream, L.map_q, L.map_k, L.map_v,
-                       L.map_o, L.p);
+  return handle.launch(attn_prompt_kernel<T>, L.device, dim3(L.grid), kThreads, kSmem, 1, stream, L.map_q, L.map_k,
+                       L.map_v, L.map_o, L.p);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_prompt(const AttnLaunch& L, bool bf16, cudaStream_t stream) {
-  if (L.p.d <= 64) return bf16 ? launch<__nv_bfloat16, 1>(L, stream) : launch<__half, 1>(L, stream);
-  return bf16 ? launch<__nv_bfloat16, 2>(L, stream) : launch<__half, 2>(L, stream);
+  return bf16 ? launch<__nv_bfloat16>(L, stream) : launch<__half>(L, stream);
 }
 
 }  // namespace oidnx

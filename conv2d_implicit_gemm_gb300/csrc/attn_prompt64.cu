@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (r == 0 && h == 0 && w.i0(t) < p.tq) {
       tma_store_4d(&map_o, out, 0, w.kvh * w.group, w.i0(t), w.b);
       bulk_commit();
-      bulk_wait_all();
+      bulk_wait_read<0>();  // the tile must outlive the store's reads
     }
   }
 
@@ -359,7 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
   if (*odd) {
-    // a key's value is no number: every row again, on its own
+    // a key's value is no number: every row again, on its own, over what the
+    // stores have written
+    bulk_wait_all();
+    __syncthreads();
     for (int r = warp; r < 2 * w.per * w.group; r += kThreads / 32) {
       const int i = w.i00 + r / w.group;
       if (i < p.tq) attend_row<T, 2>(p, w.b, i, w.kvh * w.group + r % w.group, lane);

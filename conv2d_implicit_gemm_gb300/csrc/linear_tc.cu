@@ -311,8 +311,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       tile_of(a, t, &tm, &tn);
       const int r0 = (tm * CG + static_cast<int>(rank)) * 128 + quarter * 32;
       const int c0 = tn * BN + half * (BN / 2);
-      if (a.tma_out && lane == 0 && r0 < p.m && c0 < p.n)
-        fetch_residual<BN / 2 < 64 ? BN / 2 : 64>(p, &map_r, stage, &rbar[e], r0, c0);
+      // the epilogue's reads on their way while the products run
+      if (r0 < p.m && c0 < p.n) {
+        if (a.tma_out && lane == 0)
+          fetch_residual<BN / 2 < 64 ? BN / 2 : 64>(p, &map_r, stage, &rbar[e], r0, c0);
+        if (p.bias && lane < BN / 2 / 32) prefetch_l1(static_cast<const T*>(p.bias) + min(c0 + lane * 32, p.n - 1));
+        if (p.residual && !a.tma_out && r0 + lane < p.m) {
+          const T* row = static_cast<const T*>(p.residual) + (r0 + lane) * p.ldr;
+          prefetch_l1(row + c0);
+          prefetch_l1(row + min(c0 + 63, p.n - 1));
+        }
+      }
       __syncwarp();
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[b], (n >> 1) & 1, p.status, kErrTimeoutEpilogue))) break;
       tc_fence_after();

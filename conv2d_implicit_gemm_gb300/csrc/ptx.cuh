@@ -421,20 +421,6 @@ __device__ __forceinline__ void split_tf32(uint4* hi, uint4* lo) {
   *hi = h;
 }
 
-// The barrier, and whether `v` holds in all of its threads.
-__device__ __forceinline__ bool named_barrier_all(int id, int threads, bool v) {
-  int r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.s32 p, %3, 0;\n\t"
-      "bar.red.and.pred q, %1, %2, p;\n\t"
-      "selp.s32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"(static_cast<int>(v))
-      : "memory");
-  return r != 0;
-}
-
 __device__ __forceinline__ void named_barrier_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -508,6 +494,10 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
           smem_u32(bar)),
       "h"(static_cast<uint16_t>(3))
       : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p) : "memory");
 }
 
 // ---------------------------------------------------------------- TMA stores

@@ -183,7 +183,7 @@ __device__ __forceinline__ int attn_q_len(const AttnParams& p, int b) {
 }
 __device__ __forceinline__ int attn_kv_len(const AttnParams& p, int b) {
   const int n = p.kv_lens ? p.kv_lens[b] : p.cap;
-  return n < 0 ? 0 : n;
+  return n < 0 ? 0 : min(n, 1 << 30);
 }
 // First position after the sinks whose key the cache still holds when n keys
 // have been written: the ring keeps the last cap - held_sinks of them.

@@ -50,6 +50,8 @@ template <typename F> F driver_call(const char* name) {
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+constexpr int kMost = 1 << 30;  // of a size, so that sums of a few of them stay within 32 bits
+
 // ---------------------------------------------------------------- tensor maps
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -95,6 +97,8 @@ cudaError_t scratch_pool(int device, cudaMemPool_t* out) {
   *out = pools[device];
   return cudaSuccess;
 }
+
+constexpr int kMostSplit = 65535 * 32;  // rows of a grid of the split form's gathering tiles
 
 // Few rows: K split over clusters, tokens as the narrow operand.
 cudaError_t run_split(LinearTcLaunch& L, bool bf16, cudaStream_t stream) {
@@ -152,6 +156,17 @@ cudaError_t run_linear(const LinearParams& params, bool bf16, cudaStream_t strea
   // 3501: 15 us, laid out anew first: 22); from 33 rows on, with one gathering
   // CTA an SM, its copying bounds it (64 rows: 34 and 26).  k = 0 has nothing to
   // fetch, which the gathering form's cleared blocks serve.
+  if (p.k == 0 && p.m > kMostSplit) {
+    for (int i = 0; i < params.m; i += kMostSplit) {  // rows of one grid at a time
+      LinearParams part = params;
+      part.m = std::min(kMostSplit, params.m - i);
+      part.residual = params.residual ? static_cast<const uint8_t*>(params.residual) + 2 * i * params.ldr : nullptr;
+      part.y = static_cast<uint8_t*>(params.y) + 2 * i * params.ldy;
+      e = run_linear(part, bf16, stream);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+  }
   if (p.m <= 32 || p.k == 0 || (p.m <= 128 && x_fits && w_fits)) return run_split(L, bf16, stream);
   if (x_fits && w_fits) return run_tiles(L, bf16, stream);
   const int64_t ld = (static_cast<int64_t>(p.k) + 7) / 8 * 8;
@@ -294,6 +309,7 @@ oidnx_status oidnx_linear(const void* x, long long ldx, const void* w, long long
   if (precision == OIDNX_PRECISION_FP32) return fail(OIDNX_ERR_UNSUPPORTED, "linear: fp16 or bf16 only");
   if (precision != OIDNX_PRECISION_FP16 && precision != OIDNX_PRECISION_BF16)
     return fail(OIDNX_ERR_INVALID_ARGUMENT, "linear: unknown precision %d", precision);
+  if (m > kMost || n > kMost || k > kMost) return fail(OIDNX_ERR_UNSUPPORTED, "linear: a size beyond 2^30");
   if (m == 0 || n == 0) return finish(cudaSuccess, "linear");
   if (!y || (k > 0 && (!x || !w))) return fail(OIDNX_ERR_INVALID_ARGUMENT, "linear: NULL x, w or y");
   if (ldx < k || ldw < k || ldy < n || (residual && ldr < n))
@@ -319,6 +335,7 @@ oidnx_status oidnx_qk_norm_rope(const void* q, long long q_st, long long q_sh, v
   if (t < 0 || hq < 0 || hk < 0 || d <= 0 || rot < 0 || rot > d || rot % 2)
     return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: bad sizes (t %d, heads %d and %d, d %d, rot %d)", t, hq, hk,
                 d, rot);
+  if (t > kMost) return fail(OIDNX_ERR_UNSUPPORTED, "qk_norm_rope: more than 2^30 tokens");
   if (hq > 65536 || hk > 65536) return fail(OIDNX_ERR_UNSUPPORTED, "qk_norm_rope: more than 65536 heads");
   if (!(eps >= 0.f) || std::isinf(eps)) return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: bad eps");
   if (t == 0 || (hq == 0 && hk == 0)) return finish(cudaSuccess, "qk_norm_rope");
@@ -382,6 +399,7 @@ oidnx_status oidnx_window_attention(const void* q, long long q_sb, long long q_s
     return fail(OIDNX_ERR_INVALID_ARGUMENT,
                 "window_attention: bad sizes (b %d, tq %d, cap %d, heads %d and %d, d %d, window %d, sinks %d)", b, tq,
                 cap, hq, hk, d, window, sinks);
+  if (tq > kMost || cap > kMost) return fail(OIDNX_ERR_UNSUPPORTED, "window_attention: a length beyond 2^30");
   if (d > 256) return fail(OIDNX_ERR_UNSUPPORTED, "window_attention: heads of more than 256 values (%d)", d);
   if (!std::isfinite(scale)) return fail(OIDNX_ERR_INVALID_ARGUMENT, "window_attention: scale is not finite");
   if (b == 0 || tq == 0 || hq == 0) return finish(cudaSuccess, "window_attention");

@@ -362,7 +362,7 @@ void oidnx_conv_release(oidnx_conv* c);
  * the work on `stream` is done, and orders the call after whatever wrote its
  * inputs on other streams.  Calls can be captured into a CUDA graph once one
  * call has been made on the device.  A device-side timeout is reported by
- * oidnx_token_sync_status.  */
+ * oidnx_token_sync_status.  Sizes beyond 2^30 are UNSUPPORTED.  */
 
 enum { OIDNX_ACT_NONE = 0, OIDNX_ACT_RELU = 1, OIDNX_ACT_GELU = 2 /* erf */,
        OIDNX_ACT_GELU_TANH = 3, OIDNX_ACT_SILU = 4 };
@@ -421,7 +421,8 @@ oidnx_status oidnx_qk_norm_rope(const void* q, long long q_st, long long q_sh, v
  * never used, whatever they hold.  Query head h reads key head
  * h / (hq / hk).  Strides: *_sb sequence, *_st token or slot, *_sh head;
  * the d values of a head are contiguous.  lse (fp32 [b][hq][tq]) may be NULL;
- * q_lens and kv_lens are device arrays.  o overlaps no input.
+ * q_lens and kv_lens are device arrays (up to 2^30 keys; more are read as that
+ * many).  o overlaps no input.
  * precision: OIDNX_PRECISION_FP16 or _BF16.  d <= 256; heads of up to 128
  * values in whole 16-byte pieces run on the tensor cores, others a warp a row.
  * Errors: INVALID_ARGUMENT (NULL, sizes, hq not a multiple of hk, scale,

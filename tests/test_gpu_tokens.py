@@ -103,6 +103,16 @@ def test_linear_without_products_is_the_epilogue(m):
     assert_within(f64(y), ref, UNIT["fp16"] * np.abs(ref) + 2.0 ** -23 * np.abs(ref) + TINY["fp16"])
 
 
+def test_linear_without_products_of_very_many_rows():
+    m = 65535 * 32 + 70  # more than one grid
+    r = torch.randn(m, 2, device="cuda").half()
+    y = torch.empty_like(r)
+    ox.oidnx_linear(0, 0, 0, 0, 0, r.data_ptr(), 2, y.data_ptr(), 2, m, 2, 0, ox.ACT_NONE, ox.PRECISION_FP16,
+                    torch.cuda.current_stream().cuda_stream)
+    done()
+    assert torch.equal(y, r)
+
+
 @pytest.mark.parametrize("m", [4, 180])
 def test_linear_infinities_and_nan_stay_in_their_rows_and_columns(m):
     x, w = strided((m, 64), "bf16", 1), strided((80, 64), "bf16", 2)

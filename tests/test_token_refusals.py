@@ -40,7 +40,7 @@ INVALID, UNSUPPORTED = 1, 3
     (dict(y=0), INVALID), (dict(ldx=63), INVALID), (dict(ldw=63), INVALID), (dict(ldy=31), INVALID),
     (dict(residual=P, ldr=31), INVALID), (dict(act=5), INVALID), (dict(act=-1), INVALID), (dict(x=P + 1), INVALID),
     (dict(bias=P + 1), INVALID), (dict(y=P + 1), INVALID), (dict(precision=0), INVALID), (dict(precision=4), INVALID),
-    (dict(precision=1), UNSUPPORTED),
+    (dict(precision=1), UNSUPPORTED), (dict(m=2 ** 30 + 1), UNSUPPORTED), (dict(n=2 ** 30 + 1, ldy=2 ** 31), UNSUPPORTED),
 ])
 def test_linear_refuses(ox, change, status):
     with pytest.raises(ox.OidnxError) as e:
@@ -54,6 +54,7 @@ def test_linear_refuses(ox, change, status):
     (dict(v_out=P), INVALID), (dict(cos_table=0), INVALID), (dict(positions=0), INVALID), (dict(eps=-1.0), INVALID),
     (dict(eps=float("nan")), INVALID), (dict(precision=0), INVALID), (dict(precision=4), INVALID),
     (dict(q=P + 1), INVALID), (dict(positions=P + 2), INVALID), (dict(hq=70000), UNSUPPORTED),
+    (dict(t=2 ** 30 + 1), UNSUPPORTED),
 ])
 def test_norm_refuses(ox, change, status):
     with pytest.raises(ox.OidnxError) as e:
@@ -67,7 +68,7 @@ def test_norm_refuses(ox, change, status):
     (dict(scale=float("inf")), INVALID), (dict(q=0), INVALID), (dict(k=0), INVALID), (dict(v=0), INVALID),
     (dict(o=0), INVALID), (dict(k=P + 1), INVALID), (dict(lse=P + 2), INVALID), (dict(kv_lens=P + 1), INVALID),
     (dict(precision=0), INVALID), (dict(precision=1), UNSUPPORTED), (dict(d=257), UNSUPPORTED),
-    (dict(b=100000, tq=100000), UNSUPPORTED),
+    (dict(b=100000, tq=100000), UNSUPPORTED), (dict(cap=2 ** 30 + 1), UNSUPPORTED),
 ])
 def test_attention_refuses(ox, change, status):
     with pytest.raises(ox.OidnxError) as e:
@@ -84,3 +85,14 @@ def test_empty_calls_do_nothing(ox):
     _attn(ox, tq=0)
     _attn(ox, hq=0)
     assert ox.oidnx_last_error() == ""
+
+
+@pytest.mark.parametrize("count", [14, 16])
+def test_calls_count_their_arguments(ox, count):
+    with pytest.raises(TypeError):
+        ox._calls.oidnx_linear(*[0] * count)
+
+
+def test_calls_refuse_what_no_c_int_holds(ox):
+    with pytest.raises(OverflowError):
+        _linear(ox, m=2 ** 31)
