@@ -153,14 +153,30 @@ __device__ __forceinline__ bool epilogue_tma(const TcArgs& a, const CUtensorMap*
   return true;
 }
 
-// The same through single values: any row stride and alignment.
+// The residual of a 32 x 32 tile from (r0, c0) on, column c0 + lane (zeros
+// outside or without one).
+template <typename T>
+__device__ __forceinline__ void load_residual(const LinearParams& p, int r0, int c0, int lane, T (&z)[32]) {
+  const int rows = p.residual && c0 + lane < p.n ? min(32, p.m - r0) : 0;
+  const T* res = static_cast<const T*>(p.residual) + r0 * p.ldr + c0 + lane;
+#pragma unroll
+  for (int r = 0; r < 32; ++r) z[r] = r < rows ? res[r * p.ldr] : T(0.f);
+}
+
+// The same through single values: any row stride and alignment.  z: the first
+// tile's residual; each next one is loaded a tile ahead (y may be the residual,
+// so the compiler keeps a load behind every earlier store, but another tile's
+// values are not written before).
 template <typename T, int COLS>
-__device__ __forceinline__ void epilogue_any(const TcArgs& a, uint32_t tmem, int r0, int c0, uint8_t* stage, int lane) {
+__device__ __forceinline__ void epilogue_any(const TcArgs& a, uint32_t tmem, int r0, int c0, uint8_t* stage, int lane,
+                                             T (&z)[32]) {
   const LinearParams& p = a.p;
   float* tile = reinterpret_cast<float*>(stage);  // [row][column ^ row]
 #pragma unroll 1
   for (int c = 0; c < COLS; c += 32) {
     if (c0 + c >= p.n) break;
+    T next[32];
+    if (c + 32 < COLS) load_residual<T>(p, r0, c0 + c + 32, lane, next);
     uint32_t raw[32];
     tmem_ld32_nowait(tmem + c, raw);
     tmem_wait_ld();
@@ -172,22 +188,14 @@ __device__ __forceinline__ void epilogue_any(const TcArgs& a, uint32_t tmem, int
 #pragma unroll
     for (int i = 0; i < 32; ++i) tile[lane * 32 + (i ^ lane)] = v[i];
     __syncwarp();
-    const int col = c0 + c + lane, rows = min(32, p.m - r0);
-    if (col < p.n) {
-      T* y = static_cast<T*>(p.y) + r0 * p.ldy + col;
-      const T* res = static_cast<const T*>(p.residual) + r0 * p.ldr + col;
-      // all loads before the first store: y may be the residual, so the compiler
-      // keeps a load behind every earlier store
-      T z[32];
-      if (p.residual) {
+    const int col = c0 + c + lane, rows = col < p.n ? min(32, p.m - r0) : 0;
+    T* y = static_cast<T*>(p.y) + r0 * p.ldy + col;
 #pragma unroll
-        for (int r = 0; r < 32; ++r) z[r] = r < rows ? res[r * p.ldr] : T(0.f);
-      }
-#pragma unroll
-      for (int r = 0; r < 32; ++r)
-        if (r < rows) y[r * p.ldy] = from_f32<T>(tile[r * 32 + (lane ^ r)] + (p.residual ? to_f32<T>(z[r]) : 0.f));
-    }
+    for (int r = 0; r < 32; ++r)
+      if (r < rows) y[r * p.ldy] = from_f32<T>(tile[r * 32 + (lane ^ r)] + to_f32<T>(z[r]));
     __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 32; ++r) z[r] = next[r];
   }
 }
 
@@ -312,15 +320,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const int r0 = (tm * CG + static_cast<int>(rank)) * 128 + quarter * 32;
       const int c0 = tn * BN + half * (BN / 2);
       // the epilogue's reads on their way while the products run
+      T z[32];
       if (r0 < p.m && c0 < p.n) {
         if (a.tma_out && lane == 0)
           fetch_residual<BN / 2 < 64 ? BN / 2 : 64>(p, &map_r, stage, &rbar[e], r0, c0);
         if (p.bias && lane < BN / 2 / 32) prefetch_l1(static_cast<const T*>(p.bias) + min(c0 + lane * 32, p.n - 1));
-        if (p.residual && !a.tma_out && r0 + lane < p.m) {
-          const T* row = static_cast<const T*>(p.residual) + (r0 + lane) * p.ldr;
-          prefetch_l1(row + c0);
-          prefetch_l1(row + min(c0 + 63, p.n - 1));
-        }
+        if (!a.tma_out) load_residual<T>(p, r0, c0, lane, z);
       }
       __syncwarp();
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[b], (n >> 1) & 1, p.status, kErrTimeoutEpilogue))) break;
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (a.tma_out) {
           if (!epilogue_tma<T, BN / 2>(a, &map_y, &map_r, acc, r0, c0, stage, &rbar[e], &rphase, lane)) break;
         } else {
-          epilogue_any<T, BN / 2>(a, acc, r0, c0, stage, lane);
+          epilogue_any<T, BN / 2>(a, acc, r0, c0, stage, lane, z);
         }
       }
       tc_fence_before();
