@@ -264,7 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 2; e < 16; e += 2) m4[q] = max3(m4[q], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
       }
       const float m = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-      const bool rise = (m - top) * c > 8.f;
+      // (lanes without a query hold whatever shared memory held, and must not
+      // decide for the others)
+      const bool rise = valid && (m - top) * c > 8.f;
       if (__any_sync(0xFFFFFFFFu, rise)) {
         const float up = fmaxf(m, top);
         const float f = up == -INFINITY ? 1.f : exp2_fast((top - up) * c);

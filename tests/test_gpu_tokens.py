@@ -425,6 +425,26 @@ def test_results_do_not_depend_on_the_stream_or_on_what_ran_before():
         assert all(torch.equal(a, b) for a, b in zip(got, first))
 
 
+@pytest.mark.parametrize("hq,hk,d", [(6, 2, 80), (3, 1, 64), (7, 1, 128), (5, 1, 40)])
+def test_attention_bits_do_not_depend_on_what_shared_memory_held(hq, hk, d):
+    """Groups that do not fill a row tile: the same bits with other calls in between."""
+    q, k, v = strided((2, 160, hq, d), "fp16", 1), strided((2, 900, hk, d), "fp16", 2), strided((2, 900, hk, d), "fp16", 3)
+    loud = [strided((2, 200, 4, n), "fp16", 4, scale=30.0) for n in (64, 128)]
+
+    def call():
+        o, lse = torch.empty_like(q), torch.empty(2, hq, 160, device="cuda")
+        attention(q, k, v, o, lse, None, None, 400, 2, d ** -0.5, "fp16")
+        return o, lse
+
+    first = call()
+    for _ in range(10):
+        for x in loud:
+            attention(x, x, x, torch.empty_like(x), None, None, None, 0, 0, 1.0, "fp16")
+        again = call()
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+    done()
+
+
 def test_calls_can_be_captured_into_a_graph():
     x, w = strided((9, 256), "bf16", 1), strided((256, 256), "bf16", 2)
     xo, wo = strided((200, 255), "bf16", 5), strided((64, 255), "bf16", 6)  # laid out anew in memory of the call
