@@ -6,11 +6,12 @@
 //
 // with c, s the table rows of the token's position.  Each value is read and
 // written once, so the bound is memory; everything between is fp32.  16384 tokens
-// x 48 heads x 128 in bf16: 90 us, 4.6 TB/s, 68% of the measured copy rate: with
-// 78 registers 24 warps an SM do not quite cover the rotation's and the sums'
-// latency (issue slots 49% busy).  One token: 2.2 us on the device.
+// x 48 heads x 128 in bf16: 76 us, 5.4 TB/s, 80% of the measured copy rate (a copy
+// of the same bytes takes 65 us; without the arithmetic this kernel takes 70).  One
+// warp keeps a token's rotation in registers for all its heads: read again for
+// every head, and with one head a lane group of a persistent CTA, it took 90 us.
+// One token: 1.9 us on the device.
 #include <algorithm>
-#include <climits>
 #include <type_traits>
 
 #include "ptx.cuh"
@@ -20,9 +21,8 @@ namespace oidnx {
 namespace {
 
 constexpr int kAnyThreads = 256;
-constexpr int kCtasPerSm = 2;
-constexpr int kDepth = 4;           // tokens of a lane group in flight, at most,
-constexpr int kRing = 48 * 1024;    // and within this much shared memory
+constexpr int kVecThreads = 128;
+constexpr int kCtasPerSm = 6;  // 80 registers a thread; at 5 and 7 (spills) 81 and 77 us where 6 take 76
 
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7FC00000); }
 
@@ -117,115 +117,81 @@ template <typename T, int P> struct Pairs {
   }
 };
 
-template <int N> __device__ __forceinline__ void async_copy(uint32_t dst, const void* src) {
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-
 // Heads in pieces of 2 P values, P rotation pairs a lane, so that a pair never
 // leaves its lane: 2 P consecutive values where pairs are adjacent, else P of
 // each half (of the rotated part, or of the rest, which does not turn).
 //   P     8 (16-byte loads of 16-bit values), or 4
 //   LPH   lanes a head: a power of two, or 0: d / 2P of them, packed into warps
-//   NT    threads of a CTA, which takes as many tokens at a time as it holds
-//         and strides over the tokens
-template <typename T, int P, int LPH, int NT, bool IL>
-__global__ void __launch_bounds__(NT, kCtasPerSm) qk_norm_rope_vec_kernel(const NormParams p) {
+// A warp takes one token's position, row and rotation once, then `steps` times
+// as many heads as it has lanes for, the next ones on their way meanwhile.
+template <typename T, int P, int LPH, bool IL>
+__global__ void __launch_bounds__(kVecThreads, kCtasPerSm) qk_norm_rope_vec_kernel(const NormParams p, const int chunks, const int steps) {
   using Raw = typename Pairs<T, P>::Raw;
   const int lanes = LPH ? LPH : p.d / (2 * P);
   const int per_warp = 32 / lanes;
   const int wl = threadIdx.x & 31;
-  const int group_w = wl / lanes;        // group within the warp
-  const int lane = wl - group_w * lanes;
-  const bool spare = group_w >= per_warp;  // lanes that no whole group is left for
-  const int groups = per_warp * (NT / 32);
-  const int group = (threadIdx.x >> 5) * per_warp + group_w;
+  const int group = wl / lanes;  // this lane's head of the warp's
+  const int lane = wl - group * lanes;
   const int hq = p.heads[0], hk = p.heads[1], total = hq + hk + p.heads[2];
-  const int heads_y = (total + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);  // of this CTA row
-  const int tokens = groups / heads_y;
-  const int tl = group / heads_y;
-  const int h = blockIdx.y * heads_y + group - tl * heads_y;
+  const unsigned item = blockIdx.x * (kVecThreads / 32) + (threadIdx.x >> 5);  // below 2^31: the launch sees to it
+  const int token = static_cast<int>(item / static_cast<unsigned>(chunks));
   griddep_launch_dependents();
   griddep_wait();
-
+  if (token >= p.t) return;
   // first and second values of this lane's pairs
   const int half = p.rot / 2, j = lane * P;
   const int ea = IL ? 2 * j : j < half ? j : j + half;
   const int eb = IL ? 2 * j + P : j < half ? j + half : j + half + (p.d - p.rot) / 2;
-  // this group's head: 0 of the queries, 1 of the keys, 2 of the values, -1 none
-  const int kind = spare || tl >= tokens || h >= total ? -1 : h < hq ? 0 : h < hq + hk ? 1 : 2;
-  const int k = kind < 0 ? 0 : kind;
-  const bool turns = j < half && (kind == 0 || kind == 1);
-  const int hh = h - (k > 0 ? hq : 0) - (k > 1 ? hk : 0);
-  const int tstep = gridDim.x * tokens;
-  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * tokens + tl;
-  const T* src = static_cast<const T*>(p.in[k]) + hh * p.in_h[k] + token0 * p.in_t[k];  // the token to fetch next
-  const int64_t src_step = tstep * p.in_t[k];
-  T* const dst = static_cast<T*>(p.out[k]) + hh * p.out_h[k];
-  const int64_t dst_row = p.out_t[k];
-  const bool weighted = kind >= 0 && k < 2 && p.weight[k];
-  Pairs<T, P> weight;
-  weight.a = weight.b = Raw{};
-  if (weighted) {
-    weight.a = __ldg(reinterpret_cast<const Raw*>(static_cast<const T*>(p.weight[k]) + ea));
-    weight.b = __ldg(reinterpret_cast<const Raw*>(static_cast<const T*>(p.weight[k]) + eb));
-  }
+  const int first = static_cast<int>(item - static_cast<unsigned>(token) * static_cast<unsigned>(chunks)) * steps * per_warp;  // head
+  const int last = group < per_warp ? min(total, first + steps * per_warp) : 0;  // lanes beyond the groups have none
+  const int row = p.slots ? p.slots[token] : token;  // of the keys and values
+  const int pos = p.rot ? p.positions[token] : 0;
 
-  // The heads of the next kStages - 1 tokens are on their way to shared memory
-  // (each thread's own values: no barrier); position and row are read one
-  // token ahead, so that only the rotation's load waits for another.
-  constexpr int kSlot = 2 * sizeof(Raw);
-  constexpr int kStages = kRing / (NT * kSlot) < kDepth ? kRing / (NT * kSlot) : kDepth;
-  static_assert(kStages >= 2, "one token ahead at least");
-  __shared__ __align__(16) uint8_t ring[kStages][NT][kSlot];
-  const auto fetch = [&](int64_t token, int stage) {
-    if (kind >= 0 && token < p.t) {
-      const uint32_t to = smem_u32(ring[stage][threadIdx.x]);
-      async_copy<sizeof(Raw)>(to, src + ea);
-      async_copy<sizeof(Raw)>(to + sizeof(Raw), src + eb);
+  // the head that is fetched next, one step ahead of the one at work
+  const auto kind_of = [&](int h) { return h < hq ? 0 : h < hq + hk ? 1 : 2; };
+  const auto start_of = [&](int kind) { return kind == 0 ? 0 : kind == 1 ? hq : hq + hk; };
+  Pairs<T, P> next;
+  next.a = next.b = Raw{};
+  const T* src = nullptr;
+  int h_n = first + group, kind_n = -1;
+  const auto fetch = [&] {
+    if (h_n < last) {
+      const int kind = kind_of(h_n);
+      if (kind != kind_n) {
+        kind_n = kind;
+        src = static_cast<const T*>(p.in[kind]) + token * p.in_t[kind] + (h_n - start_of(kind)) * p.in_h[kind];
+      }
+      next.a = *reinterpret_cast<const Raw*>(src + ea);
+      next.b = *reinterpret_cast<const Raw*>(src + eb);
+      src += per_warp * p.in_h[kind];
     }
-    src += src_step;
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    h_n += per_warp;
   };
-  int pos_n = 0, row_n = 0;
-  const auto where = [&](int64_t token) {
-    if (token >= p.t) return;
-    row_n = p.slots ? p.slots[token] : static_cast<int>(token);  // of the keys and values
-    if (p.rot) pos_n = p.positions[token];
-  };
+  fetch();
+  float4 c[P / 4], s[P / 4];
+  if (j < half) {
+    const bool known = pos >= 0 && pos < p.table_rows;
+    const int64_t o = static_cast<int64_t>(pos) * half + j;
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) fetch(token0 + static_cast<int64_t>(s) * tstep, s);
-  where(token0);
-  const float inv_d = 1.f / static_cast<float>(p.d);
-  int stage = 0;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * tokens; base < p.t; base += tstep) {
-    const int64_t token = base + tl;
-    const int pos = pos_n, row = row_n;
-    float4 c[P / 4], s[P / 4];
-    if (turns) {
-      const bool known = pos >= 0 && pos < p.table_rows;
-      const int64_t o = static_cast<int64_t>(pos) * half + j;
-#pragma unroll
-      for (int i = 0; i < P / 4; ++i) {
-        if (known) {
-          c[i] = __ldg(reinterpret_cast<const float4*>(p.cos_t + o) + i);
-          s[i] = __ldg(reinterpret_cast<const float4*>(p.sin_t + o) + i);
-        } else {
-          c[i] = s[i] = make_float4(quiet_nan(), quiet_nan(), quiet_nan(), quiet_nan());
-        }
+    for (int i = 0; i < P / 4; ++i) {
+      if (known) {
+        c[i] = __ldg(reinterpret_cast<const float4*>(p.cos_t + o) + i);
+        s[i] = __ldg(reinterpret_cast<const float4*>(p.sin_t + o) + i);
+      } else {
+        c[i] = s[i] = make_float4(quiet_nan(), quiet_nan(), quiet_nan(), quiet_nan());
       }
     }
-    where(token + tstep);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    Pairs<T, P> x;
-    {
-      const Raw* at = reinterpret_cast<const Raw*>(ring[stage][threadIdx.x]);
-      x.a = at[0], x.b = at[1];
-    }
-    fetch(token + static_cast<int64_t>(kStages - 1) * tstep, stage == 0 ? kStages - 1 : stage - 1);
-    if (++stage == kStages) stage = 0;
+  }
+  const bool kept = row >= 0 && row < p.cache_rows;
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  Pairs<T, P> weight;
+  weight.a = weight.b = Raw{};
+  T* dst = nullptr;
+  int kind = -1;
+  bool weighted = false;
+  for (int i = 0, h = first + group; i < steps; ++i, h += per_warp) {
+    Pairs<T, P> x = next;
+    fetch();
     uint64_t a[P / 2], b[P / 2];
     x.template unpack<IL>(a, b);
     uint64_t sq[2] = {mul2(a[0], a[0]), mul2(b[0], b[0])};
@@ -244,8 +210,17 @@ __global__ void __launch_bounds__(NT, kCtasPerSm) qk_norm_rope_vec_kernel(const 
       }
       sum = __shfl_sync(0xFFFFFFFFu, sum, wl - lane);
     }
-    const bool kept = row >= 0 && row < p.cache_rows;
-    if (kind < 0 || token >= p.t || (kind > 0 && !kept)) continue;
+    if (h >= last) continue;
+    if (kind_of(h) != kind) {
+      kind = kind_of(h);
+      dst = static_cast<T*>(p.out[kind]) + (kind ? row : token) * p.out_t[kind] + (h - start_of(kind)) * p.out_h[kind];
+      weighted = kind < 2 && p.weight[kind];
+      if (weighted) {
+        weight.a = __ldg(reinterpret_cast<const Raw*>(static_cast<const T*>(p.weight[kind]) + ea));
+        weight.b = __ldg(reinterpret_cast<const Raw*>(static_cast<const T*>(p.weight[kind]) + eb));
+      }
+    }
+    if (kind > 0 && !kept) continue;
     if (kind < 2) {
       const float r = inverse_root(fmaf(sum, inv_d, p.eps));
       const uint64_t r2 = f2(r, r);
@@ -268,9 +243,9 @@ __global__ void __launch_bounds__(NT, kCtasPerSm) qk_norm_rope_vec_kernel(const 
       }
       x.template pack<IL>(a, b);
     }
-    T* to = dst + (kind ? row : static_cast<int>(token)) * dst_row;
-    *reinterpret_cast<Raw*>(to + ea) = x.a;
-    *reinterpret_cast<Raw*>(to + eb) = x.b;
+    *reinterpret_cast<Raw*>(dst + ea) = x.a;
+    *reinterpret_cast<Raw*>(dst + eb) = x.b;
+    dst += per_warp * p.out_h[kind];
   }
 }
 
@@ -320,32 +295,22 @@ __global__ void __launch_bounds__(kAnyThreads) qk_norm_rope_any_kernel(const Nor
     dst[i] = from_f32<T>(to_f32<T>(src[i]) * r * (weight ? to_f32<T>(weight[i]) : 1.f));
 }
 
-template <typename T, int P, int LPH, int NT>
-cudaError_t launch_vec(const NormParams& p, int gy, int device, int sms, cudaStream_t stream) {
-  const int total = p.heads[0] + p.heads[1] + p.heads[2];
-  const int tokens = NT / 32 * (32 / (LPH ? LPH : p.d / (2 * P))) / ((total + gy - 1) / gy);
-  const int most = (kCtasPerSm * sms + gy - 1) / gy;  // resident together
-  const dim3 grid(std::min((p.t + tokens - 1) / tokens, most), gy);
-  static Kernel adjacent, halves;
-  return p.interleaved
-             ? adjacent.launch(qk_norm_rope_vec_kernel<T, P, LPH, NT, true>, device, grid, NT, 0, 1, stream, p)
-             : halves.launch(qk_norm_rope_vec_kernel<T, P, LPH, NT, false>, device, grid, NT, 0, 1, stream, p);
-}
-
-// 8 or 12 warps, whichever leaves fewer lane groups without a head; a token
-// with more heads is split over CTA rows.
+// A warp takes a whole token where that fills the GPU; with fewer tokens each is
+// split over as many warps as the GPU holds (2040 tokens x 21 heads x 72: two
+// warps a token 6.0 us, three 7.2; 16384 x 48 x 128: one 75.7, two 77.7).
 template <typename T, int P, int LPH>
 cudaError_t launch_heads(const NormParams& p, int device, int sms, cudaStream_t stream) {
-  const int total = p.heads[0] + p.heads[1] + p.heads[2], per_warp = 32 / (LPH ? LPH : p.d / (2 * P));
-  const auto busy = [&](int warps, int* gy) {
-    const int groups = warps * per_warp;
-    *gy = (total + groups - 1) / groups;
-    const int heads = (total + *gy - 1) / *gy;
-    return static_cast<float>(groups / heads * heads) / groups;
-  };
-  int gy8, gy12;
-  const float b8 = busy(8, &gy8), b12 = busy(12, &gy12);
-  return b12 > b8 ? launch_vec<T, P, LPH, 384>(p, gy12, device, sms, stream) : launch_vec<T, P, LPH, 256>(p, gy8, device, sms, stream);
+  const int per_warp = 32 / (LPH ? LPH : p.d / (2 * P));
+  const int most = (p.heads[0] + p.heads[1] + p.heads[2] + per_warp - 1) / per_warp;  // steps of a token
+  const int resident = kCtasPerSm * sms * (kVecThreads / 32);
+  const int split = std::min((resident - 1) / p.t + 1, most);
+  const int steps = (most + split - 1) / split, chunks = (most + steps - 1) / steps;
+  const int64_t items = static_cast<int64_t>(p.t) * chunks;
+  const dim3 grid(static_cast<unsigned>((items + kVecThreads / 32 - 1) / (kVecThreads / 32)));
+  static Kernel adjacent, halves;
+  return p.interleaved
+             ? adjacent.launch(qk_norm_rope_vec_kernel<T, P, LPH, true>, device, grid, kVecThreads, 0, 1, stream, p, chunks, steps)
+             : halves.launch(qk_norm_rope_vec_kernel<T, P, LPH, false>, device, grid, kVecThreads, 0, 1, stream, p, chunks, steps);
 }
 
 template <typename T>
