@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Tile k = w.tile(p, 0);
           see = w.seen(p, t, k);
           ok = mbar_wait_soon(&kfull[0], 0, p.status, kErrTimeoutMma);
-          if (ok && see) ok = mbar_wait_soon(&qfull[t], 0, p.status, kErrTimeoutMma);
+          if (ok && w.active(t)) ok = mbar_wait_soon(&qfull[t], 0, p.status, kErrTimeoutMma);
           tc_fence_after();
           if (ok && see) score(kd0, k.count);
           else mbar_arrive(&kempty[0]);

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Tile k = w.tile(p, 0);
         const bool any = w.seen(p, t, k);
         ok = mbar_wait_soon(&kfull[0], 0, p.status, kErrTimeoutMma);
-        if (ok && any) ok = mbar_wait_soon(&qfull[t], 0, p.status, kErrTimeoutMma);
+        if (ok && w.active(t)) ok = mbar_wait_soon(&qfull[t], 0, p.status, kErrTimeoutMma);
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
