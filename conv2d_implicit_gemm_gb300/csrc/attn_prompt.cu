@@ -9,8 +9,9 @@
 //   (one thread a row), P in 16 bits over S in tensor memory, O += P V with P
 //   as the tensor-memory operand and V read as it lies (values contiguous).
 //
-//  * The two row tiles alternate on the tensor cores: one's softmax runs under
-//    the other's products.
+//  * Each key tile in two halves of 64, each with its own columns for S and P: the
+//    tensor cores write one half's scores while the softmax warps are at the
+//    other's, and the two row tiles' products alternate.
 //  * The running maximum that P is relative to follows the true one only when
 //    it falls more than 2^8 behind, so O is rescaled rarely; P <= 2^8 stays
 //    within 16 bits and the sums are fp32, so nothing is lost by it.
@@ -23,13 +24,15 @@
 //    keys, and where a key itself holds such a value the CTA's rows are done
 //    again one by one.
 //
-// Bound by the latency of a row tile's chain (scores, softmax, products, the next
-// scores: some 3000 cycles for 128 keys, of which the products take 1024), two
-// of which are in flight: tensor memory has no room for a third with 128 output
-// values a row.  8192 tokens, window 2048, 16 heads of 128 over 4: 128 us, 943
-// TFLOP/s of visible pairs, the tensor pipe active 42% of the time.  Sixteen
-// softmax warps (two threads a row, exchanging maxima) took 141 us, one product
-// warp for both row tiles 135.
+// Bound by shared memory and the softmax warps alike: some 3000 cycles a key tile,
+// of which 2500 read operands (the queries again for each half of the keys;
+// without three quarters of those products the whole takes 8% less) and 2800 are
+// a softmax warp's own (without its exponentials alone nothing changes).  8192 tokens,
+// window 2048, 16 heads of 128 over 4: 108 us, 1110 TFLOP/s of visible pairs, the
+// tensor pipe active half of the time.  Whole key tiles, no half in advance: 128;
+// sixteen softmax warps (two threads a row, exchanging maxima) 141; waits whose
+// ready case goes through a loop (250 cycles instead of some 20, five of them a
+// key tile in the issuing thread) 112.
 //
 // Warps 0-3 and 4-7: softmax of row tile 0 and 1, rescaling, output; warp 8
 // loads (TMA), warps 9 and 10 issue the products of a row tile each (one thread
@@ -63,9 +66,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* kempty = kfull + NS;
   uint64_t* vfull = kempty + NS;
   uint64_t* vempty = vfull + NS;
-  uint64_t* sfull = vempty + NS;  // [2]
-  uint64_t* pfull = sfull + 2;    // [2 row tiles][2 halves of the keys]
-  uint64_t* odone = pfull + 4;    // [2]
+  uint64_t* sfull = vempty + NS;  // [2 row tiles][2 halves of the keys]
+  uint64_t* pfull = sfull + 4;    // the same
+  uint64_t* pdone = pfull + 4;    // the same
+  uint64_t* odone = pdone + 4;    // [2]
   uint64_t* vclean = odone + 2;   // [NS]
   uint32_t* slot = reinterpret_cast<uint32_t*>(vclean + NS);
   int* odd = reinterpret_cast<int*>(slot + 1);
@@ -74,17 +78,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 2);  // both row tiles' products
+      mbar_init(&kempty[s], 4);  // both row tiles' halves
       mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], 3);  // and the looking warp
+      mbar_init(&vempty[s], 5);  // and the looking warp
       mbar_init(&vclean[s], 32);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&qfull[t], 1);
-      mbar_init(&sfull[t], 1);
-      mbar_init(&pfull[2 * t], 128);
-      mbar_init(&pfull[2 * t + 1], 128);
       mbar_init(&odone[t], 1);
+    }
+    for (int c = 0; c < 4; ++c) {
+      mbar_init(&sfull[c], 1);
+      mbar_init(&pfull[c], 128);
+      mbar_init(&pdone[c], 1);
     }
     *odd = 0;
     fence_mbarrier_init();
@@ -98,8 +104,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   const Plan w = make_plan(p);
   const int kd = (p.d + 15) / 16;  // blocks of 16 values of a head
-  // columns: S (then P) of tile 0 and 1, O of tile 0 and 1
-  const auto s_col = [tmem](int t) { return tmem + t * 128; };
+  // columns: S (then P) of the row tiles' halves, O of the row tiles
+  const auto s_col = [tmem](int c) { return tmem + c * 64; };
   const auto o_col = [tmem](int t) { return tmem + 256 + t * 64 * DB; };
 
   if (warp >= kSoftWarps) {
@@ -136,52 +142,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp < kLookWarp) {
       // One warp a row tile.  Its thread only issues: a commit covers all the
-      // thread's earlier products, so the scores of key tile j landing tells the
-      // softmax warps that P V of the tile before is done too, and they hand the
-      // stages back (keys of j, values of j - 1).  What its rows do not see the
-      // thread hands back itself, in step with the ring.
+      // thread's earlier products, so the scores of a half of key tile j landing
+      // tells the softmax warps that its P V of the tile before is done too, and
+      // they hand the stages back (keys of j, values of j - 1).  What a half has
+      // no keys of the thread hands back itself, in step with the ring.
       const int t = warp - kMmaWarp;
       if (elect_one()) {
         constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-        const uint32_t id_s = idesc_16(bf, 128, kTileKeys), id_pv = idesc_16(bf, 128, kd * 16, true);
+        const uint32_t id_s = idesc_16(bf, 128, kHalf), id_pv = idesc_16(bf, 128, kd * 16, true);
         const uint64_t qd = smem_desc_sw128(smem_u32(Q + t * kTile));
         const uint64_t kd0 = smem_desc_sw128(smem_u32(Ks)), vd0 = value_desc(smem_u32(Vs));
-        const uint32_t s_at = s_col(t), o_at = o_col(t);
-        int n = 0;
+        const uint32_t o_at = o_col(t);
+        uint32_t phase = 0;  // of each half's weights
+        bool some = false;   // O holds something
+        bool see[2] = {false, false};
         uint32_t clean = 0;  // phase of each stage's looked-over barrier
         bool ok = true;
-        const auto score = [&](uint64_t kt, int count) {  // S of the key tile at kt
-          const uint32_t id = count == kTileKeys ? id_s : idesc_16(bf, 128, (count + 15) / 16 * 16);
+        const auto score = [&](int h, uint64_t kt, int keys) {  // S of a half of the key tile at kt
+          const uint32_t id = keys == kHalf ? id_s : idesc_16(bf, 128, (keys + 15) / 16 * 16);
 #pragma unroll
           for (int i = 0; i < 4 * DB; ++i) {
             const uint32_t off = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
-            if (i < kd) mma_f16_ss(s_at, qd + off, kt + off, id, i > 0);
+            if (i < kd) mma_f16_ss(s_col(2 * t + h), qd + off, kt + h * (kHalf * 128 >> 4) + off, id, i > 0);
           }
-          mma_commit(&sfull[t]);
+          mma_commit(&sfull[2 * t + h]);
         };
-        bool see = false;
         if (w.tiles > 0) {
           const Tile k = w.tile(p, 0);
-          see = w.seen(p, t, k);
+          const bool any = w.seen(p, t, k);
           ok = mbar_wait_soon(&kfull[0], 0, p.status, kErrTimeoutMma);
           if (ok && w.active(t)) ok = mbar_wait_soon(&qfull[t], 0, p.status, kErrTimeoutMma);
           tc_fence_after();
-          if (ok && see) score(kd0, k.count);
-          else mbar_arrive(&kempty[0]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int keys = keys_of_half(k.count, h);
+            see[h] = any && keys > 0;
+            if (ok && see[h]) score(h, kd0, keys);
+            else mbar_arrive(&kempty[0]);
+          }
         }
         int s = 0, ph = 0;
         for (int j = 0; j < w.tiles && ok; ++j) {
           const int s1 = s + 1 == NS ? 0 : s + 1, ph1 = s + 1 == NS ? ph ^ 1 : ph;
-          bool look = false, see1 = j + 1 < w.tiles && w.active(t);
-          int steps = kTileKeys / 16, count1 = kTileKeys;
+          const bool more = j + 1 < w.tiles;
+          bool look = false, any1 = more && w.active(t);
+          int count = kTileKeys, count1 = kTileKeys;
           if (!w.plain(j)) {
             const Tile k = w.tile(p, j);
             look = w.looked_over(p, k);
-            steps = (k.count + 15) / 16;
+            count = k.count;
           }
-          if (see1 && !w.plain(j + 1)) {
+          if (any1 && !w.plain(j + 1)) {
             const Tile k = w.tile(p, j + 1);
-            see1 = w.seen(p, t, k);
+            any1 = w.seen(p, t, k);
             count1 = k.count;
           }
           ok = mbar_wait_soon(&vfull[s], ph, p.status, kErrTimeoutMma);
@@ -189,28 +202,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait_soon(&vclean[s], clean >> s & 1, p.status, kErrTimeoutMma);
             clean ^= 1u << s;
           }
-          if (ok && j + 1 < w.tiles) ok = mbar_wait_soon(&kfull[s1], ph1, p.status, kErrTimeoutMma);
-          if (see) {
-            const uint64_t vt = vd0 + s * (kTile >> 4);
+          if (ok && more) ok = mbar_wait_soon(&kfull[s1], ph1, p.status, kErrTimeoutMma);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (ok) ok = mbar_wait_soon(&pfull[2 * t + h], n & 1, p.status, kErrTimeoutMma);
+          for (int h = 0; h < 2; ++h) {
+            if (see[h]) {
+              if (ok) ok = mbar_wait_soon(&pfull[2 * t + h], phase >> h & 1, p.status, kErrTimeoutMma);
               if (!ok) break;
+              phase ^= 1u << h;
               tc_fence_after();
+              const uint64_t vt = vd0 + s * (kTile >> 4) + h * (kHalf * 128 >> 4);
+              const int steps = (keys_of_half(count, h) + 15) / 16;
 #pragma unroll
-              for (int i = 4 * h; i < 4 * h + 4; ++i)
-                if (i < steps) mma_ts(o_at, s_at + i * 8, vt + i * (2048 >> 4), id_pv, n > 0 || i > 0);
+              for (int i = 0; i < kHalf / 16; ++i)
+                if (i < steps) mma_ts(o_at, s_col(2 * t + h) + i * 8, vt + i * (2048 >> 4), id_pv, some || i > 0);
+              some = true;
+              mma_commit(&pdone[2 * t + h]);
             }
-            ++n;
+            const int keys1 = keys_of_half(count1, h);
+            see[h] = any1 && keys1 > 0;
+            if (see[h]) {
+              score(h, kd0 + s1 * (kTile >> 4), keys1);
+            } else if (more) {
+              mma_commit(&vempty[s]);
+              mbar_arrive(&kempty[s1]);
+            }
           }
-          if (!ok) break;
-          if (see1) {
-            score(kd0 + s1 * (kTile >> 4), count1);
-          } else if (j + 1 < w.tiles) {
-            mma_commit(&vempty[s]);
-            mbar_arrive(&kempty[s1]);
-          }
-          see = see1;
           s = s1, ph = ph1;
         }
         mma_commit(&odone[t]);
@@ -243,7 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.scale * 1.4426950408889634f;  // scores to powers of two
     float top = -INFINITY;  // what P is relative to
     float sum = 0.f;
-    int n = 0;
+    uint32_t phase = 0;  // of each half's scores
+    int last = -1;       // the half whose weights went out last
     bool ok = true;
     const int tiles = w.active(t) ? w.tiles : 0;
     for (int j = 0; j < tiles && ok; ++j) {
@@ -255,105 +272,106 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!w.seen(p, t, k)) continue;
         whole = w.whole(p, t, k);
       }
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&sfull[t], n & 1, p.status, kErrTimeoutEpilogue));
-      if (!ok) break;
-      tc_fence_after();
-      if (r == 0) {
-        mbar_arrive(&kempty[j % NS]);
-        if (j > 0) mbar_arrive(&vempty[(j - 1) % NS]);
-      }
-      // S from tensor memory; the second half's columns are on their way while
-      // the first's are looked at
-      uint32_t raw[4][32];
-      tmem_ld32_nowait(s_col(t) + lanes, raw[0]);
-      tmem_ld32_nowait(s_col(t) + lanes + 32, raw[1]);
-      tmem_wait_ld();
-      tmem_ld32_nowait(s_col(t) + lanes + 64, raw[2]);
-      tmem_ld32_nowait(s_col(t) + lanes + 96, raw[3]);
-      float m4[4];
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        if (h == 1) tmem_wait_ld();
+        const int keys = keys_of_half(k.count, h);
+        if (keys == 0) break;
+        const uint32_t sc = s_col(2 * t + h) + lanes;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&sfull[2 * t + h], phase >> h & 1, p.status, kErrTimeoutEpilogue));
+        if (!ok) break;
+        phase ^= 1u << h;
+        tc_fence_after();
+        if (r == 0) {
+          mbar_arrive(&kempty[j % NS]);
+          if (j > 0) mbar_arrive(&vempty[(j - 1) % NS]);
+        }
+        uint32_t raw[2][32];
+        tmem_ld32_nowait(sc, raw[0]);
+        tmem_ld32_nowait(sc + 32, raw[1]);
+        tmem_wait_ld();
         if (!whole) {
           // columns lo .. hi, and the sinks
-          const int hi = min(k.count - 1, pos - k.pos) - h * 64;
-          const int lo = (p.window == 0 ? 0 : max(pos - p.window + 1 - k.pos, 0)) - h * 64;
-          const int sk = min(p.sinks - k.pos - h * 64, hi + 1);
+          const int hi = min(k.count - 1, pos - k.pos) - h * kHalf;
+          const int lo = (p.window == 0 ? 0 : max(pos - p.window + 1 - k.pos, 0)) - h * kHalf;
+          const int sk = min(p.sinks - k.pos - h * kHalf, hi + 1);
 #pragma unroll
-          for (int q = 2 * h; q < 2 * h + 2; ++q) {
-            const int o = (q & 1) * 32;
-            const uint32_t bits = (below(hi + 1 - o) & ~below(lo - o)) | below(sk - o);
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t bits = (below(hi + 1 - q * 32) & ~below(lo - q * 32)) | below(sk - q * 32);
 #pragma unroll
             for (int e = 0; e < 32; ++e) raw[q][e] = bits >> e & 1u ? raw[q][e] : 0xFF800000u;
           }
         }
+        float m4[4];
 #pragma unroll
-        for (int q = 2 * h; q < 2 * h + 2; ++q) {
-          m4[q] = fmaxf(__uint_as_float(raw[q][0]), __uint_as_float(raw[q][1]));
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t* v = raw[q >> 1] + (q & 1) * 16;
+          m4[q] = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
 #pragma unroll
-          for (int e = 2; e < 32; e += 2) m4[q] = max3(m4[q], __uint_as_float(raw[q][e]), __uint_as_float(raw[q][e + 1]));
+          for (int e = 2; e < 16; e += 2) m4[q] = max3(m4[q], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
         }
-      }
-      const float m = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-      // (lanes without a query hold whatever shared memory held, and must not
-      // decide for the others)
-      const bool rise = valid && (m - top) * c > 8.f;
-      if (__any_sync(0xFFFFFFFFu, rise)) {
-        const float up = fmaxf(m, top);
-        const float f = up == -INFINITY ? 1.f : exp2_fast((top - up) * c);
-        top = up;
-        sum *= f;
-        if (n > 0) {  // (the last P V is done: these scores were committed behind it)
+        const float m = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+        // (lanes without a query hold whatever shared memory held, and must not
+        // decide for the others)
+        const bool rise = valid && (m - top) * c > 8.f;
+        if (__any_sync(0xFFFFFFFFu, rise)) {
+          const float up = fmaxf(m, top);
+          const float f = up == -INFINITY ? 1.f : exp2_fast((top - up) * c);
+          top = up;
+          sum *= f;
+          if (last >= 0) {  // the last P V must be done
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&pdone[2 * t + last], (phase >> last & 1) ^ 1 ^ (last == h), p.status,
+                                                        kErrTimeoutEpilogue));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
-          for (int x = 0; x < kd * 16; x += 16) {
-            uint32_t o[16];
-            tmem_ld16_nowait(o_col(t) + lanes + x, o);
-            tmem_wait_ld();
+            for (int x = 0; x < kd * 16; x += 16) {
+              uint32_t o[16];
+              tmem_ld16_nowait(o_col(t) + lanes + x, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st16(o_col(t) + lanes + x, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(o_col(t) + lanes + x, o);
+            }
           }
         }
-      }
-      const float base = top == -INFINITY ? 0.f : top * c;
-      const uint64_t c2 = f2(c, c), b2 = f2(-base, -base);
-      uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+        const float base = top == -INFINITY ? 0.f : top * c;
+        const uint64_t c2 = f2(c, c), b2 = f2(-base, -base);
+        uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (q * 32 < k.count) {
-          uint32_t pk[16];
+        for (int q = 0; q < 2; ++q) {
+          if (q * 32 < keys) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 x = f2_of(fma2(f2(__uint_as_float(raw[q][e]), __uint_as_float(raw[q][e + 1])), c2, b2));
-            const float u = exp2_fast(x.x), v = exp2_fast(x.y);
-            acc[(e >> 1) & 1] = add2(acc[(e >> 1) & 1], f2(u, v));
-            pk[e / 2] = pack2<T>(u, v);
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = f2_of(fma2(f2(__uint_as_float(raw[q][e]), __uint_as_float(raw[q][e + 1])), c2, b2));
+              const float u = exp2_fast(x.x), v = exp2_fast(x.y);
+              acc[(e >> 1) & 1] = add2(acc[(e >> 1) & 1], f2(u, v));
+              pk[e / 2] = pack2<T>(u, v);
+            }
+            tmem_st16(sc + q * 16, pk);
           }
-          tmem_st16(s_col(t) + lanes + q * 16, pk);
         }
-        if (q & 1) {  // half of the keys: their product may start
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(&pfull[2 * t + (q >> 1)]);
-        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&pfull[2 * t + h]);
+        const float2 a = f2_of(add2(acc[0], acc[1]));
+        sum += a.x + a.y;
+        last = h;
       }
-      const float2 a = f2_of(add2(acc[0], acc[1]));
-      sum += a.x + a.y;
-      ++n;
     }
-    if (n > 0 && ok) {
+    if (last >= 0 && ok) {
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&odone[t], 0, p.status, kErrTimeoutEpilogue));
       tc_fence_after();
     }
     // output: through the row tile's query tile, which no product reads any more
-    const bool some = valid && n > 0 && !(sum == 0.f);
+    const bool some = valid && last >= 0 && !(sum == 0.f);
     const float inv = some ? 1.f / sum : 0.f;
     uint8_t* out = Q + t * kTile;
 #pragma unroll 1
     for (int x = 0; x < DB * 64; x += 32) {
       if (x >= p.d) break;
       uint32_t o[32];
-      if (n > 0) {
+      if (last >= 0) {
         tmem_ld32_nowait(o_col(t) + lanes + x, o);
         tmem_wait_ld();
       }

@@ -11,6 +11,7 @@
 namespace oidnx {
 
 constexpr int kTileKeys = 128;
+constexpr int kHalf = kTileKeys / 2;
 
 __device__ __forceinline__ uint64_t f2(float a, float b) {
   uint64_t r;
@@ -106,6 +107,8 @@ template <typename T, int DB> __device__ __forceinline__ bool look_over(uint8_t*
 struct Tile {
   int slot, pos, count;
 };
+
+__device__ __forceinline__ int keys_of_half(int count, int h) { return min(max(count - h * kHalf, 0), kHalf); }
 
 // The lowest n of 32 bits (none for n <= 0, all from 32 on).
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }

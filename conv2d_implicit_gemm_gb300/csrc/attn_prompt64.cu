@@ -24,10 +24,7 @@ constexpr int kThreads = (kSoftWarps + 4) * 32;
 constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kLookWarp = kSoftWarps + 3;
 constexpr int kOperand = 16384;  // 128 rows of 64 values
 constexpr int NS = 4;            // key tiles (and value tiles) in flight
-constexpr int kHalf = kTileKeys / 2;
 constexpr int kSmem = (2 + 2 * NS) * kOperand + 1024 + 512 + 4 * 128 * 8;
-
-__device__ __forceinline__ int keys_of_half(int count, int h) { return min(max(count - h * kHalf, 0), kHalf); }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)

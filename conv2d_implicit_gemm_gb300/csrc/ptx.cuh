@@ -94,9 +94,11 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   return false;
 }
 
-// The same with a few tries before the clock is first read: for waits on the
-// critical path of short steps.
+// The same with a test first (17 cycles where the phase has completed; a try
+// 90, the loops below 250) and a few tries before the clock is first read: for
+// waits on the critical path of short steps.
 __device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, int* status, int code) {
+  if (mbar_test_wait(bar, parity)) return true;
 #pragma unroll 1
   for (int i = 0; i < 16; ++i)
     if (mbar_try_wait(bar, parity)) return true;

@@ -266,12 +266,12 @@ cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
   }
   const int per = group <= 128 ? 128 / group : 1;  // queries of a row tile
   const int64_t grid = (static_cast<int64_t>(p.tq) + 2 * per - 1) / (2 * per) * p.b * p.hk;
-  // Many queries: key tiles of 128, with one row tile and two, us: heads of 128
-  // values 1.36 and 1.95 (8192 keys 90 and 131), of 64 1.0 and 1.2 (66 and 80);
-  // 4 for a CTA's ends.  The longest CTA or the mean over the SMs, whichever is
+  // Many queries: key tiles of 128, with one row tile and two on every SM, us:
+  // heads of 128 values 1.41 and 1.66 (8192 keys 101 and 118), of 64 0.88 and 1.19
+  // (64 and 85); 4 for a CTA's ends.  The longest CTA or the mean over the SMs, whichever is
   // more.
   const bool one = p.tq <= per;
-  const double tile = p.d <= 64 ? (one ? 1000 : 1200) : one ? 1360 : 1950;
+  const double tile = p.d <= 64 ? (one ? 880 : 1190) : one ? 1410 : 1660;
   const int extra = p.window > 0 ? 1 : 0;
   const double longest = (std::ceil(keys(2 * per, false) / 128) + extra) * tile;
   const double mean = (std::ceil(keys(2 * per, true) / 128) + extra) * tile;
