@@ -158,13 +158,12 @@ struct Plan {
 
 __device__ __forceinline__ Plan make_plan(const AttnParams& p) {
   Plan w;
-  const int heads = p.b * p.hk;
   // row tiles from the last to the first (causal: the longest first), the heads of one next to each other
-  const int unit = blockIdx.x % heads;
-  const int rows = static_cast<int>(gridDim.x) / heads - 1 - static_cast<int>(blockIdx.x) / heads;
-  w.b = unit / p.hk, w.kvh = unit % p.hk;
-  w.group = p.hq / p.hk;
-  w.per = 128 / w.group;
+  const unsigned heads = p.b * p.hk, from_last = blockIdx.x / heads, unit = blockIdx.x - from_last * heads;
+  const int rows = p.pairs - 1 - static_cast<int>(from_last);
+  w.b = unit / static_cast<unsigned>(p.hk), w.kvh = unit - w.b * p.hk;
+  w.group = p.group;
+  w.per = p.per;
   w.n = attn_kv_len(p, w.b), w.nq = attn_q_len(p, w.b);
   w.pq = w.n - w.nq;
   w.i00 = 2 * rows * w.per;

@@ -175,6 +175,7 @@ struct AttnParams {
   int held_sinks;  // min(sinks, cap): the slots that the ring leaves alone
   float scale;
   int* status;
+  int group, per, pairs;  // for prompts: heads a key head, queries a row tile, pairs of row tiles
 };
 
 __device__ __forceinline__ int attn_q_len(const AttnParams& p, int b) {

@@ -265,7 +265,7 @@ cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
     for (const int64_t s : {p.k_s[i], p.v_s[i]}) tiles = tiles && s < far && (i == 1 ? s > 0 : s >= 0);
   }
   const int per = group <= 128 ? 128 / group : 1;  // queries of a row tile
-  const int64_t grid = (static_cast<int64_t>(p.tq) + 2 * per - 1) / (2 * per) * p.b * p.hk;
+  const int64_t pairs = (static_cast<int64_t>(p.tq) + 2 * per - 1) / (2 * per), grid = pairs * heads;
   // Many queries: key tiles of 128, with one row tile and two on every SM, us:
   // heads of 128 values 1.41 and 1.66 (8192 keys 101 and 118), of 64 0.88 and 1.19
   // (64 and 85); 4 for a CTA's ends.  The longest CTA or the mean over the SMs, whichever is
@@ -287,7 +287,8 @@ cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
                        s[0] ? s[0] : any, 128, 1);
     };
     AttnLaunch L = {};
-    L.p = p, L.device = device, L.grid = static_cast<unsigned>(grid);
+    L.p = p, L.p.group = group, L.p.per = per, L.p.pairs = static_cast<int>(pairs);
+    L.device = device, L.grid = static_cast<unsigned>(grid);
     if (heads_map(&L.map_q, bf16, p.q, p.d, p.hq, p.q_s[2], p.tq, p.q_s[1], p.b, p.q_s[0], group, per) &&
         heads_map(&L.map_o, bf16, p.o, p.d, p.hq, p.o_s[2], p.tq, p.o_s[1], p.b, p.o_s[0], group, per) &&
         cache_map(&L.map_k, p.k, p.k_s) && cache_map(&L.map_v, p.v, p.v_s))
