@@ -28,7 +28,7 @@
 // of which 2500 read operands (the queries again for each half of the keys;
 // without three quarters of those products the whole takes 8% less) and 2800 are
 // a softmax warp's own (without its exponentials alone nothing changes).  8192 tokens,
-// window 2048, 16 heads of 128 over 4: 108 us, 1110 TFLOP/s of visible pairs, the
+// window 2048, 16 heads of 128 over 4: 107 us, 1120 TFLOP/s of visible pairs, the
 // tensor pipe active half of the time.  Whole key tiles, no half in advance: 128;
 // sixteen softmax warps (two threads a row, exchanging maxima) 141; waits whose
 // ready case goes through a loop (250 cycles instead of some 20, five of them a

@@ -1,15 +1,13 @@
 // Window attention for prompts, heads of up to 64 values: the plan, operands and
-// rules of attn_prompt.cu with four chains of scores, softmax and products in
-// flight instead of two.
+// rules of attn_prompt.cu, with the halves of a key tile as chains of their own.
 //
-// A chain's latency (scores to weights to the next scores, some 3000 cycles for
-// 128 keys) bounds that form whatever the head size: a causal 2 x 4096 x 8 x 64
-// took as long per key tile as heads of 128 with twice the products.  Here
-// tensor memory has room for a chain per row tile and half of each key tile: 64
-// columns of scores and 64 of output each.  The halves of a row keep their own
-// maximum, sum and output and are joined at the end.  2 x 4096 causal, 8 heads of
-// 64: 46 us (two chains: 54), 740 TFLOP/s of visible pairs; the longest CTA's 32
-// key tiles are what remains.
+// Bound by a chain's latency: scores to weights to the next scores, some 2300
+// cycles for 64 keys, of which the softmax warps take 1400.  Tensor memory has
+// room for a chain per row tile and half of each key tile: 64 columns of scores
+// and 64 of output each.  The halves of a row keep their own maximum, sum and
+// output, sixteen softmax warps work at once, and the halves are joined at the
+// end.  2 x 4096 causal, 8 heads of 64: 46 us (one chain a row tile: 54), 740
+// TFLOP/s of visible pairs; the longest CTA's 32 key tiles are what remains.
 //
 // Warps 4 c .. 4 c + 3: softmax of chain c = 2 (row tile) + (half of the keys),
 // one thread a row; warp 16 loads, 17 and 18 issue the products of a row tile's
