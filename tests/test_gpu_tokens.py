@@ -328,6 +328,42 @@ def test_attention_sharp_and_flat_scores(tq, scale, size):
     check_attention(1, tq, 300, 2, 2, 64, 0, 0, "fp16", scale=scale, size=size, seed=3)
 
 
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [40, 64, 80, 128])
+@pytest.mark.parametrize("tq", [1, 300, 690])
+def test_attention_scores_that_grow_along_the_keys(tq, d, kind):
+    """Every 64 keys are larger than those before: sums and outputs are scaled again and again."""
+    def edit(q, k, v):
+        k *= (1 + torch.arange(700, device="cuda") // 64 * 2).to(k.dtype)[None, :, None, None]
+
+    check_attention(1, tq, 700, 4, 2, d, 0, 0, kind, edit=edit, seed=d + tq)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tq,window", [(600, 30), (600, 200), (257, 1)])
+def test_attention_row_tiles_that_see_other_key_tiles(tq, window, d):
+    """Row tiles next to each other whose windows share no key, over many pairs of them."""
+    check_attention(3, tq, 1500, 2, 2, d, window, 0, "fp16", kv_lens=[1500, 700, 1111], seed=window)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_attention_unseen_values_of_large_heads_and_long_caches(bad):
+    """The same for heads of 128 values, whole key tiles before and after the one that holds the value."""
+    at, tq, n, window = 1000, 900, 1600, 300
+
+    def edit(q, k, v):
+        v[0, at, 0, 100] = bad
+
+    got, ref, mag = check_attention(1, tq, n, 4, 1, 128, window, 2, "bf16", edit=edit, rows=True, seed=9)
+    pos = n - tq + np.arange(tq)
+    sees = (at <= pos) & (at > pos - window)
+    np.testing.assert_array_equal(np.isfinite(got[0][~sees]), True)
+    assert not np.isfinite(got[0][sees][:, :, 100]).any()
+    got, ref, mag = got[0].copy(), ref[0].copy(), mag[0].copy()
+    got[sees, :, 100] = ref[sees, :, 100] = mag[sees, :, 100] = 0
+    assert_within(got, ref, UNIT["bf16"] * np.abs(ref) + (2 * UNIT["bf16"] + 2.0 ** -14) * mag)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 @pytest.mark.parametrize("tq", [1, 6, 300])
 def test_attention_unseen_keys_never_reach_a_row(tq, bad):
