@@ -11,8 +11,8 @@
 //    before, by linear_align.cu.)
 //  * Epilogue: eight warps, each 32 rows x half the columns, through 32 x 64
 //    tiles of 16-bit values that TMA stores (and, for the residual, loads
-//    first); outputs that TMA cannot store go through 32 x 32 fp32 tiles and
-//    single values, coalesced along the row.
+//    first); outputs that TMA cannot store go row by row in 32-bit words, shifted
+//    where a row starts on an odd place.
 //  * The MMA warp overwrites the accumulator with its first product and adds
 //    the others; products outside the matrix are zeros that TMA fills in.
 // 8192 x 8192 x 4096, bf16, gelu_tanh: 295 us alone (1865 TFLOP/s, the tensor pipe
@@ -34,7 +34,8 @@ namespace {
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpi = 4;  // warp 0 loads, warp 1 multiplies, 2 and 3 rest
 constexpr int kLinThreads = (kFirstEpi + kEpiWarps) * 32;
-constexpr int kStageOut = 4096;  // bytes of staging per epilogue warp
+constexpr int kStageOut = 4096;  // bytes of staging per epilogue warp, on 1024
+constexpr int kRoomMore = 128;   // the same of rows in words of their own (32 x 33)
 constexpr int kKB = 64;          // values of one K block: one 128-byte row of a tile
 constexpr int kRowGroup = 8;     // row blocks walked together
 
@@ -42,9 +43,9 @@ template <int CG, int BN> struct Shape {
   static constexpr int kA = 128 * 128;              // bytes of a CTA's x block
   static constexpr int kB = BN / CG * 128;          // bytes of its w block
   static constexpr int kStage = kA + kB;
-  static constexpr int kRoom = 227 * 1024 - 2048 - kEpiWarps * kStageOut;
+  static constexpr int kRoom = 227 * 1024 - 2048 - kEpiWarps * (kStageOut + kRoomMore);
   static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
-  static constexpr int kSmem = kStages * kStage + kEpiWarps * kStageOut + 2048;
+  static constexpr int kSmem = kStages * kStage + kEpiWarps * (kStageOut + kRoomMore) + 2048;
   static constexpr int kCols = 2 * BN < 32 ? 32 : 2 * BN;
 };
 
@@ -153,49 +154,123 @@ __device__ __forceinline__ bool epilogue_tma(const TcArgs& a, const CUtensorMap*
   return true;
 }
 
-// The residual of a 32 x 32 tile from (r0, c0) on, column c0 + lane (zeros
-// outside or without one).
-template <typename T>
-__device__ __forceinline__ void load_residual(const LinearParams& p, int r0, int c0, int lane, T (&z)[32]) {
-  const int rows = p.residual && c0 + lane < p.n ? min(32, p.m - r0) : 0;
-  const T* res = static_cast<const T*>(p.residual) + r0 * p.ldr + c0 + lane;
-#pragma unroll
-  for (int r = 0; r < 32; ++r) z[r] = r < rows ? res[r * p.ldr] : T(0.f);
-}
+// Outputs that TMA cannot store: tiles of 32 rows x W columns through shared
+// memory, each row in words as its own alignment asks for (2040 x 1001 x 1000 with
+// residual 15.2 us, aligned 13.9; by single 16-bit values 18.8).  With s = 1 where the
+// row starts on an odd 16-bit place (0 else), word l holds columns 2 l - s and
+// 2 l - s + 1, so that a warp reads and writes whole words; column 0 of s = 1 and
+// a last column that no pair takes go alone, one lane a row.
+template <typename T, int W> struct Ragged {
+  static constexpr int kLanes = W / 2;          // lanes a row
+  static constexpr int kRows = 32 / kLanes;     // rows at a time
+  static constexpr int kSteps = 32 / kRows;
+  static constexpr int kWords = W / 2 + 1;      // of a row (odd: no bank conflicts either way)
 
-// The same through single values: any row stride and alignment.  z: the first
-// tile's residual; each next one is loaded a tile ahead (y may be the residual,
-// so the compiler keeps a load behind every earlier store, but another tile's
-// values are not written before).
-template <typename T, int COLS>
+  const char* base;  // of the tile
+  int64_t ld;
+  int rows, cols;    // inside the matrix
+
+  __device__ __forceinline__ Ragged(const void* x, int64_t row, int m, int n, int r0, int c0)
+      : base(static_cast<const char*>(x) + 2 * (r0 * row + c0)), ld(row), rows(min(32, m - r0)), cols(min(W, n - c0)) {}
+  __device__ __forceinline__ int shift(int r) const {
+    return ((reinterpret_cast<uintptr_t>(base) >> 1) + static_cast<uint32_t>(ld) * r) & 1;
+  }
+  __device__ __forceinline__ bool first_alone(int r) const { return r < rows && cols > 0 && shift(r); }
+  __device__ __forceinline__ bool last_alone(int r) const { return r < rows && cols > 0 && ((cols ^ shift(r)) & 1); }
+  // Is word l of row r a pair inside the tile?
+  __device__ __forceinline__ bool pair(int r, int l) const {
+    const int c = 2 * l - shift(r);
+    return r < rows && c >= 0 && c + 1 < cols;
+  }
+  __device__ __forceinline__ char* at(int r, int c) const { return const_cast<char*>(base) + 2 * (r * ld + c); }
+
+  // From the matrix to registers, on to shared memory, and back from there.
+  struct Values {
+    uint32_t z[kSteps];
+    uint16_t first, last;
+  };
+  __device__ __forceinline__ void load(Values& v, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = i * kRows + lane / kLanes, l = lane % kLanes;
+      v.z[i] = pair(r, l) ? *reinterpret_cast<const uint32_t*>(at(r, 2 * l - shift(r))) : 0u;
+    }
+    v.first = first_alone(lane) ? *reinterpret_cast<const uint16_t*>(at(lane, 0)) : 0;
+    v.last = last_alone(lane) ? *reinterpret_cast<const uint16_t*>(at(lane, cols - 1)) : 0;
+  }
+  __device__ __forceinline__ void put(const Values& v, uint32_t* tile, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) tile[(i * kRows + lane / kLanes) * kWords + lane % kLanes] = v.z[i];
+    __syncwarp();
+    uint16_t* half = reinterpret_cast<uint16_t*>(tile + lane * kWords);
+    if (first_alone(lane)) half[1] = v.first;
+    if (last_alone(lane)) half[cols - 1 + shift(lane)] = v.last;
+  }
+  __device__ __forceinline__ void store(const uint32_t* tile, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = i * kRows + lane / kLanes, l = lane % kLanes;
+      if (pair(r, l)) *reinterpret_cast<uint32_t*>(at(r, 2 * l - shift(r))) = tile[r * kWords + l];
+    }
+    const uint16_t* half = reinterpret_cast<const uint16_t*>(tile + lane * kWords);
+    if (first_alone(lane)) *reinterpret_cast<uint16_t*>(at(lane, 0)) = half[1];
+    if (last_alone(lane)) *reinterpret_cast<uint16_t*>(at(lane, cols - 1)) = half[cols - 1 + shift(lane)];
+  }
+};
+
+// The epilogue for them.  z: the first tile's residual; each next one is loaded
+// a tile ahead (y may be the residual, so the compiler keeps a load behind every
+// earlier store, but another tile's values are not written before).
+template <typename T, int COLS, int W>
 __device__ __forceinline__ void epilogue_any(const TcArgs& a, uint32_t tmem, int r0, int c0, uint8_t* stage, int lane,
-                                             T (&z)[32]) {
+                                             typename Ragged<T, W>::Values& z) {
+  using R = Ragged<T, W>;
   const LinearParams& p = a.p;
-  float* tile = reinterpret_cast<float*>(stage);  // [row][column ^ row]
+  uint32_t* tile = reinterpret_cast<uint32_t*>(stage);
+  uint32_t* row = tile + lane * R::kWords;
 #pragma unroll 1
-  for (int c = 0; c < COLS; c += 32) {
+  for (int c = 0; c < COLS; c += W) {
     if (c0 + c >= p.n) break;
-    T next[32];
-    if (c + 32 < COLS) load_residual<T>(p, r0, c0 + c + 32, lane, next);
-    uint32_t raw[32];
-    tmem_ld32_nowait(tmem + c, raw);
-    tmem_wait_ld();
-    float v[32];
+    const R y(p.y, p.ldy, p.m, p.n, r0, c0 + c), res(p.residual, p.ldr, p.m, p.n, r0, c0 + c);
+    if (p.residual) {
+      res.put(z, tile, lane);
+      if (c + W < COLS) R(p.residual, p.ldr, p.m, p.n, r0, c0 + c + W).load(z, lane);
+      __syncwarp();
+    }
+    // words as they are, or each with the upper half of the one before
+    const uint32_t pick_res = res.shift(lane) ? 0x5432u : 0x3210u, pick_y = y.shift(lane) ? 0x5432u : 0x7654u;
+    uint32_t word = 0;  // the last whole one
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
-    add_bias<T>(p, c0 + c, v);
-    activate_all(v, p.act);
+    for (int h = 0; h < W; h += 32) {
+      uint32_t raw[32];
+      tmem_ld32_nowait(tmem + c + h, raw);
+      tmem_wait_ld();
+      float v[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) tile[lane * 32 + (i ^ lane)] = v[i];
+      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
+      add_bias<T>(p, c0 + c + h, v);
+      activate_all(v, p.act);
+      if (p.residual) {
+        uint32_t now = row[h / 2];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t next = row[h / 2 + i + 1];
+          const float2 f = unpack2<T>(__byte_perm(now, next, pick_res));
+          v[2 * i] += f.x, v[2 * i + 1] += f.y;
+          now = next;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t both = pack2<T>(v[2 * i], v[2 * i + 1]);
+        row[h / 2 + i] = __byte_perm(word, both, pick_y);
+        word = both;
+      }
+    }
+    row[W / 2] = word >> 16;  // (the last column's, where the row is shifted)
     __syncwarp();
-    const int col = c0 + c + lane, rows = col < p.n ? min(32, p.m - r0) : 0;
-    T* y = static_cast<T*>(p.y) + r0 * p.ldy + col;
-#pragma unroll
-    for (int r = 0; r < 32; ++r)
-      if (r < rows) y[r * p.ldy] = from_f32<T>(tile[r * 32 + (lane ^ r)] + to_f32<T>(z[r]));
+    y.store(tile, lane);
     __syncwarp();
-#pragma unroll
-    for (int r = 0; r < 32; ++r) z[r] = next[r];
   }
 }
 
@@ -210,7 +285,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;  // every tile starts on 1024 bytes
   uint8_t* staging = stages + NS * S::kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStageOut);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * (kStageOut + kRoomMore));
   uint64_t* empty = full + NS;
   uint64_t* tfull = empty + NS;    // [2]
   uint64_t* tempty = tfull + 2;    // [2]
@@ -310,7 +385,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   } else if (warp >= kFirstEpi) {
     const int e = warp - kFirstEpi;
     const int quarter = warp & 3, half = e >> 2;  // the TMEM lanes a warp may read; its columns
-    uint8_t* stage = staging + e * kStageOut;
+    uint8_t* stage = staging + e * (a.tma_out ? kStageOut : kStageOut + kRoomMore);
     uint32_t rphase = 0;
     int n = 0;
     for (int t = walker; t < tiles; t += walkers, ++n) {
@@ -320,12 +395,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const int r0 = (tm * CG + static_cast<int>(rank)) * 128 + quarter * 32;
       const int c0 = tn * BN + half * (BN / 2);
       // the epilogue's reads on their way while the products run
-      T z[32];
+      // (64 columns and the next tile's residual would not fit the registers of 256:
+      // 4000 x 3001 x 2000 69 us, with 32 59; 2040 x 1001 x 1000 in tiles of 128 columns
+      // 15.2 with 64, 17.1 with 32)
+      constexpr int W = BN == 128 ? 64 : 32;
+      typename Ragged<T, W>::Values z;
       if (r0 < p.m && c0 < p.n) {
         if (a.tma_out && lane == 0)
           fetch_residual<BN / 2 < 64 ? BN / 2 : 64>(p, &map_r, stage, &rbar[e], r0, c0);
         if (p.bias && lane < BN / 2 / 32) prefetch_l1(static_cast<const T*>(p.bias) + min(c0 + lane * 32, p.n - 1));
-        if (!a.tma_out) load_residual<T>(p, r0, c0, lane, z);
+        if (!a.tma_out && p.residual) Ragged<T, W>(p.residual, p.ldr, p.m, p.n, r0, c0).load(z, lane);
       }
       __syncwarp();
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[b], (n >> 1) & 1, p.status, kErrTimeoutEpilogue))) break;
@@ -335,7 +414,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (a.tma_out) {
           if (!epilogue_tma<T, BN / 2>(a, &map_y, &map_r, acc, r0, c0, stage, &rbar[e], &rphase, lane)) break;
         } else {
-          epilogue_any<T, BN / 2>(a, acc, r0, c0, stage, lane, z);
+          epilogue_any<T, BN / 2, W>(a, acc, r0, c0, stage, lane, z);
         }
       }
       tc_fence_before();
