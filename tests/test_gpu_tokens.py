@@ -86,6 +86,27 @@ def test_linear_adds_to_its_residual_in_place(m):
     check_linear(m, 201, 64, "bf16", "none", inplace=True)
 
 
+@pytest.mark.parametrize("at", [(0, 1), (1, 0), (1, 1)])
+@pytest.mark.parametrize("m,n", [(140, 1), (140, 2), (140, 33), (150, 64), (600, 777), (2100, 2905)])
+def test_linear_outputs_and_residuals_on_odd_places(m, n, at):
+    """Rows of the output and of the residual that start on odd places, each in its own way."""
+    x, w = strided((m, 72), "fp16", 1), strided((n, 72), "fp16", 2, scale=0.1)
+    r, y = strided((m, n), "fp16", 3, [0, 2], at[0]), strided((m, n), "fp16", 4, [0, 3], at[1])
+    around, outside = y.clone(), y._base.clone()
+    ref, size = tokens.linear(f64(x), f64(w), None, f64(r), "none")
+    linear(x, w, None, r, y, "none", "fp16")
+    done()
+    assert_within(f64(y), ref, UNIT["fp16"] * np.abs(ref) + TINY["fp16"] + 100 * 2.0 ** -23 * size + 2.0 ** -22 * np.abs(ref))
+    base = y._base
+    y.copy_(around)
+    assert torch.equal(base.view(torch.int16), outside.view(torch.int16))
+
+
+def test_linear_large_odd_sizes_in_place():
+    check_linear(1500, 1501, 264, "bf16", "gelu_tanh", inplace=True, seed=6)
+    check_linear(2100, 2999, 100, "fp16", "relu", inplace=True, seed=7)
+
+
 def test_linear_large_tiles():
     check_linear(515, 777, 320, "bf16", "gelu_tanh", seed=3)
     check_linear(1100, 2048, 520, "fp16", "silu", residual=False, seed=4)
