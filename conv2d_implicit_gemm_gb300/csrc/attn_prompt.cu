@@ -359,8 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         last = h;
       }
     }
-    if (last >= 0 && ok) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&odone[t], 0, p.status, kErrTimeoutEpilogue));
+    // What follows writes over the queries: wait for the last product, or, where the
+    // row tile saw no key tile (a prompt longer than the ring), for their load.
+    if (tiles > 0 && ok) {
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(last >= 0 ? &odone[t] : &qfull[t], 0, p.status, kErrTimeoutEpilogue));
       tc_fence_after();
     }
     // output: through the row tile's query tile, which no product reads any more

@@ -1,0 +1,40 @@
+"""Edges of the token operators: prompts longer than a ring holds (tolerances and helpers of test_gpu_tokens.py)."""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+from tests._tokens import attention, done, strided
+from tests.test_gpu_tokens import check_attention
+
+
+# ---------------------------------------------------------------- prompts longer than the ring
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("b,tq,cap,kv,hq,hk,window,sinks", [
+    (3, 512, 300, 512, 2, 2, 0, 0), (3, 1024, 600, 1024, 2, 2, 0, 0), (3, 1024, 600, 1024, 2, 2, 50, 0),
+    (2, 700, 333, 5000, 4, 2, 40, 0), (3, 640, 200, 640, 2, 2, 0, 3), (3, 900, 150, 1000003, 6, 2, 20, 0)])
+def test_attention_prompts_longer_than_the_ring(b, tq, cap, kv, hq, hk, window, sinks, d, kind):
+    """Without sinks the first queries see nothing any more: o = 0, lse = -inf, also where they share a block with rows
+    that do see keys."""
+    check_attention(b, tq, cap, hq, hk, d, window, sinks, kind, kv_lens=[kv] * b, seed=cap + d)
+
+
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("tq,cap", [(512, 300), (1024, 600), (4096, 2100)])
+def test_attention_rows_before_the_ring_stay_zero(tq, cap, d):
+    """The same call again and again: no row without a key ever holds anything but zeros."""
+    q, k, v = strided((2, tq, 4, d), "bf16", 1), strided((2, cap, 4, d), "bf16", 2), strided((2, cap, 4, d), "bf16", 3)
+    lens = torch.full((2,), tq, dtype=torch.int32, device="cuda")
+    first = None
+    for _ in range(30):
+        o = torch.full_like(q, float("nan"))
+        lse = torch.full((2, 4, tq), float("nan"), device="cuda")
+        attention(q, k, v, o, lse, None, lens, 0, 0, d ** -0.5, "bf16")
+        assert not o[:, :tq - cap].any() and torch.isneginf(lse[:, :, :tq - cap]).all()
+        first = first or (o, lse)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    done()
+    assert np.isfinite(first[1][:, :, tq - cap:].cpu().numpy()).all()
