@@ -22,7 +22,8 @@ __device__ __forceinline__ float gelu(float z) {
   q = fmaf(q, t, -0.284496736f);
   q = fmaf(q, t, 0.254829592f);
   const float half_erfc = 0.5f * (q * t) * __expf(-x * x);
-  return z < 0.f ? z * half_erfc : fmaf(-z, half_erfc, z);
+  // (from z = 14 on half_erfc is zero; the bound keeps infinity out of its product)
+  return z < 0.f ? z * half_erfc : fmaf(-fminf(z, 16.f), half_erfc, z);
 }
 
 template <int ACT> __device__ __forceinline__ float activate(float z) {

@@ -1,4 +1,5 @@
-"""Edges of the token operators: prompts longer than a ring holds (tolerances and helpers of test_gpu_tokens.py)."""
+"""Edges of the token operators: activations at infinity, prompts longer than a ring holds (tolerances and helpers of
+test_gpu_tokens.py)."""
 
 import numpy as np
 import pytest
@@ -6,8 +7,29 @@ import torch
 
 pytestmark = pytest.mark.gpu
 
-from tests._tokens import attention, done, strided
+from oracle import tokens
+from tests._tokens import ACTS, attention, done, f64, linear, strided
 from tests.test_gpu_tokens import check_attention
+
+
+# ---------------------------------------------------------------- infinities
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,k", [(4, 64), (4, 65), (33, 64), (33, 65), (180, 64), (180, 65)])
+def test_linear_activations_at_infinity(m, k, act, kind):
+    """Sums and biases of either infinity: what the definition gives (infinity, NaN or a number) at every value."""
+    x, w, b = strided((m, k), kind, 1), strided((40, k), kind, 2), strided((40,), kind, 3)
+    w[:, 5] = torch.where(torch.arange(40, device="cuda") % 2 == 0, 1.0, -1.0).to(w.dtype)
+    x[1, 5], x[2, 5] = float("inf"), float("-inf")
+    b[3], b[4], b[5] = float("inf"), float("-inf"), float("nan")
+    y = torch.empty(m, 40, dtype=x.dtype, device="cuda")
+    linear(x, w, b, None, y, act, kind)
+    done()
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref, _ = tokens.linear(f64(x), f64(w), f64(b), None, act)
+    got = f64(y)
+    for what in (np.isnan, np.isposinf, np.isneginf):
+        np.testing.assert_array_equal(what(got), what(ref))
 
 
 # ---------------------------------------------------------------- prompts longer than the ring
