@@ -13,8 +13,9 @@
 //    tensor cores write one half's scores while the softmax warps are at the
 //    other's, and the two row tiles' products alternate.
 //  * The running maximum that P is relative to follows the true one only when
-//    it falls more than 2^8 behind, so O is rescaled rarely; P <= 2^8 stays
-//    within 16 bits and the sums are fp32, so nothing is lost by it.
+//    it falls more than 2^8 behind, so O is rescaled rarely; P <= 2^8 (fp16: 2^15,
+//    to keep the small ones) stays within 16 bits and the sums are fp32, so
+//    nothing is lost by it.
 //  * P is rounded to the storage type, as both operands of a product have one
 //    type; its error is that of the inputs' own rounding and averages out
 //    over the keys.  The sum of the weights is taken before the rounding.
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float base = top == -INFINITY ? 0.f : top * c;
+        const float base = top == -INFINITY ? 0.f : top * c - kLift<T>;
         const uint64_t c2 = f2(c, c), b2 = f2(-base, -base);
         uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.lse && r < w.per * w.group && i < p.tq) {
       const int h = w.kvh * w.group + r % w.group;
       p.lse[(static_cast<int64_t>(w.b) * p.hq + h) * p.tq + i] =
-          some ? (top * c + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+          some ? (top * c - kLift<T> + log2f(sum)) * 0.69314718055994531f : -INFINITY;
     }
     fence_proxy_async_smem();
     named_barrier_sync(1 + t, 128);

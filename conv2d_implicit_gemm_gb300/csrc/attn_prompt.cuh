@@ -104,6 +104,12 @@ template <typename T, int DB> __device__ __forceinline__ bool look_over(uint8_t*
   return found;
 }
 
+// Powers of two by which weights stand above what the running maximum says: fp16
+// ends 2^24 below 1, and many small weights next to a large one would be lost to
+// the output but not to their sum.  With the 2^8 that a weight may be above 1
+// before the maximum follows, 2^15 is the largest power of two that fp16 holds.
+template <typename T> constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;
+
 struct Tile {
   int slot, pos, count;
 };

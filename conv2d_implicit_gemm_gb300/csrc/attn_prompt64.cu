@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      const float base = top == -INFINITY ? 0.f : top * c;
+      const float base = top == -INFINITY ? 0.f : top * c - kLift<T>;
       const uint64_t c2 = f2(c, c), b2 = f2(-base, -base);
       uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.lse && h == 0 && r < w.per * w.group && i < p.tq) {
       const int head = w.kvh * w.group + r % w.group;
       p.lse[(static_cast<int64_t>(w.b) * p.hq + head) * p.tq + i] =
-          some ? (both * c + log2f(total)) * 0.69314718055994531f : -INFINITY;
+          some ? (both * c - kLift<T> + log2f(total)) * 0.69314718055994531f : -INFINITY;
     }
     fence_proxy_async_smem();
     named_barrier_sync(1 + t, 256);

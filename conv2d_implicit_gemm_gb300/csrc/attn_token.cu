@@ -75,6 +75,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Powers of two by which the largest weight of a row stands above 1: weights go
+// into the second product in the storage type, and fp16 ends 2^24 below 1, so
+// relative to 1 many small weights next to a large one would be lost to the
+// output but not to their sum.  2^15 is the largest power of two that fp16 holds.
+template <typename T> constexpr float kLift = std::is_same<T, __half>::value ? 15.f : 0.f;
 // Whether a pair of 16-bit values holds an infinity or a NaN.
 template <typename T> __device__ __forceinline__ bool not_finite2(uint32_t w) {
   constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
@@ -254,7 +259,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_token_kernel(const AttnPa
         changed |= m != top[t][h];
         top[t][h] = m;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = exp2_fast(s[e] - base);
+        for (int e = 0; e < 4; ++e) s[e] = exp2_fast(s[e] - (base - kLift<T>));
         sum[t][h] = fmaf(sum[t][h], old[t][h], (s[0] + s[1]) + (s[2] + s[3]));
         pf[t][h] = pack2<T>(s[0], s[1]);
         pf[t][2 + h] = pack2<T>(s[2], s[3]);
@@ -411,7 +416,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_token_kernel(const AttnPa
         Vec16<T>::pack(acc);
     if (p.lse && c == 0)
       p.lse[(static_cast<int64_t>(b) * p.hq + h) * p.tq + i] =
-          l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+          l == 0.f ? -INFINITY : (m - kLift<T> + log2f(l)) * 0.69314718055994531f;
   }
   if (split > 1) cluster_sync();  // a part stays until everyone has read it
 }

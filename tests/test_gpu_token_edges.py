@@ -1,5 +1,5 @@
-"""Edges of the token operators: activations at infinity, prompts longer than a ring holds (tolerances and helpers of
-test_gpu_tokens.py)."""
+"""Edges of the token operators: activations at infinity, prompts longer than a ring holds, weights far below the largest
+(tolerances and helpers of test_gpu_tokens.py)."""
 
 import numpy as np
 import pytest
@@ -8,8 +8,8 @@ import torch
 pytestmark = pytest.mark.gpu
 
 from oracle import tokens
-from tests._tokens import ACTS, attention, done, f64, linear, strided
-from tests.test_gpu_tokens import check_attention
+from tests._tokens import ACTS, KINDS, TINY, UNIT, attention, done, f64, linear, strided
+from tests.test_gpu_tokens import assert_within, check_attention
 
 
 # ---------------------------------------------------------------- infinities
@@ -60,3 +60,41 @@ def test_attention_rows_before_the_ring_stay_zero(tq, cap, d):
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
     done()
     assert np.isfinite(first[1][:, :, tq - cap:].cpu().numpy()).all()
+
+
+# ---------------------------------------------------------------- weights far below the largest
+def check_one_loud_key(tq, b, n, d, gap, kind):
+    """The first key's score is `gap` above all the others' and its value zero, so that the output is the others' alone.
+
+    Tolerance, relative to the output (all weights but one are equal): the result's rounding and that of the weights,
+    UNIT each, twice the latter for the mean; scores of at most gap, in base 2, off by 2^-22 of them; exponentials 2^-20.
+    fp16 weights are held against 2^7 or more times the largest (2^-24 is the spacing of the smallest there): 2^-32 each
+    against e^-gap."""
+    q = torch.ones(b, tq, 2, d, dtype=KINDS[kind][0], device="cuda")
+    k = torch.zeros(b, n, 1, d, dtype=KINDS[kind][0], device="cuda")
+    k[:, 0, :, 0] = gap
+    v = strided((b, n, 1, d), kind, 1, mean=512.0, scale=64.0)
+    v[:, 0] = 0
+    o, lse = torch.empty_like(q), torch.empty(b, 2, tq, device="cuda")
+    attention(q, k, v, o, lse, None, None, 0, 0, 1.0, kind)
+    done()
+    ref, ref_lse, mag, dots = tokens.window_attention(f64(q), f64(k), f64(v), [tq] * b, [n] * b, 0, 0, 1.0)
+    small = 2.0 ** -32 * np.exp(gap) if kind == "fp16" else 0.0
+    tol = (3 * UNIT[kind] + 2.0 ** -22 * gap * 2 + 2.0 ** -20 + small) * np.abs(ref) + TINY[kind]
+    assert_within(f64(o), ref, tol)
+    assert_within(lse.double().cpu().numpy(), ref_lse, np.full(ref_lse.shape, 2.0 ** -18))
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("gap", [10.0, 14.0, 16.875, 18.0])
+@pytest.mark.parametrize("d", [64, 80, 128])
+def test_attention_of_prompts_far_below_the_largest_score(d, gap, kind):
+    check_one_loud_key(500, 6, 1500, d, gap, kind)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("gap", [10.0, 14.0, 16.875, 18.0])
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("b,tq,n", [(2, 1, 16), (2, 1, 2000), (200, 1, 17), (3, 20, 60)])
+def test_attention_of_few_queries_far_below_the_largest_score(b, tq, n, d, gap, kind):
+    check_one_loud_key(tq, b, n, d, gap, kind)
