@@ -5,7 +5,7 @@
 #include <type_traits>
 
 #include "attn_row.cuh"
-#include "ptx.cuh"
+#include "token_ptx.cuh"
 #include "token.h"
 
 namespace oidnx {

@@ -4,7 +4,7 @@
 // tensor-core form falls back on for tiles whose values are no numbers.
 #pragma once
 
-#include "ptx.cuh"
+#include "token_ptx.cuh"
 #include "token.h"
 
 namespace oidnx {

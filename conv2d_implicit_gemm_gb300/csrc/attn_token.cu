@@ -17,7 +17,7 @@
 // latency; its 17 MB take 2.5 us.
 #include <type_traits>
 
-#include "ptx.cuh"
+#include "token_ptx.cuh"
 #include "token.h"
 
 namespace oidnx {

@@ -3,7 +3,7 @@
 // have given.
 #pragma once
 
-#include "ptx.cuh"
+#include "token_ptx.cuh"
 #include "token.h"
 
 namespace oidnx {

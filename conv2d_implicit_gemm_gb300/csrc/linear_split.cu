@@ -13,7 +13,7 @@
 #include <type_traits>
 
 #include "linear_load.cuh"
-#include "ptx.cuh"
+#include "token_ptx.cuh"
 #include "token.h"
 #include "token_math.cuh"
 

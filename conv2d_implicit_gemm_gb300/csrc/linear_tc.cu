@@ -24,7 +24,7 @@
 #include <climits>
 #include <type_traits>
 
-#include "ptx.cuh"
+#include "token_ptx.cuh"
 #include "token.h"
 #include "token_math.cuh"
 

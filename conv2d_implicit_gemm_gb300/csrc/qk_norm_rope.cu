@@ -14,7 +14,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "ptx.cuh"
+#include "token_ptx.cuh"
 #include "token.h"
 
 namespace oidnx {
