@@ -282,10 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         phase ^= 1u << h;
         tc_fence_after();
-        if (r == 0) {
-          mbar_arrive(&kempty[j % NS]);
-          if (j > 0) mbar_arrive(&vempty[(j - 1) % NS]);
-        }
+        mbar_arrive_if(r == 0, &kempty[j % NS]);
+        if (j > 0) mbar_arrive_if(r == 0, &vempty[(j - 1) % NS]);
         uint32_t raw[2][32];
         tmem_ld32_nowait(sc, raw[0]);
         tmem_ld32_nowait(sc + 32, raw[1]);
@@ -393,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           some ? (top * c - kLift<T> + log2f(sum)) * 0.69314718055994531f : -INFINITY;
     }
     fence_proxy_async_smem();
+    __syncwarp();  // (the barrier takes whole warps)
     named_barrier_sync(1 + t, 128);
     if (r == 0 && w.i0(t) < p.tq) {
 #pragma unroll

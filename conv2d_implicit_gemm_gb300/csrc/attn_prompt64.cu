@@ -230,10 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&sfull[chain], n & 1, p.status, kErrTimeoutEpilogue));
       if (!ok) break;
       tc_fence_after();
-      if (r == 0) {
-        mbar_arrive(&kempty[j % NS]);
-        if (j > 0) mbar_arrive(&vempty[(j - 1) % NS]);
-      }
+      mbar_arrive_if(r == 0, &kempty[j % NS]);
+      if (j > 0) mbar_arrive_if(r == 0, &vempty[(j - 1) % NS]);
       uint32_t raw[2][32];
       tmem_ld32_nowait(sc, raw[0]);
       tmem_ld32_nowait(sc + 32, raw[1]);
@@ -307,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&odone[t], 0, p.status, kErrTimeoutEpilogue));
     tc_fence_after();
     stats[chain * 128 + r] = make_float2(top, sum);
+    __syncwarp();  // (the barrier takes whole warps)
     named_barrier_sync(1 + t, 256);
     const float2 a = stats[2 * t * 128 + r], b = stats[(2 * t + 1) * 128 + r];
     const bool has_a = !(a.y == 0.f), has_b = !(b.y == 0.f);
@@ -340,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           some ? (both * c - kLift<T> + log2f(total)) * 0.69314718055994531f : -INFINITY;
     }
     fence_proxy_async_smem();
+    __syncwarp();
     named_barrier_sync(1 + t, 256);
     if (r == 0 && h == 0 && w.i0(t) < p.tq) {
       tma_store_4d(&map_o, out, 0, w.kvh * w.group, w.i0(t), w.b);

@@ -228,10 +228,7 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 2)
       }
     }
   }
-  if (split > 1) {
-    __syncwarp();
-    cluster_sync();  // a part stays until everyone has read it
-  }
+  if (split > 1) cluster_sync();  // a part stays until everyone has read it
 }
 
 template <typename T, int BN, bool GATHER>
