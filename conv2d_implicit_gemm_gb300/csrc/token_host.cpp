@@ -15,6 +15,7 @@ namespace oidnx {
 oidnx_status report_error(oidnx_status status, const char* message);
 oidnx_status report_ok();
 cudaError_t token_device(int* device, int* sms, int** status);
+cudaError_t token_pool(int device, cudaMemPool_t* pool);
 cudaError_t token_status_take(int* word, cudaStream_t stream);
 }  // namespace oidnx
 
@@ -74,30 +75,6 @@ bool matrix_map(CUtensorMap* map, bool bf16, const void* base, int64_t ld, int r
 bool tma_rows(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0 && ld < (int64_t(1) << 38); }
 
 // ---------------------------------------------------------------- linear: choice of form
-// Memory of one call, ordered on its stream, from a pool of the library's own
-// that keeps what it has been given (the default pool hands it back to the
-// system at every synchronisation).
-cudaError_t scratch_pool(int device, cudaMemPool_t* out) {
-  static std::mutex mutex;
-  static cudaMemPool_t pools[64] = {};
-  std::lock_guard<std::mutex> lock(mutex);
-  if (!pools[device]) {
-    cudaMemPoolProps props = {};
-    props.allocType = cudaMemAllocationTypePinned;
-    props.location.type = cudaMemLocationTypeDevice;
-    props.location.id = device;
-    cudaMemPool_t pool;
-    cudaError_t e = cudaMemPoolCreate(&pool, &props);
-    if (e != cudaSuccess) return e;
-    uint64_t keep = UINT64_MAX;
-    e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
-    if (e != cudaSuccess) return e;
-    pools[device] = pool;
-  }
-  *out = pools[device];
-  return cudaSuccess;
-}
-
 constexpr int kMostSplit = 65535 * 32;  // rows of a grid of the split form's gathering tiles
 
 // Few rows: K split over clusters, tokens as the narrow operand.
@@ -173,7 +150,7 @@ cudaError_t run_linear(const LinearParams& params, bool bf16, cudaStream_t strea
   const int64_t x_bytes = x_fits ? 0 : ld * p.m * 2, w_bytes = w_fits ? 0 : ld * p.n * 2;
   cudaMemPool_t pool;
   void* scratch = nullptr;
-  e = scratch_pool(L.device, &pool);
+  e = token_pool(L.device, &pool);
   if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&scratch, x_bytes + w_bytes, pool, stream);
   if (e != cudaSuccess) return e;
   AlignParams a = {};
@@ -497,12 +474,28 @@ constexpr int kMaxDevices = 64;
 struct DeviceInfo {
   int* status = nullptr;
   int sms = 0;
+  cudaMemPool_t pool = nullptr;
+  cudaError_t pool_error = cudaSuccess;
 };
 std::mutex g_device_mutex;
 DeviceInfo g_devices[kMaxDevices];
+
+// A pool of the library's own that keeps what it has been given (the default pool
+// hands it back to the system at every synchronisation).
+cudaError_t make_pool(int device, cudaMemPool_t* out) {
+  cudaMemPoolProps props = {};
+  props.allocType = cudaMemAllocationTypePinned;
+  props.location.type = cudaMemLocationTypeDevice;
+  props.location.id = device;
+  cudaError_t e = cudaMemPoolCreate(out, &props);
+  if (e != cudaSuccess) return e;
+  uint64_t keep = UINT64_MAX;
+  return cudaMemPoolSetAttribute(*out, cudaMemPoolAttrReleaseThreshold, &keep);
+}
 }  // namespace
 
-// The current device, its SM count and its error word (looked up once).
+// The current device, its SM count and its error word (looked up once, and the pool
+// made with them: it cannot be made while a stream is captured).
 cudaError_t oidnx::token_device(int* device, int* sms, int** status) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -523,12 +516,22 @@ cudaError_t oidnx::token_device(int* device, int* sms, int** status) {
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = cudaGetSymbolAddress(&p, g_token_status);
     if (e != cudaSuccess) return e;
+    d.pool_error = make_pool(dev, &d.pool);
+    if (d.pool_error != cudaSuccess) cudaGetLastError();  // only calls that need the pool fail
     d.status = static_cast<int*>(p);
   }
   *device = dev;
   *sms = d.sms;
   *status = d.status;
   return cudaSuccess;
+}
+
+// Memory of one call, ordered on its stream, comes from here.  The device's look-up
+// is behind the caller.
+cudaError_t oidnx::token_pool(int device, cudaMemPool_t* pool) {
+  std::lock_guard<std::mutex> lock(g_device_mutex);
+  *pool = g_devices[device].pool;
+  return g_devices[device].pool_error;
 }
 
 // Wait for `stream`, then read and clear the error word.

@@ -1,5 +1,5 @@
-"""Edges of the token operators: activations at infinity, prompts longer than a ring holds, weights far below the largest
-(tolerances and helpers of test_gpu_tokens.py)."""
+"""Edges of the token operators: activations at infinity, prompts longer than a ring holds, weights far below the largest,
+calls captured before they were ever made (tolerances and helpers of test_gpu_tokens.py)."""
 
 import numpy as np
 import pytest
@@ -98,3 +98,59 @@ def test_attention_of_prompts_far_below_the_largest_score(d, gap, kind):
 @pytest.mark.parametrize("b,tq,n", [(2, 1, 16), (2, 1, 2000), (200, 1, 17), (3, 20, 60)])
 def test_attention_of_few_queries_far_below_the_largest_score(b, tq, n, d, gap, kind):
     check_one_loud_key(tq, b, n, d, gap, kind)
+
+
+# ---------------------------------------------------------------- graph capture
+CAPTURE = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+from tests._tokens import attention, done, linear, norm_rope, strided
+
+def product(m, n, k, shift=0):
+    x, w = strided((m, k), "bf16", 1, None, shift), strided((n, k), "bf16", 2, None, shift)
+    y = torch.zeros(m, n, dtype=torch.bfloat16, device="cuda")
+    return y, lambda: linear(x, w, None, None, y, "silu", "bf16")
+
+def window(tq, cap, hq, hk, d):
+    q, k = strided((1, tq, hq, d), "bf16", 3), strided((1, cap, hk, d), "bf16", 4)
+    o = torch.zeros_like(q)
+    return o, lambda: attention(q, k, k, o, None, None, None, 300, 4, 0.125, "bf16")
+
+def norm(d):
+    q, k = strided((3, 4, d), "bf16", 5), strided((3, 2, d), "bf16", 6)
+    qo, ko = torch.zeros_like(q), torch.zeros_like(k)
+    return qo, lambda: norm_rope(q, qo, k, ko, None, None, None, None, 1e-6, None, None, None, None, 0, False, "bf16")
+
+calls = [product(9, 256, 256), product(60, 256, 512), product(128, 256, 2048), product(9, 256, 255),
+         product(100, 64, 255, 1), product(200, 64, 255, 1), product(300, 200, 256), product(3000, 3000, 512),
+         window(1, 900, 8, 2, 64), window(1, 900, 8, 2, 128), window(20, 90, 2, 2, 128), window(600, 900, 8, 2, 64),
+         window(600, 900, 8, 2, 128), window(3, 90, 2, 1, 63), window(3, 90, 2, 1, 256), norm(64), norm(72), norm(65)]
+norm(128)[1]()  # the one call on the device
+done()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    for out, call in calls:
+        call()
+for _ in range(2):
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [out.clone() for out, call in calls]
+    for out, call in calls:
+        out.zero_()
+for (out, call), g in zip(calls, got):
+    call()
+    done()
+    assert g.any() and torch.equal(g, out)
+print("captured")
+"""
+
+
+def test_every_form_can_be_captured_once_any_call_has_been_made():
+    """In a process of its own, whose one call before the capture is a norm."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", CAPTURE.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
