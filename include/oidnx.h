@@ -354,7 +354,8 @@ void oidnx_conv_release(oidnx_conv* c);
  * nothing is kept from one call for the next.  Nothing is allocated either,
  * but for linear layers of over 32 rows whose x or w has rows that do not start
  * on 16 bytes: these take memory for copies with rows that do, ordered on the
- * stream, from a pool of the library's own that keeps it for later calls.
+ * stream, from a pool of the library's own that keeps up to 1 GiB for later
+ * calls and gives what is beyond back when the host next waits for the GPU.
  * Strides and row lengths count elements.  Pointers need the alignment of
  * their elements only; 16-byte aligned pointers and strides of whole 16
  * bytes run the fast forms.  Sums, norms and softmax statistics are fp32 and

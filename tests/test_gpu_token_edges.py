@@ -1,5 +1,5 @@
 """Edges of the token operators: activations at infinity, prompts longer than a ring holds, weights far below the largest,
-calls captured before they were ever made (tolerances and helpers of test_gpu_tokens.py)."""
+calls captured before they were ever made, memory kept (tolerances and helpers of test_gpu_tokens.py)."""
 
 import numpy as np
 import pytest
@@ -154,3 +154,18 @@ def test_every_form_can_be_captured_once_any_call_has_been_made():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     run = subprocess.run([sys.executable, "-c", CAPTURE.format(root=root)], capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
+
+
+# ---------------------------------------------------------------- memory
+def test_memory_of_a_large_unaligned_product_is_given_back():
+    """Copies of 3 GiB: of these at most 1 GiB stays with the library once the GPU has been waited for."""
+    m, k = 3 * 2 ** 20, 511
+    x, w = torch.zeros(m, k, dtype=torch.float16, device="cuda"), torch.zeros(8, k, dtype=torch.float16, device="cuda")
+    y = torch.empty(m, 8, dtype=torch.float16, device="cuda")
+    linear(x[:64], w, None, None, y[:64], "none", "fp16")
+    done()
+    before = torch.cuda.mem_get_info()[0]
+    linear(x, w, None, None, y, "none", "fp16")
+    done()
+    assert before - torch.cuda.mem_get_info()[0] <= 1 << 30
+    assert not y.any()
