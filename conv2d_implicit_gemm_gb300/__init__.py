@@ -8,7 +8,8 @@ and streams are plain integers (e.g. ``tensor.data_ptr()`` and
 
 The calls made once a token (oidnx_linear, oidnx_qk_norm_rope,
 oidnx_window_attention) go through a small extension module, _calls, as
-converting their many arguments in ctypes takes longer than the launch.
+converting their many arguments in ctypes takes longer than the launch; where
+it is missing they take ctypes like the rest (_calls_ctypes).
 
 Importing fails loudly when the library has not been built (there is no
 fallback): build it with ``python conv2d_implicit_gemm_gb300/build.py``.
@@ -29,10 +30,9 @@ if not os.path.exists(_LIB_PATH):
 _lib = ctypes.CDLL(_LIB_PATH)
 try:
     from . import _calls
-except ImportError as e:
-    raise ImportError(
-        f"{os.path.join(os.path.dirname(_LIB_PATH), '_calls.so')} is missing or unusable ({e}): "
-        "build it with the library (python conv2d_implicit_gemm_gb300/build.py)") from e
+except ImportError:
+    from . import _calls_ctypes
+    _calls = _calls_ctypes.bind(_lib)
 
 OK = 0
 ERR_INVALID_ARGUMENT = 1

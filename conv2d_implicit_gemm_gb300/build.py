@@ -1,5 +1,6 @@
 """Build liboidnx.so (the C-ABI library) in-tree with nvcc for sm_103a, and
-_calls.so, the binding's entry of the per-token calls.
+_calls.abi3.so, the binding's faster entry of the per-token calls (not needed: without
+a C compiler or Python's headers the binding does without it).
 
 Usage: python conv2d_implicit_gemm_gb300/build.py   (run as a script: importing the
 package would load the library it is about to rebuild)
@@ -19,7 +20,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liboidnx.so")
-CALLS = os.path.join(PKG, "_calls.so")
+CALLS = os.path.join(PKG, "_calls.abi3.so")  # the stable ABI: for any interpreter from 3.10 on
 SOURCES = ["oidnx_host.cpp", "conv_tc.cu", "conv_pair.cu", "conv_final.cu", "conv_tail.cu",
            "conv_head.cu", "io_passes.cu", "noalloc.cu", "token_host.cpp", "linear_tc.cu", "linear_split.cu", "linear_align.cu",
            "qk_norm_rope.cu", "attn_any.cu", "attn_token.cu", "attn_prompt.cu", "attn_prompt64.cu"]
@@ -68,14 +69,23 @@ def build(verbose=False):
 
 
 def _build_calls():
-    """_calls.so: the Python entry of the per-token calls, linked to the library beside it."""
+    """The Python entry of the per-token calls, linked to the library beside it; False if it cannot be built."""
+    for stale in (CALLS, os.path.join(PKG, "_calls.so")):
+        if os.path.exists(stale):
+            os.remove(stale)
     tmp = CALLS + ".tmp"
     cmd = [shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"],
            os.path.join(CSRC, "calls.c"), "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"building {CALLS} failed:\n{res.stdout}\n{res.stderr}")
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        failed = f"status {res.returncode}\n{res.stdout}{res.stderr}" if res.returncode else ""
+    except OSError as e:
+        failed = str(e)
+    if failed:
+        sys.stderr.write(f"{os.path.basename(CALLS)} could not be built, the per-token calls go through ctypes:\n{failed}\n")
+        return False
     os.replace(tmp, CALLS)
+    return True
 
 
 if __name__ == "__main__":

@@ -1,5 +1,6 @@
 """Edges of the token operators: activations at infinity, prompts longer than a ring holds, weights far below the largest,
-calls captured before they were ever made, memory kept (tolerances and helpers of test_gpu_tokens.py)."""
+calls captured before they were ever made, memory kept, calls through ctypes (tolerances and helpers of
+test_gpu_tokens.py)."""
 
 import numpy as np
 import pytest
@@ -8,7 +9,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 from oracle import tokens
-from tests._tokens import ACTS, KINDS, TINY, UNIT, attention, done, f64, linear, strided
+from tests._tokens import ACTS, KINDS, TINY, UNIT, attention, done, f64, linear, norm_rope, strided
 from tests.test_gpu_tokens import assert_within, check_attention
 
 
@@ -169,3 +170,23 @@ def test_memory_of_a_large_unaligned_product_is_given_back():
     done()
     assert before - torch.cuda.mem_get_info()[0] <= 1 << 30
     assert not y.any()
+
+
+# ---------------------------------------------------------------- entries
+def test_calls_through_ctypes_give_the_same_results(monkeypatch):
+    """What the package does without its extension module."""
+    import conv2d_implicit_gemm_gb300 as ox
+    from conv2d_implicit_gemm_gb300 import _calls_ctypes
+    x, w = strided((9, 256), "bf16", 1), strided((64, 256), "bf16", 2)
+    q, k = strided((3, 5, 8, 64), "bf16", 3), strided((3, 70, 2, 64), "bf16", 4)
+    results = []
+    for calls in (ox._calls, _calls_ctypes.bind(ox._lib)):
+        monkeypatch.setattr(ox, "_calls", calls)
+        y, o, lse = torch.empty(9, 64, dtype=x.dtype, device="cuda"), torch.empty_like(q), torch.empty(3, 8, 5, device="cuda")
+        qo, ko = torch.empty_like(q[0]), torch.empty_like(k[0])
+        linear(x, w, None, None, y, "silu", "bf16")
+        attention(q, k, k, o, lse, None, None, 30, 2, 0.125, "bf16")
+        norm_rope(q[0], qo, k[0, :5], ko, None, None, None, None, 1e-6, None, None, None, None, 0, False, "bf16")
+        done()
+        results.append((y, o, lse, qo, ko[:5]))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
