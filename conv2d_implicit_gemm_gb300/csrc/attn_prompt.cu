@@ -282,8 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         phase ^= 1u << h;
         tc_fence_after();
-        mbar_arrive_if(r == 0, &kempty[j % NS]);
-        if (j > 0) mbar_arrive_if(r == 0, &vempty[(j - 1) % NS]);
+        if ((warp & 3) == 0) {  // (whole warps: what follows reads tensor memory)
+          mbar_arrive_if(lane == 0, &kempty[j % NS]);
+          if (j > 0) mbar_arrive_if(lane == 0, &vempty[(j - 1) % NS]);
+        }
         uint32_t raw[2][32];
         tmem_ld32_nowait(sc, raw[0]);
         tmem_ld32_nowait(sc + 32, raw[1]);

@@ -20,10 +20,9 @@ __device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, i
 }
 
 // An arrival of the threads that `who` holds for, without a branch: the warp stays
-// together for the instructions behind it that it executes as a whole.  (8192
-// tokens, window 2048, 16 heads of 128 over 4: 108.4 us; with a branch and a
-// __syncwarp 109.4, with the branch alone 109.1.  2 x 4096 causal, 8 heads of 64:
-// 46.7, 46.7, 46.2.)
+// together for the instructions behind it that it executes as a whole.  (In the
+// prompts' softmax, 8192 tokens, window 2048, 16 heads of 128 over 4: 107.2 us; with a
+// branch and a __syncwarp 108.)
 __device__ __forceinline__ void mbar_arrive_if(bool who, uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
