@@ -113,7 +113,9 @@ cudaError_t run_tiles(LinearTcLaunch& L, bool bf16, cudaStream_t stream) {
     const int64_t cost = (tiles + slots - 1) / slots * (blocks * f.block + 1500) + 28 * f.cols + 1200 * f.pair;
     if (cost < best) best = cost, L.pair = f.pair, L.bn = f.cols;
   }
-  L.tma_out = tma_rows(p.y, p.ldy) && (!p.residual || tma_rows(p.residual, p.ldr));
+  // TMA stores whole 16-byte pieces: one that the matrix ends in would be written
+  // beyond it, whatever the map says of the row's length.
+  L.tma_out = p.n % 8 == 0 && tma_rows(p.y, p.ldy) && (!p.residual || tma_rows(p.residual, p.ldr));
   const int cols = L.bn == 64 ? 32 : 64;
   const bool ok = matrix_map(&L.map_x, bf16, p.x, p.ldx, p.m, p.k, 128, 64) &&
                   matrix_map(&L.map_w, bf16, p.w, p.ldw, p.n, p.k, L.pair ? L.bn / 2 : L.bn, 64) &&

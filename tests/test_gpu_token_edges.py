@@ -1,6 +1,6 @@
-"""Edges of the token operators: activations at infinity, prompts longer than a ring holds, weights far below the largest,
-calls captured before they were ever made, memory kept, calls through ctypes (tolerances and helpers of
-test_gpu_tokens.py)."""
+"""Edges of the token operators: activations at infinity, aligned rows that end within 16 bytes, prompts longer than a ring
+holds, weights far below the largest, calls captured before they were ever made, memory kept, calls through ctypes
+(tolerances and helpers of test_gpu_tokens.py)."""
 
 import numpy as np
 import pytest
@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 
 from oracle import tokens
 from tests._tokens import ACTS, KINDS, TINY, UNIT, attention, done, f64, linear, norm_rope, strided
-from tests.test_gpu_tokens import assert_within, check_attention
+from tests.test_gpu_tokens import assert_within, check_attention, check_linear
 
 
 # ---------------------------------------------------------------- infinities
@@ -31,6 +31,22 @@ def test_linear_activations_at_infinity(m, k, act, kind):
     got = f64(y)
     for what in (np.isnan, np.isposinf, np.isneginf):
         np.testing.assert_array_equal(what(got), what(ref))
+
+
+# ---------------------------------------------------------------- aligned rows that end within 16 bytes
+@pytest.mark.parametrize("residual,inplace", [(False, False), (True, False), (True, True)])
+@pytest.mark.parametrize("n,pad", [(1, 7), (7, 1), (45, 3), (130, 6), (133, 131), (1001, 7)])
+@pytest.mark.parametrize("m", [3, 40, 140, 600])
+def test_linear_writes_no_value_behind_its_rows(m, n, pad, residual, inplace):
+    """Rows of whole 16 bytes in memory, of which the output takes a part: what lies behind it stays."""
+    check_linear(m, n, 64, "fp16" if m % 40 else "bf16", "gelu", residual=residual, inplace=inplace, pad=pad, seed=n)
+
+
+@pytest.mark.parametrize("k,pad", [(1, 7), (7, 1), (45, 3), (130, 6), (133, 131)])
+@pytest.mark.parametrize("m", [3, 40, 140, 600])
+def test_linear_reads_no_value_behind_its_rows(m, k, pad):
+    """The same of the operands: NaN lies behind each row."""
+    check_linear(m, 72, k, "fp16", "none", pad=pad, seed=k)
 
 
 # ---------------------------------------------------------------- prompts longer than the ring
