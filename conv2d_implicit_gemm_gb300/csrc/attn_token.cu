@@ -5,16 +5,17 @@
 // them) go through warp-level products m16n8k16, which are far from being
 // the limit here; every key is read once for all of them.  The visible keys
 // (sinks, then the window, one wrap of the ring) are numbered through and cut
-// into chunks of 16; the CTAs of a cluster take contiguous parts, the four
+// into chunks of 16; the CTAs of a cluster take contiguous parts, the eight
 // warps of a CTA take turns.  A warp copies its own chunks (cp.async, three
 // in flight) and keeps its own running maximum, sum and output, so that no
 // barrier stands in the loop; warps are joined in shared memory at the end and
 // CTAs over the cluster, always in the same order.
 //
 // 64 ragged streams of one token, 8 key heads of 128, window 4096: 133 us, 5.95
-// TB/s, 88% of the measured copy rate.  One stream over 4100 slots: 11.6 us, of
-// which the launch, the lengths, two rounds of the ring and the joining are
-// latency; its 17 MB take 2.5 us.
+// TB/s, 88% of the measured copy rate.  One stream over 4100 slots: 11.6 us, where
+// its 17 MB take 2.5 at that rate: the launch, the lengths, two rounds of the ring
+// and the joining are latency, and eight CTAs a key head leave 88 of 152 SMs idle.
+// 32768 slots, a CTA's 56 GB/s being the bound: 43 us with 1, 2 or 8 key heads.
 #include <type_traits>
 
 #include "token_ptx.cuh"

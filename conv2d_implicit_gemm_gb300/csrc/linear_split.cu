@@ -7,9 +7,10 @@
 // 128 / split rows over the parts (always in the same order) and applies the
 // epilogue.
 //
-// 1 x 4096 x 4096: 9.7 us on the device (3.9 of them at any size: launch, first
-// loads, joining; the rest streams the weight at 5.8 TB/s); 1 x 8192 x 8192: 24 us,
-// 5.6 TB/s.  Rows that do not start on 16 bytes: 15.4 us for 1 x 4096 x 4095.
+// 1 x 4096 x 4096: 9.3 us on the device, 10.2 with bias and residual (3.9 of them at
+// any size: launch, first loads, joining; the rest streams the weight at 5.8 TB/s);
+// 1 x 8192 x 8192: 23.6 us, 5.7 TB/s.  Rows that do not start on 16 bytes: 15.7 us for
+// 1 x 4096 x 4095, their copies and shifts being two passes through shared memory.
 #include <type_traits>
 
 #include "linear_load.cuh"

@@ -157,7 +157,8 @@ __device__ __forceinline__ bool epilogue_tma(const TcArgs& a, const CUtensorMap*
 
 // Outputs that TMA cannot store: tiles of 32 rows x W columns through shared
 // memory, each row in words as its own alignment asks for (2040 x 1001 x 1000 with
-// residual 15.2 us, aligned 13.9; by single 16-bit values 18.8).  With s = 1 where the
+// residual 14.7 us, 2040 x 1000 x 1000 through TMA 13.6; by single 16-bit values 18.8).
+// Rows on 16 bytes that end within 16 (1001 values of 1008): 14.4.  With s = 1 where the
 // row starts on an odd 16-bit place (0 else), word l holds columns 2 l - s and
 // 2 l - s + 1, so that a warp reads and writes whole words; column 0 of s = 1 and
 // a last column that no pair takes go alone, one lane a row.

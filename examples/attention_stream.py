@@ -1,6 +1,6 @@
 """An attention block over endless token streams, from the token operators.
 
-Each stream sends a few tokens at a time (the tokens of a frame's bottleneck map, or one token a frame).  A step projects
+Each stream sends a few tokens at a time (a few for each frame, say); random ones here.  A step projects
 them to queries, keys and values (oidnx_linear), norms and rotates the heads and appends keys and values to the stream's
 ring cache (oidnx_qk_norm_rope), attends over the first tokens and a sliding window (oidnx_window_attention), and ends in
 the output projection and a feed-forward pair, each with its residual in the same call.  The cache holds

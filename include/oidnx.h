@@ -348,7 +348,9 @@ void oidnx_conv_release(oidnx_conv* c);
  * bottleneck map, or one token per frame along a stream): a linear layer, the
  * norm and rotation of queries and keys with their append to a cache, and
  * attention with a sliding window and sinks over that cache.  The pages have
- * no counterpart of these calls; they are an addition of this library.
+ * no counterpart of these calls; they are an addition of this library.  Tokens
+ * are rows of values that the caller has: a filter neither exposes its
+ * bottleneck map nor lays it out in rows.
  *
  * For all of them: direct calls on device pointers, enqueued on `stream`;
  * nothing is kept from one call for the next.  Nothing is allocated either,
@@ -359,11 +361,15 @@ void oidnx_conv_release(oidnx_conv* c);
  * Strides and row lengths count elements.  Pointers need the alignment of
  * their elements only; 16-byte aligned pointers and strides of whole 16
  * bytes run the fast forms.  Sums, norms and softmax statistics are fp32 and
- * each output is rounded once.  The caller keeps every buffer alive until
+ * each output is rounded once; attention's weights are rounded once more, to the
+ * storage type, before their product with the values (fp16 ones relative to 2^7
+ * times the largest or more, so that those down to 2^-21 of it lose no bits).
+ * Nothing is written between the rows of an output.  The caller keeps every buffer alive until
  * the work on `stream` is done, and orders the call after whatever wrote its
  * inputs on other streams.  Calls can be captured into a CUDA graph once one
- * call has been made on the device.  A device-side timeout is reported by
- * oidnx_token_sync_status.  Sizes beyond 2^30 are UNSUPPORTED.  */
+ * call has been made on the device.  A device-side timeout (two seconds without
+ * progress; a single tile of a product of some 5e8 terms a value takes as long)
+ * is reported by oidnx_token_sync_status.  Sizes beyond 2^30 are UNSUPPORTED.  */
 
 enum { OIDNX_ACT_NONE = 0, OIDNX_ACT_RELU = 1, OIDNX_ACT_GELU = 2 /* erf */,
        OIDNX_ACT_GELU_TANH = 3, OIDNX_ACT_SILU = 4 };
