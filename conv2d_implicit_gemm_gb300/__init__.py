@@ -7,7 +7,8 @@ and streams are plain integers (e.g. ``tensor.data_ptr()`` and
 ``OidnxError`` carrying the status code and ``oidnx_last_error()``.
 
 The calls made once a token (oidnx_linear, oidnx_qk_norm_rope,
-oidnx_window_attention) go through a small extension module, _calls, as
+oidnx_window_attention, oidnx_block_norm, oidnx_qk_norm_rope_axes,
+oidnx_cross_attention) go through a small extension module, _calls, as
 converting their many arguments in ctypes takes longer than the launch; where
 it is missing they take ctypes like the rest (_calls_ctypes).
 
@@ -46,6 +47,8 @@ ERR_NOT_COMMITTED = 8
 
 IMAGE_COLOR, IMAGE_ALBEDO, IMAGE_NORMAL, IMAGE_OUTPUT = 0, 1, 2, 3
 PRECISION_AUTO, PRECISION_FP32, PRECISION_FP16, PRECISION_BF16 = 0, 1, 2, 3
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+GATE_PLAIN, GATE_TANH, GATE_SIGMOID = 0, 1, 2
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 TRANSFER_PU, TRANSFER_LOG = 0, 1
 
@@ -282,6 +285,39 @@ def oidnx_window_attention(q, q_sb, q_st, q_sh, k, k_sb, k_st, k_sh, v, v_sb, v_
     _check(_calls.oidnx_window_attention(q, q_sb, q_st, q_sh, k, k_sb, k_st, k_sh, v, v_sb, v_st,
                                        v_sh, o, o_sb, o_st, o_sh, lse, q_lens, kv_lens, b, tq, cap,
                                        hq, hk, d, window, sinks, scale, precision, stream))
+
+
+def oidnx_block_norm(x, ldx, residual, ldr, sum, ld_sum, y, ldy, post, post_weight, post_bias, pre, pre_weight,
+                     pre_bias, eps, gate, ldg, gate_act, scale, lds, shift, ldh, groups, per, count,
+                     residual_scale, branch_scale, t, n, precision, sum_precision=PRECISION_AUTO, stream=0):
+    """Norm after a branch, its gate, the residual, and the norm before the next branch; residual, sum, y,
+    weights, biases, gate, scale, shift and groups may be 0."""
+    _check(_calls.oidnx_block_norm(x, ldx, residual, ldr, sum, ld_sum, y, ldy, post, post_weight, post_bias, pre,
+                                   pre_weight, pre_bias, eps, gate, ldg, gate_act, scale, lds, shift, ldh, groups,
+                                   per, count, residual_scale, branch_scale, t, n, precision, sum_precision, stream))
+
+
+def oidnx_qk_norm_rope_axes(q, q_st, q_sh, q_out, qo_st, qo_sh, k, k_st, k_sh, k_out, ko_st, ko_sh,
+                            v, v_st, v_sh, v_out, vo_st, vo_sh, norm, q_weight, k_weight, eps, cos_table,
+                            sin_table, table_rows, positions, positions_stride, axes, pair_axes, slots,
+                            cache_rows, t, hq, hk, d, rot, interleaved, precision, stream=0):
+    """oidnx_qk_norm_rope with a position an axis: pair_axes is a bytes object of rot / 2 axis numbers."""
+    if len(pair_axes) < rot // 2:
+        raise ValueError(f"pair_axes holds {len(pair_axes)} of {rot // 2} pairs")
+    _check(_calls.oidnx_qk_norm_rope_axes(q, q_st, q_sh, q_out, qo_st, qo_sh, k, k_st, k_sh, k_out, ko_st, ko_sh,
+                                          v, v_st, v_sh, v_out, vo_st, vo_sh, norm, q_weight, k_weight, eps,
+                                          cos_table, sin_table, table_rows, positions, positions_stride, axes,
+                                          pair_axes, slots, cache_rows, t, hq, hk, d, rot, interleaved, precision,
+                                          stream))
+
+
+def oidnx_cross_attention(q, q_sb, q_st, q_sh, k, k_sb, k_st, k_sh, v, v_sb, v_st, v_sh, o, o_sb, o_st, o_sh,
+                          lse, q_lens, kv_lens, mask, mask_sb, b, tq, kv, hq, hk, d, scale, precision, stream=0):
+    """Attention to keys and values of another length, with a mask over them; lse, q_lens, kv_lens and mask
+    may be 0."""
+    _check(_calls.oidnx_cross_attention(q, q_sb, q_st, q_sh, k, k_sb, k_st, k_sh, v, v_sb, v_st, v_sh, o, o_sb,
+                                        o_st, o_sh, lse, q_lens, kv_lens, mask, mask_sb, b, tq, kv, hq, hk, d,
+                                        scale, precision, stream))
 
 
 def oidnx_token_sync_status(stream=0):

@@ -8,11 +8,14 @@ import ctypes
 import operator
 import types
 
-# one letter an argument: p pointer, l long long, i int, f float
+# one letter an argument: p pointer, l long long, i int, f float, b bytes
 KINDS = {"oidnx_linear": "plplpplpliiiiip",
          "oidnx_qk_norm_rope": "pllpllpllpllpllpllppfpplppliiiiiiip",
-         "oidnx_window_attention": "plllplllplllplllpppiiiiiiiifip"}
-_TYPES = {"p": ctypes.c_void_p, "l": ctypes.c_longlong, "i": ctypes.c_int, "f": ctypes.c_float}
+         "oidnx_window_attention": "plllplllplllplllpppiiiiiiiifip",
+         "oidnx_block_norm": "plplplplippippfpliplplpiiffiiiip",
+         "oidnx_qk_norm_rope_axes": "pllpllpllpllpllpllippfpplplibpliiiiiiip",
+         "oidnx_cross_attention": "plllplllplllplllppppliiiiiifip"}
+_TYPES = {"p": ctypes.c_void_p, "b": ctypes.c_char_p, "l": ctypes.c_longlong, "i": ctypes.c_int, "f": ctypes.c_float}
 _RANGE = {"p": (0, 2 ** 64 - 1), "l": (-2 ** 63, 2 ** 63 - 1), "i": (-2 ** 31, 2 ** 31 - 1)}
 
 
@@ -23,8 +26,12 @@ def _convert(name, kinds, args):
     for n, (kind, a) in enumerate(zip(kinds, args)):
         if kind == "f":
             out.append(float(a))
-        elif kind == "p" and a is None:
+        elif kind in "pb" and a is None:
             out.append(None)
+        elif kind == "b":
+            if not isinstance(a, bytes):
+                raise TypeError(f"{name}: argument {n + 1} is no bytes object")
+            out.append(a)
         else:
             v, (low, high) = operator.index(a), _RANGE[kind]
             if not low <= v <= high:
@@ -34,7 +41,7 @@ def _convert(name, kinds, args):
 
 
 def bind(lib):
-    """The three calls of the loaded library, each by position and returning the status."""
+    """The calls of the loaded library, each by position and returning the status."""
     calls = types.SimpleNamespace()
     for name, kinds in KINDS.items():
         fn = getattr(lib, name)

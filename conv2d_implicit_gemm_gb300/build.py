@@ -23,7 +23,8 @@ LIB = os.path.join(PKG, "liboidnx.so")
 CALLS = os.path.join(PKG, "_calls.abi3.so")  # the stable ABI: for any interpreter from 3.10 on
 SOURCES = ["oidnx_host.cpp", "conv_tc.cu", "conv_pair.cu", "conv_final.cu", "conv_tail.cu",
            "conv_head.cu", "io_passes.cu", "noalloc.cu", "token_host.cpp", "linear_tc.cu", "linear_split.cu", "linear_align.cu",
-           "qk_norm_rope.cu", "attn_any.cu", "attn_token.cu", "attn_prompt.cu", "attn_prompt64.cu"]
+           "qk_norm_rope.cu", "attn_any.cu", "attn_token.cu", "attn_prompt.cu", "attn_prompt64.cu",
+           "block_host.cpp", "block_norm.cu", "cross_tile.cu", "cross_token.cu", "heads_copy.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

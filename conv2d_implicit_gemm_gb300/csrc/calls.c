@@ -1,5 +1,5 @@
 /* Python entry of the calls made once a token: the same C functions that the
- * ctypes binding reaches, with their (up to 35) arguments converted here, which
+ * ctypes binding reaches, with their (up to 39) arguments converted here, which
  * takes 0.5 us instead of 3.  Only the stable ABI is used, so that one build
  * serves every interpreter from 3.10 on.  Each takes its C function's arguments by
  * position (None: a NULL pointer) and returns the status. */
@@ -11,7 +11,7 @@
 
 #include "../../include/oidnx.h"
 
-/* One letter an argument: p pointer, l long long, i int, f float. */
+/* One letter an argument: p pointer, l long long, i int, f float, b bytes. */
 typedef union {
   void* p;
   long long l;
@@ -33,9 +33,14 @@ static int convert(const char* name, const char* kinds, PyObject* const* args, P
       out[k].f = (float)v;
       continue;
     }
-    if (kinds[k] == 'p') {
+    if (kinds[k] == 'p' || kinds[k] == 'b') {
       if (a == Py_None) {
         out[k].p = NULL;
+        continue;
+      }
+      if (kinds[k] == 'b') {
+        out[k].p = PyBytes_AsString(a);  /* alive as long as the caller's argument */
+        if (!out[k].p) return 0;
         continue;
       }
       const unsigned long long v = PyLong_AsUnsignedLongLong(a);
@@ -97,10 +102,56 @@ static PyObject* window_attention(PyObject* self, PyObject* const* args, Py_ssiz
   return PyLong_FromLong(s);
 }
 
+static PyObject* block_norm(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  Arg a[32];
+  oidnx_status s;
+  (void)self;
+  if (!convert("oidnx_block_norm", "plplplplippippfpliplplpiiffiiiip", args, n, a)) return NULL;
+  Py_BEGIN_ALLOW_THREADS;
+  s = oidnx_block_norm(a[0].p, a[1].l, a[2].p, a[3].l, a[4].p, a[5].l, a[6].p, a[7].l, a[8].i, a[9].p, a[10].p, a[11].i,
+                       a[12].p, a[13].p, a[14].f, a[15].p, a[16].l, a[17].i, a[18].p, a[19].l,
+                       a[20].p, a[21].l, a[22].p, a[23].i, a[24].i, a[25].f, a[26].f, a[27].i,
+                       a[28].i, a[29].i, a[30].i, a[31].p);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(s);
+}
+
+static PyObject* qk_norm_rope_axes(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  Arg a[39];
+  oidnx_status s;
+  (void)self;
+  if (!convert("oidnx_qk_norm_rope_axes", "pllpllpllpllpllpllippfpplplibpliiiiiiip", args, n, a)) return NULL;
+  Py_BEGIN_ALLOW_THREADS;
+  s = oidnx_qk_norm_rope_axes(a[0].p, a[1].l, a[2].l, a[3].p, a[4].l, a[5].l, a[6].p, a[7].l, a[8].l, a[9].p, a[10].l, a[11].l,
+                              a[12].p, a[13].l, a[14].l, a[15].p, a[16].l, a[17].l, a[18].i,
+                              a[19].p, a[20].p, a[21].f, a[22].p, a[23].p, a[24].l, a[25].p,
+                              a[26].l, a[27].i, a[28].p, a[29].p, a[30].l, a[31].i, a[32].i,
+                              a[33].i, a[34].i, a[35].i, a[36].i, a[37].i, a[38].p);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(s);
+}
+
+static PyObject* cross_attention(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  Arg a[30];
+  oidnx_status s;
+  (void)self;
+  if (!convert("oidnx_cross_attention", "plllplllplllplllppppliiiiiifip", args, n, a)) return NULL;
+  Py_BEGIN_ALLOW_THREADS;
+  s = oidnx_cross_attention(a[0].p, a[1].l, a[2].l, a[3].l, a[4].p, a[5].l, a[6].l, a[7].l, a[8].p, a[9].l, a[10].l, a[11].l,
+                            a[12].p, a[13].l, a[14].l, a[15].l, a[16].p, a[17].p, a[18].p, a[19].p,
+                            a[20].l, a[21].i, a[22].i, a[23].i, a[24].i, a[25].i, a[26].i, a[27].f,
+                            a[28].i, a[29].p);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(s);
+}
+
 static PyMethodDef methods[] = {
     {"oidnx_linear", (PyCFunction)(void (*)(void))linear, METH_FASTCALL, NULL},
     {"oidnx_qk_norm_rope", (PyCFunction)(void (*)(void))qk_norm_rope, METH_FASTCALL, NULL},
     {"oidnx_window_attention", (PyCFunction)(void (*)(void))window_attention, METH_FASTCALL, NULL},
+    {"oidnx_block_norm", (PyCFunction)(void (*)(void))block_norm, METH_FASTCALL, NULL},
+    {"oidnx_qk_norm_rope_axes", (PyCFunction)(void (*)(void))qk_norm_rope_axes, METH_FASTCALL, NULL},
+    {"oidnx_cross_attention", (PyCFunction)(void (*)(void))cross_attention, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", NULL, -1, methods, NULL, NULL, NULL, NULL};

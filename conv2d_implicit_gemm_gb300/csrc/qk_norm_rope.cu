@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "token_math.cuh"
 #include "token_ptx.cuh"
 #include "token.h"
 
@@ -26,14 +27,6 @@ constexpr int kVecThreads = 128;
 constexpr int kCtasPerSm = 6;  // 80 registers a thread; at 5 and 7 (spills) 81 and 77 us where 6 take 76
 
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7FC00000); }
-
-// 1 / sqrt(x) to fp32's last place or two: the hardware's 2^-22 and one Newton
-// step.  Zero and infinity keep the hardware's answer (infinity and zero).
-__device__ __forceinline__ float inverse_root(float x) {
-  const float r = rsqrtf(x);
-  const float e = fmaf(-x * r, r, 1.f);
-  return x > 0.f && x < INFINITY ? fmaf(0.5f * r, e, r) : r;
-}
 
 // Pairs of fp32 values, two operations an instruction.
 __device__ __forceinline__ uint64_t f2(float a, float b) {
@@ -125,8 +118,11 @@ template <typename T, int P> struct Pairs {
 //   LPH   lanes a head: a power of two, or 0: d / 2P of them, packed into warps
 // A warp takes one token's position, row and rotation once, then `steps` times
 // as many heads as it has lanes for, the next ones on their way meanwhile.
-template <typename T, int P, int LPH, bool IL>
-__global__ void __launch_bounds__(kVecThreads, kCtasPerSm) qk_norm_rope_vec_kernel(const NormParams p, const int chunks, const int steps) {
+// With a position an axis (AxesParams) a lane's four pairs of one axis take a
+// vector of the table's row; pairs of several axes one value each.
+template <typename T, int P, int LPH, bool IL, typename Params>
+__global__ void __launch_bounds__(kVecThreads, kCtasPerSm) qk_norm_rope_vec_kernel(const __grid_constant__ Params p, const int chunks, const int steps) {
+  constexpr bool AXES = std::is_same<Params, AxesParams>::value;
   using Raw = typename Pairs<T, P>::Raw;
   const int lanes = LPH ? LPH : p.d / (2 * P);
   const int per_warp = 32 / lanes;
@@ -146,7 +142,12 @@ __global__ void __launch_bounds__(kVecThreads, kCtasPerSm) qk_norm_rope_vec_kern
   const int first = static_cast<int>(item - static_cast<unsigned>(token) * static_cast<unsigned>(chunks)) * steps * per_warp;  // head
   const int last = group < per_warp ? min(total, first + steps * per_warp) : 0;  // lanes beyond the groups have none
   const int row = p.slots ? p.slots[token] : token;  // of the keys and values
-  const int pos = p.rot ? p.positions[token] : 0;
+  int pos = 0;
+  if constexpr (AXES) {
+    if (p.rot && wl < p.axes) pos = p.positions[wl * p.positions_stride + token];  // lane a: that of axis a
+  } else {
+    pos = p.rot ? p.positions[token] : 0;
+  }
 
   // the head that is fetched next, one step ahead of the one at work
   const auto kind_of = [&](int h) { return h < hq ? 0 : h < hq + hk ? 1 : 2; };
@@ -170,7 +171,38 @@ __global__ void __launch_bounds__(kVecThreads, kCtasPerSm) qk_norm_rope_vec_kern
   };
   fetch();
   float4 c[P / 4], s[P / 4];
-  if (j < half) {
+  if constexpr (AXES) {
+#pragma unroll
+    for (int i = 0; i < P / 4; ++i) {
+      const uint32_t axis = j < half ? *reinterpret_cast<const uint32_t*>(p.pair_axis + j + 4 * i) : 0u;
+      const bool one = axis == (axis & 0xFFu) * 0x01010101u;
+      const bool all = __all_sync(0xFFFFFFFFu, one);
+      int at[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) at[k] = k == 0 || !all ? __shfl_sync(0xFFFFFFFFu, pos, axis >> (8 * k) & 0xFFu) : at[0];
+      float cv[4], sv[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) cv[k] = sv[k] = quiet_nan();
+      if (j < half && one) {
+        if (at[0] >= 0 && at[0] < p.table_rows) {
+          const int64_t o = at[0] * static_cast<int64_t>(half) + j + 4 * i;
+          const float4 cc = __ldg(reinterpret_cast<const float4*>(p.cos_t + o)), ss = __ldg(reinterpret_cast<const float4*>(p.sin_t + o));
+          cv[0] = cc.x, cv[1] = cc.y, cv[2] = cc.z, cv[3] = cc.w;
+          sv[0] = ss.x, sv[1] = ss.y, sv[2] = ss.z, sv[3] = ss.w;
+        }
+      } else if (j < half) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (at[k] >= 0 && at[k] < p.table_rows) {
+            const int64_t o = at[k] * static_cast<int64_t>(half) + j + 4 * i + k;
+            cv[k] = __ldg(p.cos_t + o), sv[k] = __ldg(p.sin_t + o);
+          }
+        }
+      }
+      c[i] = make_float4(cv[0], cv[1], cv[2], cv[3]);
+      s[i] = make_float4(sv[0], sv[1], sv[2], sv[3]);
+    }
+  } else if (j < half) {
     const bool known = pos >= 0 && pos < p.table_rows;
     const int64_t o = static_cast<int64_t>(pos) * half + j;
 #pragma unroll
@@ -223,10 +255,14 @@ __global__ void __launch_bounds__(kVecThreads, kCtasPerSm) qk_norm_rope_vec_kern
     }
     if (kind > 0 && !kept) continue;
     if (kind < 2) {
-      const float r = inverse_root(fmaf(sum, inv_d, p.eps));
-      const uint64_t r2 = f2(r, r);
+      bool normed = true;
+      if constexpr (AXES) normed = p.norm;
+      if (normed) {
+        const float r = inverse_root(fmaf(sum, inv_d, p.eps));
+        const uint64_t r2 = f2(r, r);
 #pragma unroll
-      for (int i = 0; i < P / 2; ++i) a[i] = mul2(a[i], r2), b[i] = mul2(b[i], r2);
+        for (int i = 0; i < P / 2; ++i) a[i] = mul2(a[i], r2), b[i] = mul2(b[i], r2);
+      }
       if (weighted) {
         uint64_t wa[P / 2], wb[P / 2];
         weight.template unpack<IL>(wa, wb);
@@ -251,8 +287,9 @@ __global__ void __launch_bounds__(kVecThreads, kCtasPerSm) qk_norm_rope_vec_kern
 }
 
 // Any alignment, stride or even head size: one warp per head, single values.
-template <typename T>
-__global__ void __launch_bounds__(kAnyThreads) qk_norm_rope_any_kernel(const NormParams p) {
+template <typename T, typename Params>
+__global__ void __launch_bounds__(kAnyThreads) qk_norm_rope_any_kernel(const __grid_constant__ Params p) {
+  constexpr bool AXES = std::is_same<Params, AxesParams>::value;
   const int lane = threadIdx.x & 31;
   const int hq = p.heads[0], hk = p.heads[1], total = hq + hk + p.heads[2];
   const int token = blockIdx.x;
@@ -270,8 +307,12 @@ __global__ void __launch_bounds__(kAnyThreads) qk_norm_rope_any_kernel(const Nor
     for (int i = lane; i < p.d; i += 32) dst[i] = src[i];
     return;
   }
-  const int pos = p.rot ? p.positions[token] : 0;
-  const bool known = pos >= 0 && pos < p.table_rows;
+  int pos = 0;
+  bool known = true;
+  if constexpr (!AXES) {
+    pos = p.rot ? p.positions[token] : 0;
+    known = pos >= 0 && pos < p.table_rows;
+  }
   float sum = 0.f;
   for (int i = lane; i < p.d; i += 32) {
     const float v = to_f32<T>(src[i]);
@@ -279,7 +320,8 @@ __global__ void __launch_bounds__(kAnyThreads) qk_norm_rope_any_kernel(const Nor
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  const float r = 1.0f / sqrtf(sum / static_cast<float>(p.d) + p.eps);
+  float r = 1.0f / sqrtf(sum / static_cast<float>(p.d) + p.eps);
+  if constexpr (AXES) r = p.norm ? r : 1.f;
   const T* weight = static_cast<const T*>(p.weight[kind]);
   const int half = p.rot / 2;
   // the lane that reads a pair also writes it, so the output may be the input
@@ -287,6 +329,10 @@ __global__ void __launch_bounds__(kAnyThreads) qk_norm_rope_any_kernel(const Nor
     const int ia = p.interleaved ? 2 * i : i, ib = p.interleaved ? 2 * i + 1 : i + half;
     const float a = to_f32<T>(src[ia]) * r * (weight ? to_f32<T>(weight[ia]) : 1.f);
     const float b = to_f32<T>(src[ib]) * r * (weight ? to_f32<T>(weight[ib]) : 1.f);
+    if constexpr (AXES) {
+      pos = p.positions[p.pair_axis[i] * p.positions_stride + token];
+      known = pos >= 0 && pos < p.table_rows;
+    }
     const int64_t at = static_cast<int64_t>(pos) * half + i;
     const float c = known ? p.cos_t[at] : quiet_nan(), s = known ? p.sin_t[at] : quiet_nan();
     dst[ia] = from_f32<T>(fmaf(a, c, -b * s));
@@ -299,8 +345,8 @@ __global__ void __launch_bounds__(kAnyThreads) qk_norm_rope_any_kernel(const Nor
 // A warp takes a whole token where that fills the GPU; with fewer tokens each is
 // split over as many warps as the GPU holds (2040 tokens x 21 heads x 72: two
 // warps a token 6.0 us, three 7.2; 16384 x 48 x 128: one 75.7, two 77.7).
-template <typename T, int P, int LPH>
-cudaError_t launch_heads(const NormParams& p, int device, int sms, cudaStream_t stream) {
+template <typename T, int P, int LPH, typename Params>
+cudaError_t launch_heads(const Params& p, int device, int sms, cudaStream_t stream) {
   const int per_warp = 32 / (LPH ? LPH : p.d / (2 * P));
   const int most = (p.heads[0] + p.heads[1] + p.heads[2] + per_warp - 1) / per_warp;  // steps of a token
   const int resident = kCtasPerSm * sms * (kVecThreads / 32);
@@ -310,12 +356,12 @@ cudaError_t launch_heads(const NormParams& p, int device, int sms, cudaStream_t 
   const dim3 grid(static_cast<unsigned>((items + kVecThreads / 32 - 1) / (kVecThreads / 32)));
   static Kernel adjacent, halves;
   return p.interleaved
-             ? adjacent.launch(qk_norm_rope_vec_kernel<T, P, LPH, true>, device, grid, kVecThreads, 0, 1, stream, p, chunks, steps)
-             : halves.launch(qk_norm_rope_vec_kernel<T, P, LPH, false>, device, grid, kVecThreads, 0, 1, stream, p, chunks, steps);
+             ? adjacent.launch(qk_norm_rope_vec_kernel<T, P, LPH, true, Params>, device, grid, kVecThreads, 0, 1, stream, p, chunks, steps)
+             : halves.launch(qk_norm_rope_vec_kernel<T, P, LPH, false, Params>, device, grid, kVecThreads, 0, 1, stream, p, chunks, steps);
 }
 
-template <typename T>
-cudaError_t launch_vec_t(const NormParams& p, int device, int sms, cudaStream_t stream) {
+template <typename T, typename Params>
+cudaError_t launch_vec_t(const Params& p, int device, int sms, cudaStream_t stream) {
   if constexpr (sizeof(T) == 2) {
     if (p.wide && p.d == 64) return launch_heads<T, 8, 4>(p, device, sms, stream);
     if (p.wide && p.d == 128) return launch_heads<T, 8, 8>(p, device, sms, stream);
@@ -327,25 +373,38 @@ cudaError_t launch_vec_t(const NormParams& p, int device, int sms, cudaStream_t 
   return launch_heads<T, 4, 0>(p, device, sms, stream);
 }
 
-template <typename T>
-cudaError_t launch_any_t(const NormParams& p, int device, cudaStream_t stream) {
+template <typename T, typename Params>
+cudaError_t launch_any_t(const Params& p, int device, cudaStream_t stream) {
   const int total = p.heads[0] + p.heads[1] + p.heads[2], per = kAnyThreads / 32;
   static Kernel handle;
-  return handle.launch(qk_norm_rope_any_kernel<T>, device, dim3(p.t, (total + per - 1) / per), kAnyThreads, 0, 1, stream, p);
+  return handle.launch(qk_norm_rope_any_kernel<T, Params>, device, dim3(p.t, (total + per - 1) / per), kAnyThreads, 0, 1, stream, p);
 }
 
-}  // namespace
-
-cudaError_t launch_norm_vec(const NormParams& p, int precision, int device, int sms, cudaStream_t stream) {
+template <typename Params>
+cudaError_t launch_vec(const Params& p, int precision, int device, int sms, cudaStream_t stream) {
   if (precision == OIDNX_PRECISION_FP32) return launch_vec_t<float>(p, device, sms, stream);
   if (precision == OIDNX_PRECISION_BF16) return launch_vec_t<__nv_bfloat16>(p, device, sms, stream);
   return launch_vec_t<__half>(p, device, sms, stream);
 }
-
-cudaError_t launch_norm_any(const NormParams& p, int precision, int device, cudaStream_t stream) {
+template <typename Params>
+cudaError_t launch_any(const Params& p, int precision, int device, cudaStream_t stream) {
   if (precision == OIDNX_PRECISION_FP32) return launch_any_t<float>(p, device, stream);
   if (precision == OIDNX_PRECISION_BF16) return launch_any_t<__nv_bfloat16>(p, device, stream);
   return launch_any_t<__half>(p, device, stream);
+}
+}  // namespace
+
+cudaError_t launch_norm_vec(const NormParams& p, int precision, int device, int sms, cudaStream_t stream) {
+  return launch_vec(p, precision, device, sms, stream);
+}
+cudaError_t launch_norm_any(const NormParams& p, int precision, int device, cudaStream_t stream) {
+  return launch_any(p, precision, device, stream);
+}
+cudaError_t launch_axes_vec(const AxesParams& p, int precision, int device, int sms, cudaStream_t stream) {
+  return launch_vec(p, precision, device, sms, stream);
+}
+cudaError_t launch_axes_any(const AxesParams& p, int precision, int device, cudaStream_t stream) {
+  return launch_any(p, precision, device, stream);
 }
 
 }  // namespace oidnx

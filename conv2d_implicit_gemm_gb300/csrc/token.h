@@ -158,6 +158,39 @@ struct NormParams {
   int wide;  // vector form: 16-byte loads of 16-bit values (else 8-byte)
 };
 
+// The same with a position an axis and pair: the pairs turn by
+// positions[pair_axis[r] * positions_stride + token].
+constexpr int kMostAxes = 8, kMostPairs = 256;
+struct AxesParams : NormParams {
+  int64_t positions_stride;
+  int axes;
+  int norm;
+  uint8_t pair_axis[kMostPairs];
+};
+
+// ---------------------------------------------------------------- norms around a branch
+// s = alpha residual + beta g(gate) post(x), y = pre(s) (1 + scale) + shift;
+// row strides in elements.
+struct BlockParams {
+  const void* x;
+  const void* residual;  // or null
+  void* sum;             // or null
+  void* y;               // or null
+  int64_t ldx, ldr, ld_sum, ldy;
+  const void* weight[2];  // post, pre; or null
+  const void* bias[2];
+  const void* gate;  // or null
+  const void* scale;
+  const void* shift;
+  int64_t ldg, lds, ldh;
+  const int* groups;  // or null: row / per
+  int per, count;
+  int norm[2];
+  int gate_act;
+  float eps, alpha, beta;
+  int t, n;
+};
+
 // ---------------------------------------------------------------- attention
 // Strides in elements: batch, token, head.
 struct AttnParams {
@@ -203,6 +236,11 @@ cudaError_t launch_align_rows(const AlignParams& p, int count, int device, int s
 cudaError_t launch_linear_split(const LinearTcLaunch& L, bool bf16, cudaStream_t stream);
 cudaError_t launch_norm_vec(const NormParams& p, int precision, int device, int sms, cudaStream_t stream);
 cudaError_t launch_norm_any(const NormParams& p, int precision, int device, cudaStream_t stream);
+cudaError_t launch_axes_vec(const AxesParams& p, int precision, int device, int sms, cudaStream_t stream);
+cudaError_t launch_axes_any(const AxesParams& p, int precision, int device, cudaStream_t stream);
+// vector: rows in whole 16-byte pieces
+cudaError_t launch_block_norm(const BlockParams& p, bool vector, int precision, int sum_precision, int device, int sms,
+                              cudaStream_t stream);
 cudaError_t launch_attn_token(const AttnParams& p, bool bf16, int split, int device, cudaStream_t stream);
 // CTAs in clusters of `split` that the device holds at once.
 int attn_token_slots(const AttnParams& p, bool bf16, int split, int device);

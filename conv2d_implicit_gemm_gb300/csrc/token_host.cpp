@@ -4,60 +4,16 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
-#include <cstdio>
 #include <cstring>
 #include <mutex>
 
-#include "../../include/oidnx.h"
-#include "token.h"
-
-namespace oidnx {
-oidnx_status report_error(oidnx_status status, const char* message);
-oidnx_status report_ok();
-cudaError_t token_device(int* device, int* sms, int** status);
-cudaError_t token_pool(int device, cudaMemPool_t* pool);
-cudaError_t token_status_take(int* word, cudaStream_t stream);
-}  // namespace oidnx
+#include "token_host.h"
 
 using namespace oidnx;
 
 namespace {
 
-template <typename... A>
-oidnx_status fail(oidnx_status s, const char* fmt, A... args) {
-  char buf[512];
-  snprintf(buf, sizeof(buf), fmt, args...);
-  return report_error(s, buf);
-}
-oidnx_status fail(oidnx_status s, const char* text) { return report_error(s, text); }
-
-oidnx_status finish(cudaError_t e, const char* call) {
-  if (e != cudaSuccess) {
-    cudaGetLastError();  // a refused launch must not show up in the caller's next check
-    return fail(e == cudaErrorMemoryAllocation ? OIDNX_ERR_OUT_OF_MEMORY : OIDNX_ERR_CUDA, "%s: %s", call,
-                cudaGetErrorString(e));
-  }
-  return report_ok();
-}
-
-template <typename F> F driver_call(const char* name) {
-  void* ptr = nullptr;
-  cudaDriverEntryPointQueryResult q;
-  return cudaGetDriverEntryPointByVersion(name, &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-                 q == cudaDriverEntryPointSuccess
-             ? reinterpret_cast<F>(ptr)
-             : F(nullptr);
-}
-
-bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-constexpr int kMost = 1 << 30;  // of a size, so that sums of a few of them stay within 32 bits
-
 // ---------------------------------------------------------------- tensor maps
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 // A matrix of rows x cols 16-bit values with row stride ld, in boxes of
 // box_cols (64: 128-byte rows, 32: 64-byte rows) x box_rows, swizzled.
 bool matrix_map(CUtensorMap* map, bool bf16, const void* base, int64_t ld, int rows, int cols, int box_rows, int box_cols) {
@@ -174,23 +130,6 @@ cudaError_t run_linear(const LinearParams& params, bool bf16, cudaStream_t strea
 }
 
 // ---------------------------------------------------------------- attention: choice of form
-// Heads of 16-bit values as [sequence][outer][inner][value] in boxes of 64
-// values x box1 x box2, 128-byte rows, swizzled.  outer and inner are tokens
-// and heads in either order.
-bool heads_map(CUtensorMap* map, bool bf16, const void* base, int d, int n1, int64_t s1, int n2, int64_t s2, int n3,
-               int64_t s3, int box1, int box2) {
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2),
-                              static_cast<cuuint64_t>(n3)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2,
-                                 static_cast<cuuint64_t>(s3) * 2};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2), 1}, step[4] = {1, 1, 1, 1};
-  static const EncodeFn fn = driver_call<EncodeFn>("cuTensorMapEncodeTiled");
-  return fn && fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                  const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
   int device, sms;
   const cudaError_t e = token_device(&device, &sms, &p.status);
@@ -276,6 +215,67 @@ cudaError_t run_attention(AttnParams& p, int precision, cudaStream_t stream) {
   return launch_attn_any(p, precision, device, stream);
 }
 
+// ---------------------------------------------------------------- norm and rotation: checks and parameters
+// Index 0 = queries, 1 = keys, 2 = values.
+struct HeadViews {
+  const void* in[3];
+  void* out[3];
+  long long in_t[3], in_h[3], out_t[3], out_h[3];
+};
+
+oidnx_status norm_params(const char* name, const HeadViews& w, const void* q_weight, const void* k_weight, float eps,
+                         const float* cos_table, const float* sin_table, long long table_rows, const int* positions,
+                         const int* slots, long long cache_rows, int t, int hq, int hk, int d, int rot, int interleaved,
+                         int precision, NormParams* out_params, bool* fast) {
+  const void *q = w.in[0], *k = w.in[1], *v = w.in[2], *q_out = w.out[0], *k_out = w.out[1], *v_out = w.out[2];
+  if (precision < OIDNX_PRECISION_FP32 || precision > OIDNX_PRECISION_BF16)
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "%s: unknown precision %d", name, precision);
+  if (t < 0 || hq < 0 || hk < 0 || d <= 0 || rot < 0 || rot > d || rot % 2)
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "%s: bad sizes (t %d, heads %d and %d, d %d, rot %d)", name, t, hq, hk,
+                d, rot);
+  if (t > kMost) return fail(OIDNX_ERR_UNSUPPORTED, "%s: more than 2^30 tokens", name);
+  if (hq > 65536 || hk > 65536) return fail(OIDNX_ERR_UNSUPPORTED, "%s: more than 65536 heads", name);
+  if (!(eps >= 0.f) || std::isinf(eps)) return fail(OIDNX_ERR_INVALID_ARGUMENT, "%s: bad eps", name);
+  if (t == 0 || (hq == 0 && hk == 0)) return finish(cudaSuccess, name);
+  if ((hq && (!q || !q_out)) || (hk && (!k || !k_out)) || !v != !v_out)
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "%s: NULL heads", name);
+  if (rot && (!cos_table || !sin_table || !positions || table_rows < 0))
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "%s: NULL tables or positions", name);
+  const size_t size = precision == OIDNX_PRECISION_FP32 ? 4 : 2;
+  const void* all[] = {q, q_out, k, k_out, v, v_out, q_weight, k_weight};
+  for (const void* a : all)
+    if (!aligned(a, size))
+      return fail(OIDNX_ERR_INVALID_ARGUMENT, "%s: pointers must be aligned to their elements", name);
+  if (!aligned(cos_table, 4) || !aligned(sin_table, 4) || !aligned(positions, 4) || !aligned(slots, 4))
+    return fail(OIDNX_ERR_INVALID_ARGUMENT, "%s: tables, positions and slots must be 4-byte aligned", name);
+  NormParams& p = *out_params;
+  p.heads[0] = hq, p.heads[1] = hk, p.heads[2] = v ? hk : 0;
+  // Vector forms: heads in whole groups of four rotation pairs (eight: wide),
+  // the rotated part and the rest alike, everything aligned to four values
+  // (eight).  Values of 32 bits: four pairs and 16 bytes.
+  const auto fits = [&](int pairs) {
+    const size_t align = pairs * size;
+    bool ok = d % (2 * pairs) == 0 && d / (2 * pairs) <= 32 && rot % (2 * pairs) == 0 && aligned(q_weight, align) &&
+              aligned(k_weight, align) && aligned(cos_table, 16) && aligned(sin_table, 16);
+    for (int i = 0; i < 3; ++i)
+      if (p.heads[i])
+        ok = ok && aligned(w.in[i], align) && aligned(w.out[i], align) && w.in_t[i] % pairs == 0 &&
+             w.in_h[i] % pairs == 0 && w.out_t[i] % pairs == 0 && w.out_h[i] % pairs == 0;
+    return ok;
+  };
+  for (int i = 0; i < 3; ++i) {
+    p.in[i] = w.in[i], p.out[i] = w.out[i];
+    p.in_t[i] = w.in_t[i], p.in_h[i] = w.in_h[i], p.out_t[i] = w.out_t[i], p.out_h[i] = w.out_h[i];
+  }
+  p.wide = size == 2 && fits(8);
+  *fast = p.wide || fits(4);
+  p.weight[0] = q_weight, p.weight[1] = k_weight;
+  p.eps = eps, p.cos_t = cos_table, p.sin_t = sin_table, p.table_rows = table_rows;
+  p.positions = positions, p.slots = slots, p.cache_rows = cache_rows;
+  p.t = t, p.d = d, p.rot = rot, p.interleaved = interleaved != 0;
+  return OIDNX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -310,60 +310,51 @@ oidnx_status oidnx_qk_norm_rope(const void* q, long long q_st, long long q_sh, v
                                 const void* k_weight, float eps, const float* cos_table, const float* sin_table,
                                 long long table_rows, const int* positions, const int* slots, long long cache_rows,
                                 int t, int hq, int hk, int d, int rot, int interleaved, int precision, void* stream) {
-  if (precision < OIDNX_PRECISION_FP32 || precision > OIDNX_PRECISION_BF16)
-    return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: unknown precision %d", precision);
-  if (t < 0 || hq < 0 || hk < 0 || d <= 0 || rot < 0 || rot > d || rot % 2)
-    return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: bad sizes (t %d, heads %d and %d, d %d, rot %d)", t, hq, hk,
-                d, rot);
-  if (t > kMost) return fail(OIDNX_ERR_UNSUPPORTED, "qk_norm_rope: more than 2^30 tokens");
-  if (hq > 65536 || hk > 65536) return fail(OIDNX_ERR_UNSUPPORTED, "qk_norm_rope: more than 65536 heads");
-  if (!(eps >= 0.f) || std::isinf(eps)) return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: bad eps");
-  if (t == 0 || (hq == 0 && hk == 0)) return finish(cudaSuccess, "qk_norm_rope");
-  if ((hq && (!q || !q_out)) || (hk && (!k || !k_out)) || !v != !v_out)
-    return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: NULL heads");
-  if (rot && (!cos_table || !sin_table || !positions || table_rows < 0))
-    return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: NULL tables or positions");
-  const size_t size = precision == OIDNX_PRECISION_FP32 ? 4 : 2;
-  const void* all[] = {q, q_out, k, k_out, v, v_out, q_weight, k_weight};
-  for (const void* a : all)
-    if (!aligned(a, size))
-      return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: pointers must be aligned to their elements");
-  if (!aligned(cos_table, 4) || !aligned(sin_table, 4) || !aligned(positions, 4) || !aligned(slots, 4))
-    return fail(OIDNX_ERR_INVALID_ARGUMENT, "qk_norm_rope: tables, positions and slots must be 4-byte aligned");
+  const HeadViews heads = {{q, k, v}, {q_out, k_out, v_out}, {q_st, k_st, v_st}, {q_sh, k_sh, v_sh}, {qo_st, ko_st, vo_st},
+                           {qo_sh, ko_sh, vo_sh}};
   NormParams p = {};
-  const void* in[3] = {q, k, v};
-  void* out[3] = {q_out, k_out, v_out};
-  const long long it[3] = {q_st, k_st, v_st}, ih[3] = {q_sh, k_sh, v_sh};
-  const long long ot[3] = {qo_st, ko_st, vo_st}, oh[3] = {qo_sh, ko_sh, vo_sh};
-  p.heads[0] = hq, p.heads[1] = hk, p.heads[2] = v ? hk : 0;
-  // Vector forms: heads in whole groups of four rotation pairs (eight: wide),
-  // the rotated part and the rest alike, everything aligned to four values
-  // (eight).  Values of 32 bits: four pairs and 16 bytes.
-  const auto fits = [&](int pairs) {
-    const size_t align = pairs * size;
-    bool ok = d % (2 * pairs) == 0 && d / (2 * pairs) <= 32 && rot % (2 * pairs) == 0 && aligned(q_weight, align) &&
-              aligned(k_weight, align) && aligned(cos_table, 16) && aligned(sin_table, 16);
-    for (int i = 0; i < 3; ++i)
-      if (p.heads[i])
-        ok = ok && aligned(in[i], align) && aligned(out[i], align) && it[i] % pairs == 0 && ih[i] % pairs == 0 &&
-             ot[i] % pairs == 0 && oh[i] % pairs == 0;
-    return ok;
-  };
-  for (int i = 0; i < 3; ++i) {
-    p.in[i] = in[i], p.out[i] = out[i];
-    p.in_t[i] = it[i], p.in_h[i] = ih[i], p.out_t[i] = ot[i], p.out_h[i] = oh[i];
-  }
-  p.wide = size == 2 && fits(8);
-  const bool fast = p.wide || fits(4);
-  p.weight[0] = q_weight, p.weight[1] = k_weight;
-  p.eps = eps, p.cos_t = cos_table, p.sin_t = sin_table, p.table_rows = table_rows;
-  p.positions = positions, p.slots = slots, p.cache_rows = cache_rows;
-  p.t = t, p.d = d, p.rot = rot, p.interleaved = interleaved != 0;
+  bool fast;
+  const oidnx_status refused = norm_params("qk_norm_rope", heads, q_weight, k_weight, eps, cos_table, sin_table, table_rows,
+                                           positions, slots, cache_rows, t, hq, hk, d, rot, interleaved, precision, &p, &fast);
+  if (refused != OIDNX_OK || t == 0 || (hq == 0 && hk == 0)) return refused;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int device, sms, *status;
   cudaError_t e = token_device(&device, &sms, &status);
   if (e == cudaSuccess) e = fast ? launch_norm_vec(p, precision, device, sms, s) : launch_norm_any(p, precision, device, s);
   return finish(e, "qk_norm_rope");
+}
+
+oidnx_status oidnx_qk_norm_rope_axes(const void* q, long long q_st, long long q_sh, void* q_out, long long qo_st,
+                                     long long qo_sh, const void* k, long long k_st, long long k_sh, void* k_out,
+                                     long long ko_st, long long ko_sh, const void* v, long long v_st, long long v_sh,
+                                     void* v_out, long long vo_st, long long vo_sh, int norm, const void* q_weight,
+                                     const void* k_weight, float eps, const float* cos_table, const float* sin_table,
+                                     long long table_rows, const int* positions, long long positions_stride, int axes,
+                                     const unsigned char* pair_axes, const int* slots, long long cache_rows, int t, int hq,
+                                     int hk, int d, int rot, int interleaved, int precision, void* stream) {
+  const char* name = "qk_norm_rope_axes";
+  if (axes < 1 || axes > kMostAxes) return fail(OIDNX_ERR_INVALID_ARGUMENT, "%s: %d axes (1 to %d)", name, axes, kMostAxes);
+  const HeadViews heads = {{q, k, v}, {q_out, k_out, v_out}, {q_st, k_st, v_st}, {q_sh, k_sh, v_sh}, {qo_st, ko_st, vo_st},
+                           {qo_sh, ko_sh, vo_sh}};
+  AxesParams p = {};
+  bool fast;
+  const oidnx_status refused = norm_params(name, heads, q_weight, k_weight, eps, cos_table, sin_table, table_rows, positions,
+                                           slots, cache_rows, t, hq, hk, d, rot, interleaved, precision, &p, &fast);
+  if (refused != OIDNX_OK) return refused;
+  if (rot > 2 * kMostPairs) return fail(OIDNX_ERR_UNSUPPORTED, "%s: more than %d rotated values (%d)", name, 2 * kMostPairs, rot);
+  if (rot && t && positions_stride < t) return fail(OIDNX_ERR_INVALID_ARGUMENT, "%s: positions_stride below t", name);
+  if (rot && !pair_axes) return fail(OIDNX_ERR_INVALID_ARGUMENT, "%s: NULL pair_axes", name);
+  for (int r = 0; r < rot / 2; ++r) {
+    if (pair_axes[r] >= axes) return fail(OIDNX_ERR_INVALID_ARGUMENT, "%s: pair %d turns by axis %d of %d", name, r, pair_axes[r], axes);
+    p.pair_axis[r] = pair_axes[r];
+  }
+  if (t == 0 || (hq == 0 && hk == 0)) return finish(cudaSuccess, name);
+  p.positions_stride = positions_stride, p.axes = axes, p.norm = norm != 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int device, sms, *status;
+  cudaError_t e = token_device(&device, &sms, &status);
+  if (e == cudaSuccess) e = fast ? launch_axes_vec(p, precision, device, sms, s) : launch_axes_any(p, precision, device, s);
+  return finish(e, name);
 }
 
 oidnx_status oidnx_window_attention(const void* q, long long q_sb, long long q_st, long long q_sh, const void* k,

@@ -1,9 +1,23 @@
-// Activations of the linear layer's epilogue, in fp32.
+// Activations of the linear layer's epilogue and the roots of the norms, in fp32.
 #pragma once
 
 #include "../../include/oidnx.h"
 
 namespace oidnx {
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / sqrt(x) to fp32's last place or two: the hardware's 2^-22 and one Newton
+// step.  Zero and infinity keep the hardware's answer (infinity and zero).
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = rsqrtf(x);
+  const float e = fmaf(-x * r, r, 1.f);
+  return x > 0.f && x < INFINITY ? fmaf(0.5f * r, e, r) : r;
+}
 
 // 1 / (1 + e^-z): the hardware's exp2 and reciprocal are good to about 2^-22,
 // far below the 16-bit rounding that follows.  e^-z overflows to infinity

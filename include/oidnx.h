@@ -443,6 +443,90 @@ oidnx_status oidnx_window_attention(const void* q, long long q_sb, long long q_s
                                     int cap, int hq, int hk, int d, int window, int sinks,
                                     float scale, int precision, void* stream);
 
+/* ---- a conditioned block's operators -----------------------------------
+ * What a block over the tokens of an image or a video needs beside the calls
+ * above, under the same rules: the norms before and after a branch with its gate
+ * and residual, heads turned by positions of several axes, and attention to an
+ * encoder's states.  Of these only oidnx_cross_attention takes memory of its own
+ * (from the same pool, ordered on the stream): for copies of operands that do
+ * not start on 16 bytes, and for the parts of few queries' long sums.  */
+
+enum { OIDNX_NORM_NONE = 0, OIDNX_NORM_RMS = 1, OIDNX_NORM_LAYER = 2 };
+enum { OIDNX_GATE_PLAIN = 0, OIDNX_GATE_TANH = 1, OIDNX_GATE_SIGMOID = 2 };
+
+/* Norm after a branch, its gate, the residual, and the norm before the next:
+ *   s[i] = residual_scale residual[i] + branch_scale g(gate[m]) post(x[i])
+ *   y[i] = pre(s[i]) (1 + scale[m]) + shift[m]
+ * for the rows i < t of n values, with m = groups[i], or i / per where groups is
+ * NULL.  post and pre are
+ *   OIDNX_NORM_NONE   z
+ *   OIDNX_NORM_RMS    z / sqrt(mean(z^2) + eps) weight + bias
+ *   OIDNX_NORM_LAYER  (z - mean(z)) / sqrt(mean((z - mean(z))^2) + eps) weight + bias
+ * (weight, bias [n]; NULL: 1 and 0) and g is the value itself, its tanh or its
+ * sigmoid (gate_act).  gate, scale and shift have a row for each of `count`
+ * groups, with row strides ldg, lds and ldh (0: one row for all; NULL: gate 1,
+ * scale and shift 0).  residual NULL: none.  sum and y receive s and y; either
+ * may be NULL.  pre works on s before its rounding.  A row whose m is outside
+ * [0, count) is padding: nothing of it is written.  sum may be the residual and
+ * y may be x (same pointer, stride and type); they overlap nothing else.
+ * precision: OIDNX_PRECISION_FP32, _FP16 or _BF16, of x, y and the vectors;
+ * sum_precision, of residual and sum: the same, or _FP32, or _AUTO (the same).
+ * Errors: INVALID_ARGUMENT (NULL, sizes, strides shorter than rows, misaligned
+ * pointers, unknown norm, gate_act or precision, per <= 0 without groups, eps or
+ * a factor that is not finite), UNSUPPORTED (a size beyond 2^30), CUDA.  */
+oidnx_status oidnx_block_norm(const void* x, long long ldx, const void* residual, long long ldr, void* sum,
+                              long long ld_sum, void* y, long long ldy, int post, const void* post_weight,
+                              const void* post_bias, int pre, const void* pre_weight, const void* pre_bias,
+                              float eps, const void* gate, long long ldg, int gate_act, const void* scale,
+                              long long lds, const void* shift, long long ldh, const int* groups, int per,
+                              int count, float residual_scale, float branch_scale, int t, int n, int precision,
+                              int sum_precision, void* stream);
+
+/* oidnx_qk_norm_rope with a position for each of `axes` axes (time, height and
+ * width, say): rotation pair r of token i turns by row
+ * positions[pair_axes[r]][i] of the tables, column r.  positions is a device
+ * array [axes][t] with axis stride positions_stride; pair_axes is an array of
+ * rot / 2 axis numbers in host memory, read before the call returns.  (Sections
+ * of pairs one after the other, or axes taking turns; a table may hold other
+ * angles for an axis in rows of its own.)  norm = 0: no norm; the weights still
+ * multiply.  A position outside the table gives NaN in the values that its axis
+ * turns.  All else is as there.
+ * Errors: as there, and INVALID_ARGUMENT (axes outside 1 .. 8, an axis number
+ * not below axes, positions_stride below t), UNSUPPORTED (rot over 512).  */
+oidnx_status oidnx_qk_norm_rope_axes(const void* q, long long q_st, long long q_sh, void* q_out, long long qo_st,
+                                     long long qo_sh, const void* k, long long k_st, long long k_sh, void* k_out,
+                                     long long ko_st, long long ko_sh, const void* v, long long v_st,
+                                     long long v_sh, void* v_out, long long vo_st, long long vo_sh, int norm,
+                                     const void* q_weight, const void* k_weight, float eps,
+                                     const float* cos_table, const float* sin_table, long long table_rows,
+                                     const int* positions, long long positions_stride, int axes,
+                                     const unsigned char* pair_axes, const int* slots, long long cache_rows,
+                                     int t, int hq, int hk, int d, int rot, int interleaved, int precision,
+                                     void* stream);
+
+/* Attention of b sequences of tq queries to kv keys each, of another length and
+ * without an order among them (an encoder's states; a map's own tokens):
+ *   o = sum_j softmax_j(scale q.k_j) v_j,  lse = log(sum_j exp(scale q.k_j))
+ * over the keys j < kv_lens[s] (NULL: kv) whose mask byte mask[s][j] is not 0
+ * (mask [b][kv] with sequence stride mask_sb, 0: one for all; NULL: every key).
+ * Rows from q_lens[s] on (NULL: tq) and queries that see no key give o = 0 and
+ * lse = -inf.  Keys and values that are not seen are never used, whatever they
+ * hold.  Query head h reads key head h / (hq / hk).  Strides as in
+ * oidnx_window_attention; queries, keys and values may be shared by sequences
+ * or heads (stride 0).  lse (fp32 [b][hq][tq]) may be NULL.  q_lens, kv_lens and
+ * mask are device arrays.  o overlaps no input.
+ * precision: OIDNX_PRECISION_FP16 or _BF16.  d <= 256, any size: operands whose
+ * heads are not whole 16-byte pieces on 16 bytes are copied first.
+ * Errors: INVALID_ARGUMENT (NULL, sizes, hq not a multiple of hk, scale, mask
+ * stride below kv and not 0, misaligned pointers, unknown precision), UNSUPPORTED
+ * (fp32, d > 256, over 4e9 query heads), OUT_OF_MEMORY, CUDA.  */
+oidnx_status oidnx_cross_attention(const void* q, long long q_sb, long long q_st, long long q_sh, const void* k,
+                                   long long k_sb, long long k_st, long long k_sh, const void* v, long long v_sb,
+                                   long long v_st, long long v_sh, void* o, long long o_sb, long long o_st,
+                                   long long o_sh, float* lse, const int* q_lens, const int* kv_lens,
+                                   const unsigned char* mask, long long mask_sb, int b, int tq, int kv, int hq,
+                                   int hk, int d, float scale, int precision, void* stream);
+
 /* Wait for `stream`, then report and clear the token operators' error word
  * on the current device: OK, or TIMEOUT if a kernel's bounded wait gave up
  * (that call's output is then undefined).  Errors: CUDA.  */

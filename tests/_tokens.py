@@ -60,5 +60,38 @@ def attention(q, k, v, o, lse, q_lens, kv_lens, window, sinks, scale, kind):
                               sinks, scale, KINDS[kind][1], stream())
 
 
+NORMS = ("none", "rms", "layer")
+GATES = ("plain", "tanh", "sigmoid")
+
+
+def block_norm(x, residual, total, y, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps, gate, gate_act, scale,
+               shift, groups, per, count, residual_scale, branch_scale, kind, total_kind):
+    def row(t):
+        return (0, 0) if t is None else (ptr(t), t.stride(0))
+    t, n = x.shape
+    ox.oidnx_block_norm(*row(x), *row(residual), *row(total), *row(y), NORMS.index(post), ptr(post_weight), ptr(post_bias),
+                        NORMS.index(pre), ptr(pre_weight), ptr(pre_bias), eps, *row(gate), GATES.index(gate_act), *row(scale),
+                        *row(shift), ptr(groups), per, count, residual_scale, branch_scale, t, n, KINDS[kind][1],
+                        KINDS[total_kind][1], stream())
+
+
+def norm_rope_axes(q, qo, k, ko, v, vo, norm, qw, kw, eps, cos, sin, positions, pair_axes, slots, interleaved, kind):
+    def view(t):
+        return (0, 0, 0) if t is None else (ptr(t), t.stride(0), t.stride(1))
+    t, hq, d = q.shape
+    ox.oidnx_qk_norm_rope_axes(*view(q), *view(qo), *view(k), *view(ko), *view(v), *view(vo), int(norm), ptr(qw), ptr(kw),
+                               eps, ptr(cos), ptr(sin), 0 if cos is None else cos.shape[0], ptr(positions),
+                               positions.stride(0), positions.shape[0], bytes(pair_axes), ptr(slots), ko.shape[0], t, hq,
+                               k.shape[1], d, 2 * len(pair_axes), int(interleaved), KINDS[kind][1], stream())
+
+
+def cross_attention(q, k, v, o, lse, q_lens, kv_lens, mask, scale, kind):
+    b, tq, hq, d = q.shape
+    kv, hk = k.shape[1:3]
+    ox.oidnx_cross_attention(ptr(q), *q.stride()[:3], ptr(k), *k.stride()[:3], ptr(v), *v.stride()[:3], ptr(o),
+                             *o.stride()[:3], ptr(lse), ptr(q_lens), ptr(kv_lens), ptr(mask),
+                             0 if mask is None else mask.stride(0), b, tq, kv, hq, hk, d, scale, KINDS[kind][1], stream())
+
+
 def done():
     ox.oidnx_token_sync_status(stream())
