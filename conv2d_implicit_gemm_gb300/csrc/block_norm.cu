@@ -10,7 +10,8 @@
 #include <type_traits>
 
 #include "token_math.cuh"
-#include "token_ptx.cuh"
+#include "token_pairs.cuh"
+#include "token_warp.cuh"
 #include "token.h"
 
 namespace oidnx {
@@ -24,48 +25,90 @@ __device__ __forceinline__ float gate_of(float g, int act) {
   return g;
 }
 
-// V consecutive values as they lie in memory: 16-byte pieces for V = 8, else one.
-template <typename T, int V> struct Piece {
-  static constexpr int N = V == 8 ? 8 * sizeof(T) / 16 : 1;
-  using Raw = typename std::conditional<V == 8, uint4, T>::type;
-  Raw r[N];
-  __device__ __forceinline__ void load(const T* p) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = reinterpret_cast<const Raw*>(p)[i];
+// A thread's E values of a row: pieces of 8 a team apart (V = 8), or single ones.  They
+// are fetched as words, zeros past the row, and worked on in pairs.
+template <int V, int E> struct Mine {
+  static constexpr int PAIRS = E / 2, N = E / V;
+  int first, step, count;  // pieces first, first + step, ..; those within the row
+  __device__ __forceinline__ Mine(int tid, int team, int n) : first(tid * V), step(team * V) {
+    count = first < n ? (n - first + step - 1) / step : 0;
   }
-  __device__ __forceinline__ void load_const(const T* p) {
+  template <typename U> static constexpr int kWords = V == 8 ? E * static_cast<int>(sizeof(U)) / 4 : E;
+
+  // (words past the row are left alone)
+  template <typename U, int W> __device__ __forceinline__ void fetch(const U* p, uint32_t (&w)[W]) const {
+    static_assert(W == kWords<U>, "");
+    p += first;
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = __ldg(reinterpret_cast<const Raw*>(p) + i);
-  }
-  __device__ __forceinline__ void store(T* p) const {
+    for (int c = 0; c < N; ++c, p += step) {
+      if (c < count) {
+        if constexpr (V == 8) {
+          constexpr int Q = sizeof(U) / 2;
 #pragma unroll
-    for (int i = 0; i < N; ++i) reinterpret_cast<Raw*>(p)[i] = r[i];
-  }
-  __device__ __forceinline__ void unpack(float (&f)[V]) const {
-    if constexpr (V == 1) {
-      f[0] = to_f32<T>(r[0]);
-    } else {
-      constexpr int M = Vec16<T>::N;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        float part[M];
-        Vec16<T>::unpack(r[i], part);
-#pragma unroll
-        for (int k = 0; k < M; ++k) f[i * M + k] = part[k];
+          for (int k = 0; k < Q; ++k) {
+            const uint4 q = reinterpret_cast<const uint4*>(p)[k];
+            w[(c * Q + k) * 4] = q.x, w[(c * Q + k) * 4 + 1] = q.y, w[(c * Q + k) * 4 + 2] = q.z, w[(c * Q + k) * 4 + 3] = q.w;
+          }
+        } else if constexpr (sizeof(U) == 2) {
+          w[c] = *reinterpret_cast<const uint16_t*>(p);
+        } else {
+          w[c] = *reinterpret_cast<const uint32_t*>(p);
+        }
       }
     }
   }
-  __device__ __forceinline__ void pack(const float (&f)[V]) {
-    if constexpr (V == 1) {
-      r[0] = from_f32<T>(f[0]);
-    } else {
-      constexpr int M = Vec16<T>::N;
+  template <typename U, int W> static __device__ __forceinline__ void pairs(const uint32_t (&w)[W], uint64_t (&v)[PAIRS]) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        float part[M];
+    for (int i = 0; i < PAIRS; ++i) {
+      if constexpr (sizeof(U) == 4) {
+        v[i] = f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+      } else {
+        const float2 u = unpack2<U>(V == 8 ? w[i] : w[2 * i] | w[2 * i + 1] << 16);
+        v[i] = f2(u.x, u.y);
+      }
+    }
+  }
+  template <typename U> __device__ __forceinline__ void load(const U* p, uint64_t (&v)[PAIRS]) const {
+    uint32_t w[kWords<U>] = {};
+    fetch(p, w);
+    pairs<U>(w, v);
+  }
+  template <typename U> __device__ __forceinline__ void store(U* p, const uint64_t (&v)[PAIRS]) const {
+    uint32_t w[E * sizeof(U) / 4];
 #pragma unroll
-        for (int k = 0; k < M; ++k) part[k] = f[i * M + k];
-        r[i] = Vec16<T>::pack(part);
+    for (int i = 0; i < PAIRS; ++i) {
+      const float2 u = f2_of(v[i]);
+      if constexpr (sizeof(U) == 4) w[2 * i] = __float_as_uint(u.x), w[2 * i + 1] = __float_as_uint(u.y);
+      else w[i] = pack2<U>(u.x, u.y);
+    }
+    p += first;
+#pragma unroll
+    for (int c = 0; c < N; ++c, p += step) {
+      if (c < count) {
+        if constexpr (V == 8) {
+          constexpr int Q = sizeof(U) / 2;
+#pragma unroll
+          for (int k = 0; k < Q; ++k)
+            reinterpret_cast<uint4*>(p)[k] =
+                make_uint4(w[(c * Q + k) * 4], w[(c * Q + k) * 4 + 1], w[(c * Q + k) * 4 + 2], w[(c * Q + k) * 4 + 3]);
+        } else if constexpr (sizeof(U) == 2) {
+          *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(c % 2 ? w[c / 2] >> 16 : w[c / 2]);
+        } else {
+          *reinterpret_cast<uint32_t*>(p) = w[c];
+        }
+      }
+    }
+  }
+  // zeros in the places past the row
+  __device__ __forceinline__ void clear(uint64_t (&v)[PAIRS]) const {
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      if constexpr (V == 8) {
+        if (2 * i / V >= count) v[i] = 0;
+      } else {
+        float2 u = f2_of(v[i]);
+        u.x = 2 * i < count ? u.x : 0.f, u.y = 2 * i + 1 < count ? u.y : 0.f;
+        v[i] = f2(u.x, u.y);
       }
     }
   }
@@ -91,147 +134,325 @@ template <int TH> __device__ __forceinline__ float row_sum(float v, float (*part
   return v;
 }
 
-// Rows of up to TH x CH x V values, V consecutive ones of each chunk a thread.
-template <typename T, typename S, int V, int CH, int TH>
-__global__ void __launch_bounds__(TH < 128 ? 128 : TH) block_norm_kernel(const BlockParams p) {
-  constexpr int ROWS = TH < 128 ? 128 / TH : 1;  // of a CTA at a time
+// Few rows, or long ones: a CTA a row of up to 512 x E values.
+template <typename T, typename S, int V, int E>
+__global__ void __launch_bounds__(kMostThreads) block_norm_kernel(const BlockParams p) {
+  constexpr int TH = kMostThreads, PAIRS = E / 2;
   __shared__ __align__(16) float parts[2][kMostThreads / 32];
-  const int sub = TH < 128 ? threadIdx.x / TH : 0, tid = TH < 128 ? threadIdx.x % TH : threadIdx.x;
-  const T* x = static_cast<const T*>(p.x);
-  const S* residual = static_cast<const S*>(p.residual);
+  const Mine<V, E> own(threadIdx.x, TH, p.n);
   const float inv_n = 1.f / static_cast<float>(p.n);
   int flip = 0;
   griddep_launch_dependents();
   griddep_wait();
 
-  Piece<T, V> xr[CH];
-  Piece<S, V> rr[CH];
-  const auto fetch = [&](int64_t row) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int e = (c * TH + tid) * V;
-      if (e < p.n) {
-        xr[c].load(x + row * p.ldx + e);
-        if (residual) rr[c].load(residual + row * p.ldr + e);
-      }
-    }
-  };
-  int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + sub;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
-  if (row < p.t) fetch(row);
-  for (; row < p.t; row += step) {
+  for (int64_t row = blockIdx.x; row < p.t; row += gridDim.x) {
     const int m = p.groups ? p.groups[row] : static_cast<int>(row) / p.per;
-    if (m < 0 || m >= p.count) {  // padding
-      if (row + step < p.t) fetch(row + step);
-      continue;
-    }
-    float v[CH][V];
-    float mean = 0.f, scale = 1.f;
-    const auto statistics = [&](int norm) {
-      mean = 0.f, scale = 1.f;
+    if (m < 0 || m >= p.count) continue;  // padding
+    uint32_t rw[Mine<V, E>::template kWords<S>] = {};
+    uint64_t v[PAIRS], f[PAIRS];
+    own.load(static_cast<const T*>(p.x) + row * p.ldx, v);
+    if (p.residual) own.fetch(static_cast<const S*>(p.residual) + row * p.ldr, rw);
+    float mean, root;
+    const auto statistics = [&](int norm) {  // of v, which is zero past the row
+      mean = 0.f, root = 1.f;
       if (norm == OIDNX_NORM_NONE) return;
+      uint64_t a = 0, b = 0;
       if (norm == OIDNX_NORM_LAYER) {
-        float a = 0.f;
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int i = 0; i < V; ++i) a += v[c][i];
-        mean = row_sum<TH>(a, parts, flip) * inv_n;
+        for (int i = 0; i < PAIRS; ++i) a = add2(a, v[i]);
+        const float2 u = f2_of(a);
+        mean = row_sum<TH>(u.x + u.y, parts, flip) * inv_n;
+        a = 0;
       }
-      float a = 0.f;
+      uint64_t c[PAIRS];
+      const uint64_t less = f2(-mean, -mean);
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        if ((c * TH + tid) * V < p.n) {
+      for (int i = 0; i < PAIRS; ++i) c[i] = add2(v[i], less);
+      own.clear(c);
 #pragma unroll
-          for (int i = 0; i < V; ++i) a = fmaf(v[c][i] - mean, v[c][i] - mean, a);
-        }
-      }
-      scale = inverse_root(fmaf(row_sum<TH>(a, parts, flip), inv_n, p.eps));
+      for (int i = 0; i < PAIRS; i += 2) a = fma2(c[i], c[i], a), b = fma2(c[i + 1], c[i + 1], b);
+      const float2 u = f2_of(add2(a, b));
+      root = inverse_root(fmaf(row_sum<TH>(u.x + u.y, parts, flip), inv_n, p.eps));
     };
-    const auto normalise = [&](int which, int c, int e) {
+    const auto normalise = [&](int which) {
       if (p.norm[which] == OIDNX_NORM_NONE) return;
+      statistics(p.norm[which]);
+      const uint64_t roots = f2(root, root), shifts = f2(-mean * root, -mean * root);
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[c][i] = (v[c][i] - mean) * scale;
-      float f[V];
-      Piece<T, V> w;
+      for (int i = 0; i < PAIRS; ++i) v[i] = fma2(v[i], roots, shifts);
       if (p.weight[which]) {
-        w.load_const(static_cast<const T*>(p.weight[which]) + e);
-        w.unpack(f);
+        own.load(static_cast<const T*>(p.weight[which]), f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[c][i] *= f[i];
+        for (int i = 0; i < PAIRS; ++i) v[i] = mul2(v[i], f[i]);
       }
       if (p.bias[which]) {
-        w.load_const(static_cast<const T*>(p.bias[which]) + e);
-        w.unpack(f);
+        own.load(static_cast<const T*>(p.bias[which]), f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[c][i] += f[i];
+        for (int i = 0; i < PAIRS; ++i) v[i] = add2(v[i], f[i]);
       }
+      own.clear(v);
     };
-
+    normalise(0);
+    const uint64_t beta = f2(p.beta, p.beta), alpha = f2(p.alpha, p.alpha);
+    if (p.gate) {
+      own.load(static_cast<const T*>(p.gate) + m * p.ldg, f);
+      if (p.gate_act != OIDNX_GATE_PLAIN) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if ((c * TH + tid) * V < p.n) {
-        xr[c].unpack(v[c]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[c][i] = 0.f;
-      }
-    }
-    statistics(p.norm[0]);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int e = (c * TH + tid) * V;
-      if (e < p.n) {
-        normalise(0, c, e);
-        if (p.gate) {
-          Piece<T, V> g;
-          float f[V];
-          g.load_const(static_cast<const T*>(p.gate) + m * p.ldg + e);
-          g.unpack(f);
-#pragma unroll
-          for (int i = 0; i < V; ++i) v[c][i] *= gate_of(f[i], p.gate_act);
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[c][i] *= p.beta;
-        if (residual) {
-          float f[V];
-          rr[c].unpack(f);
-#pragma unroll
-          for (int i = 0; i < V; ++i) v[c][i] = fmaf(p.alpha, f[i], v[c][i]);
-        }
-        if (p.sum) {
-          Piece<S, V> out;
-          out.pack(v[c]);
-          out.store(static_cast<S*>(p.sum) + row * p.ld_sum + e);
+        for (int i = 0; i < PAIRS; ++i) {
+          const float2 u = f2_of(f[i]);
+          f[i] = f2(gate_of(u.x, p.gate_act), gate_of(u.y, p.gate_act));
         }
       }
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) v[i] = mul2(v[i], f[i]);
     }
-    if (row + step < p.t) fetch(row + step);
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) v[i] = mul2(v[i], beta);
+    if (p.residual) {
+      Mine<V, E>::template pairs<S>(rw, f);
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) v[i] = fma2(f[i], alpha, v[i]);
+    }
+    if (p.sum) own.store(static_cast<S*>(p.sum) + row * p.ld_sum, v);
     if (!p.y) continue;
-    statistics(p.norm[1]);
+    normalise(1);
+    if (p.scale) {
+      own.load(static_cast<const T*>(p.scale) + m * p.lds, f);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int e = (c * TH + tid) * V;
-      if (e < p.n) {
-        normalise(1, c, e);
-        Piece<T, V> w;
-        float f[V];
-        if (p.scale) {
-          w.load_const(static_cast<const T*>(p.scale) + m * p.lds + e);
-          w.unpack(f);
+      for (int i = 0; i < PAIRS; ++i) v[i] = fma2(v[i], f[i], v[i]);
+    }
+    if (p.shift) {
+      own.load(static_cast<const T*>(p.shift) + m * p.ldh, f);
 #pragma unroll
-          for (int i = 0; i < V; ++i) v[c][i] = fmaf(v[c][i], f[i], v[c][i]);
+      for (int i = 0; i < PAIRS; ++i) v[i] = add2(v[i], f[i]);
+    }
+    own.store(static_cast<T*>(p.y) + row * p.ldy, v);
+  }
+}
+
+// Many rows of up to 8192 values: teams of `team` threads take consecutive rows, 16
+// values a thread.  Rows come through a ring in shared memory (cp.async, several
+// rows ahead), and what stands beside a row (weights, gate, modulation) is
+// multiplied together once a group and stays in registers:
+//
+//   s = alpha r + a (x - mean) root + b,   a = beta g w_post,   b = beta g b_post
+//   y = (s - mean) root c + d,             c = (1 + scale) w_pre, d = (1 + scale) b_pre + shift
+//
+// A thread copies the pieces that it will read itself.  Rows that do not start on 16
+// bytes are copied by the whole team, from the 16 bytes that they start in to the 16
+// that they end in (which are in their pages).
+//
+// 16384 rows of 4096 in bf16: 101 us, 5.3 TB/s, 78% of the measured copy rate (of 2048:
+// 92 us, of 512: 101); with an fp32 sum 143 us, 83%; odd widths half of that, a value at
+// a time.  Without the sums' waits 4096 took 99: what is left is instructions (32 a
+// value).  Not kept: rows side by side sharing a wait (105 to 127 us, as registers
+// spilled into what shared memory leaves of L1), what stands beside the rows in shared
+// memory (124 and up, the same), rows copied whole by one thread (178).
+constexpr int kMostStages = 8;
+constexpr int kRingThreads = 512;
+struct RingParams : BlockParams {
+  int team, stages;
+  int x_bytes, stage_bytes;  // of a stage: x, then the residual
+};
+constexpr int kRingBytes = 200 * 1024;  // of an SM's shared memory
+
+template <typename T, typename S, int V>
+__global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const RingParams p) {
+  constexpr int PAIRS = 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) float parts[2][kRingThreads / 32];
+  const int team = p.team, mine = threadIdx.x / team, tid = threadIdx.x - mine * team, warps = team / 32;
+  uint8_t* ring = smem + mine * p.stages * p.stage_bytes;
+  const int64_t teams = static_cast<int64_t>(gridDim.x) * (blockDim.x / team);
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * (blockDim.x / team) + mine;
+  const int begin = static_cast<int>(p.t * at / teams), end = static_cast<int>(p.t * (at + 1) / teams);
+  griddep_launch_dependents();
+  griddep_wait();
+
+  const Mine<V, 16> own(tid, team, p.n);
+  // bytes of a row's first 16 that stand before it
+  const auto skip = [](const void* q) { return V == 8 ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(q) & 15u); };
+  const T* x_next = static_cast<const T*>(p.x) + begin * p.ldx;  // the row that is fetched next
+  const S* r_next = static_cast<const S*>(p.residual) + (p.residual ? begin * p.ldr : 0);
+  int fetched = begin, to_stage = 0;
+  const auto copy_row = [&](uint32_t to, const auto* row) {
+    constexpr int size = sizeof(*row);
+    if constexpr (V == 8) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (c < own.count) {
+#pragma unroll
+          for (int k = 0; k < size / 2; ++k)
+            cp_async16(to + (own.first + c * own.step) * size + 16 * k,
+                       reinterpret_cast<const uint8_t*>(row + own.first + c * own.step) + 16 * k, 16u);
         }
-        if (p.shift) {
-          w.load_const(static_cast<const T*>(p.shift) + m * p.ldh + e);
-          w.unpack(f);
+    } else {
+      const uint32_t before = skip(row), bytes = before + p.n * size;
+      const uint8_t* from = reinterpret_cast<const uint8_t*>(row) - before;
+      for (uint32_t k = tid * 16; k < bytes; k += team * 16) cp_async16(to + k, from + k, 16u);
+    }
+  };
+  const auto fetch = [&] {
+    if (fetched < end) {
+      const uint32_t to = smem_u32(ring + to_stage * p.stage_bytes);
+      copy_row(to, x_next);
+      x_next += p.ldx;
+      if (p.residual) {
+        copy_row(to + p.x_bytes, r_next);
+        r_next += p.ldr;
+      }
+      ++fetched;
+      if (++to_stage == p.stages) to_stage = 0;
+    }
+    cp_async_commit();
+  };
+  for (int s = 0; s + 1 < p.stages; ++s) fetch();
+
+  const float inv_n = 1.f / static_cast<float>(p.n);
+  int flip = 0;
+  // sum over the team, the same in all its threads
+  const auto team_sum = [&](float v) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) v[c][i] += f[i];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (warps == 1) return v;
+    float* to = parts[flip] + mine * warps;
+    flip ^= 1;
+    if ((threadIdx.x & 31) == 0) to[tid >> 5] = v;
+    __syncwarp();
+    named_barrier_sync(1 + mine, team);
+    if (warps == 2) return to[0] + to[1];
+    float4 q = *reinterpret_cast<const float4*>(to);
+    v = (q.x + q.y) + (q.z + q.w);
+    for (int i = 4; i < warps; i += 4) {
+      q = *reinterpret_cast<const float4*>(to + i);
+      v += (q.x + q.y) + (q.z + q.w);
+    }
+    return v;
+  };
+  uint64_t v[PAIRS];
+  float mean = 0.f, root = 1.f;
+  const auto statistics = [&](int norm) {  // of v, which is zero past the row
+    mean = 0.f, root = 1.f;
+    if (norm == OIDNX_NORM_NONE) return;
+    uint64_t c[PAIRS], a = 0, b = 0;
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) c[i] = v[i];
+    if (norm == OIDNX_NORM_LAYER) {
+#pragma unroll
+      for (int i = 0; i < PAIRS; i += 2) a = add2(a, v[i]), b = add2(b, v[i + 1]);
+      const float2 u = f2_of(add2(a, b));
+      mean = team_sum(u.x + u.y) * inv_n;
+      a = b = 0;
+      const uint64_t less = f2(-mean, -mean);
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) c[i] = add2(v[i], less);
+      own.clear(c);
+    }
+#pragma unroll
+    for (int i = 0; i < PAIRS; i += 2) a = fma2(c[i], c[i], a), b = fma2(c[i + 1], c[i + 1], b);
+    const float2 u = f2_of(add2(a, b));
+    root = inverse_root(fmaf(team_sum(u.x + u.y), inv_n, p.eps));
+  };
+
+  uint64_t ca[PAIRS], cb[PAIRS], cc[PAIRS], cd[PAIRS];
+#pragma unroll
+  for (int i = 0; i < PAIRS; ++i) ca[i] = cb[i] = cc[i] = cd[i] = 0;
+  const auto read = [&](const void* q, int64_t offset, uint64_t (&f)[PAIRS], float none) {
+    if (q) {
+      own.load(static_cast<const T*>(q) + offset, f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) f[i] = f2(none, none);
+      own.clear(f);
+    }
+  };
+  int group = -1, group_end = begin;  // rows of one group, where they follow one another
+  bool kept = false;
+  S* sum_row = static_cast<S*>(p.sum) + (p.sum ? begin * p.ld_sum : 0);
+  T* y_row = static_cast<T*>(p.y) + (p.y ? begin * p.ldy : 0);
+  const T* x_row = static_cast<const T*>(p.x) + begin * p.ldx;
+  const S* r_row = static_cast<const S*>(p.residual) + (p.residual ? begin * p.ldr : 0);
+  int stage = 0;
+#pragma unroll 1
+  for (int row = begin; row < end; ++row) {
+    if (row >= group_end) {
+      const int m = p.groups ? p.groups[row] : row / p.per;
+      group_end = p.groups ? row + 1 : static_cast<int>(min(static_cast<int64_t>(m + 1) * p.per, static_cast<int64_t>(end)));
+      kept = m >= 0 && m < p.count;  // else padding
+      if (kept && m != group) {
+        group = m;
+        uint64_t f[PAIRS], g[PAIRS];
+        const uint64_t beta = f2(p.beta, p.beta);
+        read(p.gate, m * p.ldg, g, 1.f);
+        if (p.gate && p.gate_act != OIDNX_GATE_PLAIN) {
+#pragma unroll
+          for (int i = 0; i < PAIRS; ++i) {
+            const float2 u = f2_of(g[i]);
+            g[i] = f2(gate_of(u.x, p.gate_act), gate_of(u.y, p.gate_act));
+          }
+          own.clear(g);
         }
-        w.pack(v[c]);
-        w.store(static_cast<T*>(p.y) + row * p.ldy + e);
+        read(p.weight[0], 0, f, 1.f);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) g[i] = mul2(g[i], beta), ca[i] = mul2(f[i], g[i]);
+        read(p.bias[0], 0, f, 0.f);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) cb[i] = mul2(f[i], g[i]);
+        read(p.scale, m * p.lds, g, 0.f);
+        read(p.weight[1], 0, f, 1.f);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) cc[i] = fma2(f[i], g[i], f[i]);
+        read(p.bias[1], 0, f, 0.f);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) cd[i] = fma2(f[i], g[i], f[i]);
+        read(p.shift, m * p.ldh, g, 0.f);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) cd[i] = add2(cd[i], g[i]);
       }
     }
+    // rows stages - 1 at most are in flight: this one is the oldest
+    switch (p.stages) {
+      case 2: cp_async_wait<0>(); break;
+      case 3: cp_async_wait<1>(); break;
+      case 4: cp_async_wait<2>(); break;
+      case 5: cp_async_wait<3>(); break;
+      case 6: cp_async_wait<4>(); break;
+      case 7: cp_async_wait<5>(); break;
+      default: cp_async_wait<6>(); break;
+    }
+    if constexpr (V == 1) {  // the team has copied it together
+      __syncwarp();
+      if (warps > 1) named_barrier_sync(1 + mine, team);
+    }
+    fetch();  // over the last row, which every reader is done with
+    const uint8_t* from = ring + stage * p.stage_bytes;
+    if (kept) {
+      own.load(reinterpret_cast<const T*>(from + skip(x_row)), v);
+      statistics(p.norm[0]);
+      const uint64_t roots = f2(root, root), shifts = f2(-mean * root, -mean * root);
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) v[i] = fma2(fma2(v[i], roots, shifts), ca[i], cb[i]);
+      if (p.residual) {
+        uint64_t r[PAIRS];
+        own.load(reinterpret_cast<const S*>(from + p.x_bytes + skip(r_row)), r);
+        const uint64_t alpha = f2(p.alpha, p.alpha);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) v[i] = fma2(r[i], alpha, v[i]);
+      }
+      if (p.sum) own.store(sum_row, v);
+      if (p.y) {
+        statistics(p.norm[1]);
+      }
+    }
+    if (kept && p.y) {
+      const uint64_t roots = f2(root, root), shifts = f2(-mean * root, -mean * root);
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) v[i] = fma2(fma2(v[i], roots, shifts), cc[i], cd[i]);
+      own.store(y_row, v);
+    }
+    sum_row += p.ld_sum, y_row += p.ldy;
+    if constexpr (V == 1) x_row += p.ldx, r_row += p.ldr;
+    if (++stage == p.stages) stage = 0;
   }
 }
 
@@ -293,34 +514,42 @@ template <typename T, typename S> __global__ void __launch_bounds__(kLongThreads
   }
 }
 
-template <typename T, typename S, int V, int CH, int TH>
+template <typename T, typename S, int V, int E>
 cudaError_t launch_rows(const BlockParams& p, int device, int sms, cudaStream_t stream) {
-  constexpr int threads = TH < 128 ? 128 : TH, rows = threads / TH;
-  const int64_t ctas = (static_cast<int64_t>(p.t) + rows - 1) / rows;
-  const int64_t most = static_cast<int64_t>(sms) * (2048 / threads);
   static Kernel handle;
-  return handle.launch(block_norm_kernel<T, S, V, CH, TH>, device, dim3(static_cast<unsigned>(std::min(ctas, most))), threads,
-                       0, 1, stream, p);
+  return handle.launch(block_norm_kernel<T, S, V, E>, device, dim3(std::min(p.t, 4 * sms)), kMostThreads, 0, 1, stream, p);
+}
+
+template <typename T, typename S, int V>
+cudaError_t launch_ring(const BlockParams& p, int device, int sms, cudaStream_t stream) {
+  RingParams q;
+  static_cast<BlockParams&>(q) = p;
+  q.team = 32;
+  while (q.team * 16 < p.n) q.team *= 2;
+  const int threads = std::max(q.team, 256), teams = threads / q.team;
+  q.x_bytes = (p.n * static_cast<int>(sizeof(T)) + 31) / 16 * 16;
+  q.stage_bytes = q.x_bytes + (p.residual ? (p.n * static_cast<int>(sizeof(S)) + 31) / 16 * 16 : 0);
+  const int budget = kRingBytes / (kRingThreads / threads) / teams;
+  q.stages = std::min(kMostStages, budget / q.stage_bytes);
+  const int64_t most = static_cast<int64_t>(sms) * (kRingThreads / threads), want = (static_cast<int64_t>(p.t) + teams - 1) / teams;
+  static Kernel handle(kRingBytes);
+  return handle.launch(block_norm_ring_kernel<T, S, V>, device, dim3(static_cast<unsigned>(std::min(most, want))), threads,
+                       teams * q.stages * q.stage_bytes, 1, stream, q);
 }
 
 template <typename T, typename S>
 cudaError_t launch_t(const BlockParams& p, bool vector, int device, int sms, cudaStream_t stream) {
   const int n = p.n;
-  if (vector) {
-    if (n <= 256) return launch_rows<T, S, 8, 1, 32>(p, device, sms, stream);
-    if (n <= 512) return launch_rows<T, S, 8, 2, 32>(p, device, sms, stream);
-    if (n <= 1024) return launch_rows<T, S, 8, 4, 32>(p, device, sms, stream);
-    if (n <= 4096 && p.t <= sms) return launch_rows<T, S, 8, 1, 512>(p, device, sms, stream);
-    if (n <= 2048) return launch_rows<T, S, 8, 2, 128>(p, device, sms, stream);
-    if (n <= 4096) return launch_rows<T, S, 8, 4, 128>(p, device, sms, stream);
-    if (n <= 8192) return launch_rows<T, S, 8, 2, 512>(p, device, sms, stream);
-    if (n <= 16384) return launch_rows<T, S, 8, 4, 512>(p, device, sms, stream);
-  } else {
-    if (n <= 256) return launch_rows<T, S, 1, 8, 32>(p, device, sms, stream);
-    if (n <= 1024) return launch_rows<T, S, 1, 32, 32>(p, device, sms, stream);
-    if (n <= 4096) return launch_rows<T, S, 1, 32, 128>(p, device, sms, stream);
-    if (n <= 16384) return launch_rows<T, S, 1, 32, 512>(p, device, sms, stream);
-  }
+  // Rows of a CTA each start sooner, teams keep what stands beside the rows: us, bf16,
+  // 153, 300 and 608 rows of 1024 values 3.3, 3.4, 6.2 and 3.7, 3.8, 3.8; of 4096 3.6,
+  // 5.0, 9.1 and 4.3, 5.8, 8.4; 153 and 300 rows of 8192 9.3, 10.4 and 7.7, 8.8.
+  if (p.t > (n <= kMostThreads * 8 ? 2 : 1) * sms && n <= kRingThreads * 16)
+    return vector ? launch_ring<T, S, 8>(p, device, sms, stream) : launch_ring<T, S, 1>(p, device, sms, stream);
+  if (n <= kMostThreads * 8)
+    return vector ? launch_rows<T, S, 8, 8>(p, device, sms, stream) : launch_rows<T, S, 1, 8>(p, device, sms, stream);
+  if (n <= kMostThreads * 16 && vector) return launch_rows<T, S, 8, 16>(p, device, sms, stream);
+  if (n <= kMostThreads * 32)
+    return vector ? launch_rows<T, S, 8, 32>(p, device, sms, stream) : launch_rows<T, S, 1, 32>(p, device, sms, stream);
   static Kernel handle;
   return handle.launch(block_norm_long_kernel<T, S>, device, dim3(std::min(p.t, 4 * sms)), kLongThreads, 0, 1, stream, p);
 }

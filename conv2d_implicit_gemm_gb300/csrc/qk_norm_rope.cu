@@ -16,6 +16,7 @@
 #include <type_traits>
 
 #include "token_math.cuh"
+#include "token_pairs.cuh"
 #include "token_ptx.cuh"
 #include "token.h"
 
@@ -27,28 +28,6 @@ constexpr int kVecThreads = 128;
 constexpr int kCtasPerSm = 6;  // 80 registers a thread; at 5 and 7 (spills) 81 and 77 us where 6 take 76
 
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7FC00000); }
-
-// Pairs of fp32 values, two operations an instruction.
-__device__ __forceinline__ uint64_t f2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 f2_of(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 
 // P rotation pairs of one head: the first values and the second values of
 // each (half-split), or the pairs one after the other (adjacent).

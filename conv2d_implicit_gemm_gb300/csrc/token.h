@@ -110,6 +110,8 @@ struct LinearTcLaunch {
 // single-token step is bound by the host, and the runtime's launch (symbol
 // look-up, configuration) is most of what this library adds to it.
 struct Kernel {
+  explicit Kernel(int most_smem = 0) : most(most_smem) {}  // of all its launches, where they differ
+  const int most;
   std::atomic<CUfunction> fn[64] = {};  // by device
 
   template <typename... KArgs, typename... Args>

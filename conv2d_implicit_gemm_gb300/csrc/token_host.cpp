@@ -405,6 +405,7 @@ oidnx_status oidnx_token_sync_status(void* stream) {
 cudaError_t oidnx::Kernel::find(const void* kernel, int smem, int device, CUfunction* f) {
   if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
   cudaError_t e = cudaSuccess;
+  smem = std::max(smem, most);
   if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   cudaFunction_t found = nullptr;
   if (e == cudaSuccess) e = cudaGetFuncBySymbol(&found, kernel);
