@@ -40,28 +40,41 @@ struct Tiles {
   double cost = INFINITY;  // ns
 };
 
+// Bytes of queries, keys, values and output at 6.2 TB/s, ns.
+double traffic_ns(const CrossParams& p) {
+  return 2.0 * p.d * p.b * (2.0 * p.kv * p.hk + 2.0 * p.tq * p.hq) / 6200;
+}
+
+// Many queries: rounds of resident CTAs times an item's units of 64 keys, and its
+// ends; what does not fill a round divided over clusters of 2 to 8, if they all fit.
+// Measured, us a unit of one, two and four row tiles: heads of 64 values 0.85, 0.91,
+// 1.30; of 128 0.62, 0.79; of 256 2.1.  8160 queries and keys, 16 heads of 128: 426 in
+// four rounds, 388 with the last divided by two; 8 heads of 64 over 2040 keys: two row
+// tiles 34, divided by two 26.
 Tiles plan_tiles(const CrossParams& p, bool bf16, int device, int sms) {
   Tiles best;
   if (p.group > 128 || p.kv == 0) return best;
   const int per = 128 / p.group, most = cross_most_tiles(p.d);
   const int64_t row_tiles = (static_cast<int64_t>(p.tq) + per - 1) / per;
   const double units = std::max(1, (p.kv + 63) / 64);
-  const double unit_ns = p.d <= 64 ? 330 : p.d <= 128 ? 415 : 830, start_ns = 4000, item_ns = 1500;
-  for (int tiles = 1; tiles <= most; tiles *= 2) {
+  static const double unit_ns[3][3] = {{850, 910, 1300}, {620, 790, 0}, {2100, 0, 0}};
+  const double start_ns = 3000, item_ns = 3000, join_ns = 4000;
+  for (int tiles = 1, at = 0; tiles <= most; tiles *= 2, ++at) {
     const int64_t blocks = (row_tiles + tiles - 1) / tiles, items = blocks * p.b * p.hk;
     if (items > INT_MAX / 2) continue;
-    const double unit = unit_ns * (0.4 + 0.6 * tiles / most);
+    const double unit = unit_ns[p.d <= 64 ? 0 : p.d <= 128 ? 1 : 2][at];
     for (int cluster = 1; cluster <= 8; cluster *= 2) {
       const int slots = cluster == 1 ? sms : cross_tile_slots(p.d, bf16, cluster, device);
       if (slots <= 0) continue;
       int64_t whole = items, rest = 0;
       if (cluster > 1) {
         whole = items / slots * slots, rest = items - whole;
-        if (rest == 0 || rest > slots / cluster || units / cluster < 2) continue;
+        if (rest == 0 || rest > slots / cluster || units < 2 * cluster) continue;
       }
       const double rounds = std::ceil(static_cast<double>(whole) / slots);
       double cost = start_ns + rounds * (item_ns + units * unit);
-      if (rest) cost += item_ns + 3000 + units / cluster * unit;
+      if (rest) cost += item_ns + join_ns + units / cluster * unit;
+      cost = std::max(cost, start_ns + traffic_ns(p));
       if (cost < best.cost) {
         best.tiles = tiles, best.blocks = static_cast<int>(blocks), best.items = static_cast<int>(items);
         best.whole = static_cast<int>(whole), best.cluster = cluster;
@@ -78,23 +91,32 @@ struct Parts {
   double cost = INFINITY;
 };
 
+// Few queries: rounds of resident CTAs times a CTA's keys, and its start.  Measured,
+// us, 16 rows: heads of 64 values 4.3 + 3.7 a thousand keys, of 128 5.0 + 6.8, of 256
+// 6.4 + 13.3; 32 rows 8.2 + 4.8 and 9.5 + 11.  Keys divided over as many CTAs as fit
+// where clusters leave SMs idle: 20000 keys, 8 key heads of 128 21.9 -> 19, one 20.6 ->
+// 10.2 in 38 parts; more of them cost their join (152: 12.1), so a part has 512 keys.
 Parts plan_parts(const CrossParams& p, bool bf16, int device) {
   Parts best;
   const int64_t rows = static_cast<int64_t>(p.tq) * p.group;
   const int per = rows > 16 && p.d <= 128 ? 32 : 16;
   const int64_t row_tiles = (rows + per - 1) / per, units = static_cast<int64_t>(p.b) * p.hk * row_tiles;
-  const double key = (p.d <= 64 ? 5.0 : p.d <= 128 ? 9.1 : 18.0) * (per == 32 ? 1.4 : 1.0), start = p.d <= 64 ? 4000 : 6000;
-  for (int split = 1; split <= 8; split *= 2) {
-    const int slots = cross_token_slots(p, bf16, split, device);
+  const double key = p.d <= 64 ? (per == 32 ? 4.8 : 3.7) : p.d <= 128 ? (per == 32 ? 11 : 6.8) : 13.3;
+  const double start = p.d <= 64 ? (per == 32 ? 8200 : 4300) : p.d <= 128 ? (per == 32 ? 9500 : 5000) : 6400;
+  const double least = start + traffic_ns(p);
+  double joining = 1500;  // 500 for each doubling
+  int slots = 0;
+  for (int split = 8; split >= 1; split /= 2) {
+    slots = cross_token_slots(p, bf16, split, device);
     if (slots <= 0 || units * split > INT_MAX) continue;
     const double rounds = std::ceil(static_cast<double>(units) * split / slots);
-    const double cost = rounds * (static_cast<double>(p.kv) / split * key + start);
-    if (cost < best.cost) best.cost = cost, best.split = split, best.parts = 1;
+    const double cost = std::max(rounds * (static_cast<double>(p.kv) / split * key + start), least) + joining;
+    joining -= 500;
+    if (cost <= best.cost) best.cost = cost, best.split = split, best.parts = 1;
   }
-  const int slots = cross_token_slots(p, bf16, 1, device);
-  const int parts = static_cast<int>(std::min<int64_t>(slots / std::max<int64_t>(units, 1), (p.kv + 127) / 128));
+  const int parts = static_cast<int>(std::min<int64_t>(slots / units, (p.kv + 511) / 512));
   if (parts > 8) {
-    const double cost = static_cast<double>(p.kv) / parts * key + start + 4000;
+    const double cost = std::max(static_cast<double>(p.kv) / parts * key + start, least) + 3000;
     if (cost < best.cost) best.cost = cost, best.split = 1, best.parts = parts;
   }
   return best;

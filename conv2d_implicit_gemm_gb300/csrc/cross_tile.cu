@@ -40,6 +40,7 @@ template <int DB> struct Shape {
   static constexpr int SB = DB == 1 ? 1 : 2;                // score buffers of a row tile
   static constexpr int UPS = DB == 4 ? 1 : 2;               // units of a stage
   static constexpr int NS = DB == 1 ? 3 : 2;                // stages of keys and of values
+  static constexpr int QB = DB == 1 ? 2 : 1;                // buffers of queries; with two the output takes its own queries' place
   static constexpr int NM = DB == 4 ? 1 : 2;                // issuing warps
   static constexpr int TPW = NT / NM;                       // row tiles of one
   static constexpr int kBlock = UPS * kUnit * 128;          // bytes of a stage's 64-value block
@@ -49,19 +50,21 @@ template <int DB> struct Shape {
   static constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 1, kLookWarp = kMmaWarp + NM;
   static constexpr int kThreads = (kLookWarp + 1) * 32;
   static constexpr int kOut = 16384;  // a row tile's 64 values on their way out
-  static constexpr int kSmem = NT * kQTile + 2 * NS * kStage + NT * kOut + 1024 + 512;
+  static constexpr int kSmem = QB * NT * kQTile + 2 * NS * kStage + (QB == 1 ? NT * kOut : 0) + 1024 + 512;
 };
 static_assert(Shape<1>::kSmem <= 227 * 1024 && Shape<2>::kSmem <= 227 * 1024 && Shape<4>::kSmem <= 227 * 1024, "");
-// the parts of a divided item, [row][value] in fp32, take the operands' place
-static_assert(4 * 128 * 64 * 4 <= 4 * Shape<1>::kQTile + 6 * Shape<1>::kStage, "");
-static_assert(2 * 128 * 128 * 4 <= 2 * Shape<2>::kQTile + 4 * Shape<2>::kStage, "");
-static_assert(128 * 256 * 4 <= Shape<4>::kQTile + 4 * Shape<4>::kStage, "");
+// the parts of a divided item, [row][value] in fp32, take the operands' place (with two
+// buffers of queries theirs alone: their statistics stand where values were)
+template <int DB> constexpr int kParts = Shape<DB>::NT * 128 * DB * 64 * 4;
+static_assert(kParts<1> <= Shape<1>::QB * Shape<1>::NT * Shape<1>::kQTile, "");
+static_assert(kParts<2> <= 2 * Shape<2>::kQTile + 4 * Shape<2>::kStage && kParts<4> <= Shape<4>::kQTile + 4 * Shape<4>::kStage, "");
 
 struct TileParams : CrossParams {
   int per;      // queries of a row tile
   int tiles;    // row tiles of an item
   int blocks;   // items of a key head
   int items, whole, cluster;
+  int step_block, step_kvh, step_b;  // from an item to the grid's size behind it
 };
 
 // One item, or a part of its keys; every role computes the same.
@@ -72,33 +75,58 @@ struct Work {
   bool part;
 };
 
+// The items of a CTA: blockIdx.x and every gridDim.x-th from there, by steps (a
+// division takes 400 cycles), then its part of a divided one.
 template <int DB> struct Schedule {
   const TileParams& p;
-  int next;             // item of the next round
+  int next, block, kvh, b;
+  int n, nq;  // of the next item's sequence, on their way
   bool tail;
-  __device__ Schedule(const TileParams& p_) : p(p_), next(blockIdx.x), tail(true) {}
-  __device__ __forceinline__ bool take(Work& w) {
-    int item = next, part = 0, ways = 1;
-    if (next < p.whole) {
-      next += gridDim.x;
-    } else {
-      if (!tail) return false;
-      tail = false;
-      item = p.whole + blockIdx.x / p.cluster;
-      if (item >= p.items) return false;
-      part = blockIdx.x % p.cluster, ways = p.cluster;
+  __device__ __forceinline__ Schedule(const TileParams& p_) : p(p_), next(blockIdx.x), tail(true) {
+    if (next >= p.whole) {
+      next = p.whole + blockIdx.x / p.cluster;
+      tail = next < p.items;
     }
-    const int unit = item / p.blocks, rows = item - unit * p.blocks;
-    w.b = unit / p.hk, w.kvh = unit - w.b * p.hk;
-    w.i0 = rows * p.tiles * p.per;
-    w.n = cross_kv_len(p, w.b), w.nq = cross_q_len(p, w.b);
-    constexpr int KT = Shape<DB>::UPS * kUnit;
-    const int tiles = w.i0 < w.nq ? (w.n + KT - 1) / KT : 0, all = w.i0 < w.nq ? (w.n + kUnit - 1) / kUnit : 0;
-    const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * part / ways);
-    const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (part + 1) / ways);
-    w.u0 = t0 * Shape<DB>::UPS;
-    w.units = min(t1 * Shape<DB>::UPS, all) - w.u0;
-    w.part = ways > 1;
+    locate();
+  }
+  __device__ __forceinline__ void locate() {
+    const int unit = next / p.blocks;
+    block = next - unit * p.blocks;
+    b = unit / p.hk, kvh = unit - b * p.hk;
+    if (b >= p.b) b = 0;  // (no item: its lengths are not used)
+  }
+  __device__ __forceinline__ void lengths() { n = cross_kv_len(p, b), nq = cross_q_len(p, b); }
+  __device__ __forceinline__ bool take(Work& w) {
+    const bool whole = next < p.whole;
+    if (!whole && !tail) return false;
+    w.b = b, w.kvh = kvh, w.i0 = block * p.tiles * p.per;
+    w.n = n, w.nq = nq;
+    w.u0 = 0;
+    w.units = w.i0 < nq ? (n + kUnit - 1) / kUnit : 0;
+    w.part = !whole && p.cluster > 1;
+    if (w.part) {  // whole stages of them
+      constexpr int KT = Shape<DB>::UPS * kUnit;
+      const int part = blockIdx.x % p.cluster;
+      const int64_t tiles = w.i0 < nq ? (n + KT - 1) / KT : 0;
+      w.u0 = static_cast<int>(tiles * part / p.cluster) * Shape<DB>::UPS;
+      w.units = min(static_cast<int>(tiles * (part + 1) / p.cluster) * Shape<DB>::UPS, w.units) - w.u0;
+    }
+    if (!whole) {
+      tail = false;
+      return true;
+    }
+    next += gridDim.x;
+    if (next < p.whole) {
+      block += p.step_block;
+      kvh += p.step_kvh, b += p.step_b;
+      if (block >= p.blocks) block -= p.blocks, ++kvh;
+      if (kvh >= p.hk) kvh -= p.hk, ++b;
+    } else {
+      next = p.whole + blockIdx.x / p.cluster;
+      tail = next < p.items;
+      locate();
+    }
+    lengths();
     return true;
   }
 };
@@ -116,14 +144,16 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
   constexpr int NT = C::NT, SB = C::SB, UPS = C::UPS, NS = C::NS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
-  uint8_t* Q = smem_raw + pad;  // [NT]
-  uint8_t* Ks = Q + NT * C::kQTile;
+  constexpr int QB = C::QB;
+  uint8_t* Q = smem_raw + pad;  // [QB][NT]
+  uint8_t* Ks = Q + QB * NT * C::kQTile;
   uint8_t* Vs = Ks + NS * C::kStage;
-  uint8_t* Out = Vs + NS * C::kStage;  // [NT]
-  float2* stats = reinterpret_cast<float2*>(Out);  // [NT][128]: maximum and sum of a part, once nothing goes out any more
-  uint64_t* qfull = reinterpret_cast<uint64_t*>(Out + NT * C::kOut);  // [NT]
-  uint64_t* qempty = qfull + NT;
-  uint64_t* kfull = qempty + NT;  // [NS]
+  uint8_t* Out = Vs + NS * C::kStage;  // [NT], where it has a place of its own
+  // [NT][128]: maximum and sum of a part, once nothing comes or goes any more
+  float2* stats = reinterpret_cast<float2*>(QB == 1 ? Out : Vs);
+  uint64_t* qfull = reinterpret_cast<uint64_t*>(Out + (QB == 1 ? NT * C::kOut : 0));  // [QB][NT]
+  uint64_t* qempty = qfull + QB * NT;
+  uint64_t* kfull = qempty + QB * NT;  // [NS]
   uint64_t* kempty = kfull + NS;
   uint64_t* vfull = kempty + NS;
   uint64_t* vempty = vfull + NS;
@@ -143,9 +173,11 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
       mbar_init(&vempty[s], p.tiles + 1);  // and the clearing warp
       mbar_init(&vclean[s], 32);
     }
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < QB * NT; ++t) {
       mbar_init(&qfull[t], 1);
       mbar_init(&qempty[t], 1);
+    }
+    for (int t = 0; t < NT; ++t) {
       mbar_init(&odone[t], 1);
       mbar_init(&plast[t], 1);
     }
@@ -156,20 +188,22 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
     fence_mbarrier_init();
   }
   if (warp == C::kMmaWarp) tmem_alloc(slot, 512);
+  if (warp == C::kLoadWarp && lane < 4) prefetch_tmap(lane == 0 ? &map_k : lane == 1 ? &map_q : lane == 2 ? &map_v : &map_o);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
+  Work w;
+  Schedule<DB> work(p);
   griddep_launch_dependents();
   griddep_wait();
+  work.lengths();
   const int kd = (p.d + 15) / 16;  // blocks of 16 values of a head
   // columns: S (then P) of the row tiles' buffers, O of the row tiles
   const auto s_col = [tmem](int t, int c) { return tmem + (t * SB + c) * 64; };
   const auto o_col = [tmem](int t) { return tmem + NT * SB * 64 + t * 64 * DB; };
   // a stage's use count gives its phase: tile g of all that the CTA takes is in stage g % NS
   const bool masked = p.mask != nullptr;
-  Work w;
-  Schedule<DB> work(p);
   bool ok = true;
   // of a softmax thread, after its last item
   float top = -INFINITY, sum = 0.f;
@@ -180,9 +214,30 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
       const uint64_t pol = l2_evict_normal();
       const int q_bytes = p.per * p.group * 128;
       int s = 0, ph = 0, round = 0;
-      while (ok && work.take(w)) {
-        if (w.units <= 0) continue;
+      const auto queries = [&](const Work& q) {  // the round'th item's
+        const int at = round % QB * NT, phase = round / QB & 1;
+        for (int t = 0; t < p.tiles && ok; ++t) {
+          ok = mbar_wait_soon(&qempty[at + t], phase ^ 1, p.status, kErrTimeoutProducer);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&qfull[at + t], DB * q_bytes);
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+            tma_load_4d(Q + (at + t) * C::kQTile + d * 16384, &map_q, &qfull[at + t], d * 64, q.kvh * p.group, q.i0 + t * p.per,
+                        p.q_s[0] ? q.b : 0, pol);
+        }
+        ++round;
+      };
+      const auto next_with_keys = [&](Work& q) {
+        while (work.take(q))
+          if (q.units > 0) return true;
+        return false;
+      };
+      bool more = next_with_keys(w);
+      if (QB == 2 && more) queries(w);
+      while (ok && more) {
         const int tiles = (w.units + UPS - 1) / UPS;
+        Work after;
+        bool another = false;
         for (int j = 0; j < tiles && ok; ++j) {
           const int key = (w.u0 + j * UPS) * kUnit;
           ok = mbar_wait_soon(&kempty[s], ph ^ 1, p.status, kErrTimeoutProducer);
@@ -192,19 +247,8 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
           for (int d = 0; d < DB; ++d)
             tma_load_4d(Ks + s * C::kStage + d * C::kBlock, &map_k, &kfull[s], d * 64, key, p.k_s[2] ? w.kvh : 0,
                         p.k_s[0] ? w.b : 0, pol);
-          if (j == 0) {
-            for (int t = 0; t < p.tiles && ok; ++t) {
-              ok = mbar_wait_soon(&qempty[t], (round & 1) ^ 1, p.status, kErrTimeoutProducer);
-              if (!ok) break;
-              mbar_arrive_expect_tx(&qfull[t], DB * q_bytes);
-#pragma unroll
-              for (int d = 0; d < DB; ++d)
-                tma_load_4d(Q + t * C::kQTile + d * 16384, &map_q, &qfull[t], d * 64, w.kvh * p.group, w.i0 + t * p.per,
-                            p.q_s[0] ? w.b : 0, pol);
-            }
-            if (!ok) break;
-            ++round;
-          }
+          if (QB == 1 && j == 0) queries(w);
+          if (!ok) break;
           ok = mbar_wait_soon(&vempty[s], ph ^ 1, p.status, kErrTimeoutProducer);
           if (!ok) break;
           mbar_arrive_expect_tx(&vfull[s], C::kStage);
@@ -214,6 +258,10 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
                         p.v_s[0] ? w.b : 0, pol);
           if (++s == NS) s = 0, ph ^= 1;
         }
+        if (!ok) break;
+        another = next_with_keys(after);
+        if (QB == 2 && another) queries(after);
+        w = after, more = another;
       }
     }
   } else if (warp >= C::kMmaWarp && warp < C::kLookWarp) {
@@ -231,16 +279,15 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
       uint32_t clean = 0;    // of the cleared stages'
       const auto stage_of = [](int g) { return g % NS; };
       const auto phase_of = [](int g) { return (g / NS) & 1; };
-      const auto score = [&](int t, int u, int keys, int stage) {  // S of unit u
+      const auto score = [&](int t, int u, int keys, int stage, uint32_t to) {  // S of unit u
         const uint32_t id = keys == kUnit ? id_s : idesc_16(bf, 128, (keys + 15) / 16 * 16);
-        const uint64_t qd = q0 + t * (C::kQTile >> 4);
+        const uint64_t qd = q0 + (round % QB * NT + t) * (C::kQTile >> 4);
         const uint64_t kt = k0 + stage * (C::kStage >> 4) + (u % UPS) * (kUnit * 128 >> 4);
 #pragma unroll
         for (int i = 0; i < 4 * DB; ++i)
           if (i < kd)
-            mma_f16_ss(s_col(t, u % SB), qd + (((i >> 2) * 16384 + (i & 3) * 32) >> 4),
+            mma_f16_ss(to, qd + (((i >> 2) * 16384 + (i & 3) * 32) >> 4),
                        kt + (((i >> 2) * C::kBlock + (i & 3) * 32) >> 4), id, i > 0);
-        mma_commit(&sfull[t * SB + u % SB]);
       };
       while (ok && work.take(w)) {
         if (w.units <= 0) continue;
@@ -249,17 +296,18 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
         for (int u = 0; u < SB && u < U && ok; ++u) {
           if (u % UPS == 0) ok = mbar_wait_soon(&kfull[stage_of(g + u / UPS)], phase_of(g + u / UPS), p.status, kErrTimeoutMma);
           for (int t = t0; t < t1 && ok; ++t) {
-            if (u == 0) ok = mbar_wait_soon(&qfull[t], round & 1, p.status, kErrTimeoutMma);
+            if (u == 0) ok = mbar_wait_soon(&qfull[round % QB * NT + t], round / QB & 1, p.status, kErrTimeoutMma);
             if (!ok) break;
             tc_fence_after();
-            score(t, u, min(left - u * kUnit, kUnit), stage_of(g + u / UPS));
+            score(t, u, min(left - u * kUnit, kUnit), stage_of(g + u / UPS), s_col(t, u % SB));
+            mma_commit(&sfull[t * SB + u % SB]);
           }
         }
         for (int u = 0; u < U && ok; ++u) {
           const int gu = g + u / UPS, s = stage_of(gu), nu = u + SB;
           if (u % UPS == 0) {
             ok = mbar_wait_soon(&vfull[s], phase_of(gu), p.status, kErrTimeoutMma);
-            if (ok && (masked || (u + UPS) * kUnit > left)) {
+            if (ok && (masked || (w.n < p.kv && (u + UPS) * kUnit > left))) {
               ok = mbar_wait_soon(&vclean[s], clean >> s & 1, p.status, kErrTimeoutMma);
               clean ^= 1u << s;
             }
@@ -268,7 +316,11 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
           if (ok && nu < U && nu % UPS == 0) ok = mbar_wait_soon(&kfull[stage_of(gn)], phase_of(gn), p.status, kErrTimeoutMma);
           const uint64_t vt = v0 + s * (C::kStage >> 4) + (u % UPS) * (kUnit * 128 >> 4);
           const int steps = (min(left - u * kUnit, kUnit) + 15) / 16;
-          for (int t = t0; t < t1 && ok; ++t) {
+          // the row tile whose weights are there first
+          const int turn = C::TPW == 2 && t1 - t0 == 2 && !mbar_test_wait(&pfull[t0 * SB + u % SB], phase >> (t0 * SB + u % SB) & 1) &&
+                           mbar_test_wait(&pfull[(t0 + 1) * SB + u % SB], phase >> ((t0 + 1) * SB + u % SB) & 1);
+          for (int k = t0; k < t1 && ok; ++k) {
+            const int t = turn ? t0 + t1 - 1 - k : k;
             const int c = t * SB + u % SB;
             ok = mbar_wait_soon(&pfull[c], phase >> c & 1, p.status, kErrTimeoutMma);
             if (!ok) break;
@@ -277,8 +329,12 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kUnit / 16; ++i)
               if (i < steps) mma_ts(o_col(t), s_col(t, u % SB) + i * 8, vt + i * (2048 >> 4), id_pv, u > 0 || i > 0);
-            if (nu < U) score(t, nu, min(left - nu * kUnit, kUnit), stage_of(gn));
-            else if (SB > 1 && u + 2 == U) mma_commit(&plast[t]);
+            if (nu < U) {
+              score(t, nu, min(left - nu * kUnit, kUnit), stage_of(gn), s_col(t, nu % SB));
+              mma_commit(&sfull[t * SB + nu % SB]);
+            } else if (SB > 1 && u + 2 == U) {
+              mma_commit(&plast[t]);
+            }
             if (u + 1 == U) mma_commit(&odone[t]);
           }
         }
@@ -287,7 +343,7 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
       }
     }
   } else if (warp == C::kLookWarp) {
-    // clears the values that no row sees; every tile is waited for and handed back,
+    // Clears the values that no row sees; every tile is waited for and handed back,
     // so that the phases stay in step
     int s = 0, ph = 0;
     while (ok && work.take(w)) {
@@ -305,7 +361,7 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
         }
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&vfull[s], ph, p.status, kErrTimeoutProducer));
         if (!ok) break;
-        if (masked || key + UPS * kUnit > w.n) {
+        if (masked || (w.n < p.kv && key + UPS * kUnit > w.n)) {
           if (!all) {
             for (int r = 0; r < UPS * kUnit; r += 4) {  // four rows of a 64-value block at a time
               const int row = r + lane / 8;
@@ -334,11 +390,15 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
     const int r = threadIdx.x & 127;  // row of the tile = lane of tensor memory
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float c = p.scale * 1.4426950408889634f;  // scores to powers of two
+    const int query = t * p.per + r / p.group, head = r % p.group;  // of the row, from the item's first
+    const bool row_used = r < p.per * p.group;
     uint32_t phase = 0;  // of each buffer's scores
     int g = 0, last_phase = 0, done_phase = 0;
-    while (ok && work.take(w)) {
-      const int i = w.i0 + t * p.per + r / p.group;
-      valid = r < p.per * p.group && i < w.nq;
+    int round = 0;  // items with keys
+    bool more = work.take(w);
+    while (ok && more) {
+      const int i = w.i0 + query;
+      valid = row_used && i < w.nq;
       const int U = max(w.units, 0);
       top = -INFINITY;  // what P is relative to
       sum = 0.f;
@@ -354,7 +414,7 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
       for (int u = 0; u < U; ++u) {
         const int keys = min(w.n - (w.u0 + u) * kUnit, kUnit);
         const int buf = u % SB;
-        uint32_t bits[2] = {below(keys), below(keys - 32)};
+        uint32_t bits[2] = {below(keys), below(keys - 32)};  // which are seen
         if (masked) {
           bits[0] = __ballot_sync(0xFFFFFFFFu, first), bits[1] = __ballot_sync(0xFFFFFFFFu, second);
           if (u + 1 < U) look(u + 1);
@@ -365,31 +425,51 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
         phase ^= 1u << buf;
         tc_fence_after();
         if ((warp & 3) == 0) {  // (whole warps: what follows reads tensor memory)
-          const bool k_done = u % UPS == UPS - 1 || u == U - 1;
-          mbar_arrive_if(lane == 0 && k_done, &kempty[(g + u / UPS) % NS]);
+          mbar_arrive_if(lane == 0 && (u % UPS == UPS - 1 || u == U - 1), &kempty[(g + u / UPS) % NS]);
           const int before = u - SB;  // its values have been read
           if (before >= 0) mbar_arrive_if(lane == 0 && before % UPS == UPS - 1, &vempty[(g + before / UPS) % NS]);
-          mbar_arrive_if(lane == 0 && u == U - 1, &qempty[t]);
+          if constexpr (QB == 1) mbar_arrive_if(lane == 0 && u == U - 1, &qempty[t]);
         }
-        uint32_t raw[2][32];
-        tmem_ld32_nowait(sc, raw[0]);
-        tmem_ld32_nowait(sc + 32, raw[1]);
-        tmem_wait_ld();
-        if ((bits[0] & bits[1]) != 0xFFFFFFFFu) {
+        const auto hide = [](uint32_t seen, uint32_t (&s)[32]) {
+          if (seen != 0xFFFFFFFFu) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+            for (int e = 0; e < 32; ++e) s[e] = seen >> e & 1u ? s[e] : 0xFF800000u;
+          }
+        };
+        const auto largest = [](const uint32_t (&s)[32]) {
+          float m2[2];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) raw[q][e] = bits[q] >> e & 1u ? raw[q][e] : 0xFF800000u;
+          for (int q = 0; q < 2; ++q) {
+            m2[q] = fmaxf(__uint_as_float(s[16 * q]), __uint_as_float(s[16 * q + 1]));
+#pragma unroll
+            for (int e = 2; e < 16; e += 2) m2[q] = max3(m2[q], __uint_as_float(s[16 * q + e]), __uint_as_float(s[16 * q + e + 1]));
+          }
+          return fmaxf(m2[0], m2[1]);
+        };
+        // With four row tiles registers hold 32 scores at a time: the second half is
+        // looked over, let go and read again.
+        constexpr int HELD = SB == 1 ? 1 : 2;
+        uint32_t raw[HELD][32];
+        float m = -INFINITY;
+        if constexpr (HELD == 2) {
+          tmem_ld32_nowait(sc, raw[0]);
+          tmem_ld32_nowait(sc + 32, raw[1]);
+          tmem_wait_ld();
+          hide(bits[0], raw[0]);
+          hide(bits[1], raw[1]);
+          m = fmaxf(largest(raw[0]), largest(raw[1]));
+        } else {
+          if (keys > 32) {
+            tmem_ld32_nowait(sc + 32, raw[0]);
+            tmem_wait_ld();
+            hide(bits[1], raw[0]);
+            m = largest(raw[0]);
+          }
+          tmem_ld32_nowait(sc, raw[0]);
+          tmem_wait_ld();
+          hide(bits[0], raw[0]);
+          m = fmaxf(m, largest(raw[0]));
         }
-        float m4[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t* v = raw[q >> 1] + (q & 1) * 16;
-          m4[q] = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
-#pragma unroll
-          for (int e = 2; e < 16; e += 2) m4[q] = max3(m4[q], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-        }
-        const float m = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
         // (lanes without a query hold whatever shared memory held, and must not
         // decide for the others)
         const bool rise = valid && (m - top) * c > 8.f;
@@ -423,18 +503,27 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
         const float base = top == -INFINITY ? 0.f : top * c - kLift<T>;
         const uint64_t c2 = f2(c, c), b2 = f2(-base, -base);
         uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+        const auto weigh = [&](int q, const uint32_t (&s)[32]) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (q * 32 < keys) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 x = f2_of(fma2(f2(__uint_as_float(raw[q][e]), __uint_as_float(raw[q][e + 1])), c2, b2));
-              const float a = exp2_fast(x.x), b = exp2_fast(x.y);
-              acc[(e >> 1) & 1] = add2(acc[(e >> 1) & 1], f2(a, b));
-              pk[e / 2] = pack2<T>(a, b);
-            }
-            tmem_st16(sc + q * 16, pk);
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = f2_of(fma2(f2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, b2));
+            const float a = exp2_fast(x.x), b = exp2_fast(x.y);
+            acc[(e >> 1) & 1] = add2(acc[(e >> 1) & 1], f2(a, b));
+            pk[e / 2] = pack2<T>(a, b);
+          }
+          tmem_st16(sc + q * 16, pk);
+        };
+        if constexpr (HELD == 2) {
+          weigh(0, raw[0]);
+          if (keys > 32) weigh(1, raw[1]);
+        } else {
+          weigh(0, raw[0]);
+          if (keys > 32) {
+            tmem_ld32_nowait(sc + 32, raw[0]);
+            tmem_wait_ld();
+            hide(bits[1], raw[0]);
+            weigh(1, raw[0]);
           }
         }
         tmem_wait_st();
@@ -442,8 +531,32 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
         mbar_arrive(&pfull[t * SB + buf]);
         const float2 a = f2_of(add2(acc[0], acc[1]));
         sum += a.x + a.y;
+        if (QB == 2 && u == 0 && round > 0) {  // the last item's output has left its buffer by now
+          if (r == 0) {
+            bulk_wait_read<0>();
+            mbar_arrive(&qempty[(round - 1) % QB * NT + t]);
+          }
+          __syncwarp();
+        }
       }
       if (!ok) break;
+      // while the last product runs: the statistics out, the next item
+      const bool some = valid && !(sum == 0.f);
+      const bool part = w.part;
+      const int b = w.b, kvh = w.kvh, i0 = w.i0;
+      if (!part && p.lse && row_used && i < p.tq) {
+        const float base = top == -INFINITY ? 0.f : top * c - kLift<T>;
+        p.lse[(static_cast<int64_t>(w.b) * p.hq + w.kvh * p.group + head) * p.tq + i] =
+            some ? (base + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      }
+      if (U == 0 && !part) {  // nothing is seen
+        if (row_used && i < p.tq) {
+          T* to = static_cast<T*>(p.o) + w.b * p.o_s[0] + i * p.o_s[1] + (w.kvh * p.group + head) * p.o_s[2];
+          for (int x = 0; x < p.d; x += 8) *reinterpret_cast<uint4*>(to + x) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+      }
+      more = work.take(w);
       if (U > 0) {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_soon(&odone[t], done_phase, p.status, kErrTimeoutEpilogue));
         if (!ok) break;
@@ -456,43 +569,40 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
         }
         g += (U + UPS - 1) / UPS;
       }
-      if (w.part) break;  // joined below; always a CTA's last
-      const bool some = valid && !(sum == 0.f);
+      if (part) break;  // joined below; always a CTA's last
+      if (U == 0) continue;
       const float inv = some ? 1.f / sum : 0.f;
-      uint8_t* out = Out + t * C::kOut;
+      uint8_t* out = QB == 1 ? Out + t * C::kOut : Q + (round % QB * NT + t) * C::kQTile;
+      ++round;
 #pragma unroll 1
       for (int d = 0; d * 64 < p.d; ++d) {
-        if (r == 0) bulk_wait_read<0>();  // the last store has read the buffer
-        __syncwarp();
-        named_barrier_sync(1 + t, 128);
+        if (QB == 1) {
+          if (r == 0) bulk_wait_read<0>();  // the last store has read the buffer
+          __syncwarp();
+          named_barrier_sync(1 + t, 128);
+        }
 #pragma unroll 1
-        for (int x = 0; x < 64; x += 16) {
-          uint32_t o[16];
-          if (U > 0) {
-            tmem_ld16_nowait(o_col(t) + lanes + d * 64 + x, o);
-            tmem_wait_ld();
-          }
+        for (int x = 0; x < 64; x += 32) {
+          uint32_t o[32];
+          tmem_ld32_nowait(o_col(t) + lanes + d * 64 + x, o);
+          tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < 4; ++q) {
             float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = some ? __uint_as_float(o[q * 8 + e]) * inv : 0.f;
-            *reinterpret_cast<uint4*>(out + r * 128 + (((x / 8 + q) ^ (r & 7)) << 4)) = Vec16<T>::pack(v);
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[q * 8 + e]) * inv;
+            const uint4 z = Vec16<T>::pack(v);
+            *reinterpret_cast<uint4*>(out + r * 128 + (((x / 8 + q) ^ (r & 7)) << 4)) = some ? z : make_uint4(0u, 0u, 0u, 0u);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();  // (the barrier takes whole warps)
         named_barrier_sync(1 + t, 128);
-        if (r == 0 && w.i0 + t * p.per < p.tq) {
-          tma_store_4d(&map_o, out, d * 64, w.kvh * p.group, w.i0 + t * p.per, w.b);
+        if (r == 0 && i0 + t * p.per < p.tq) {
+          tma_store_4d(&map_o, out, d * 64, kvh * p.group, i0 + t * p.per, b);
           bulk_commit();
         }
         __syncwarp();
-      }
-      if (p.lse && r < p.per * p.group && i < p.tq) {
-        const float base = top == -INFINITY ? 0.f : top * c - kLift<T>;
-        p.lse[(static_cast<int64_t>(w.b) * p.hq + w.kvh * p.group + r % p.group) * p.tq + i] =
-            some ? (base + log2f(sum)) * 0.69314718055994531f : -INFINITY;
       }
       tc_fence_before();  // (the next item's products overwrite what was read)
     }
@@ -503,7 +613,8 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
   // ---- a divided item: each CTA's part to its shared memory, joined over the cluster
   if (p.cluster > 1 && p.whole + static_cast<int>(blockIdx.x) / p.cluster < p.items) {
     Schedule<DB> again(p);
-    again.next = p.whole;
+    again.lengths();
+    while (again.next < p.whole) again.take(w);
     again.take(w);
     tc_fence_before();
     __syncthreads();  // every row tile's products are done: the operands' memory is free
@@ -607,6 +718,8 @@ template <typename T, int DB> cudaError_t launch(const CrossTileLaunch* L, int c
   TileParams p;
   static_cast<CrossParams&>(p) = L->p;
   p.per = L->per, p.tiles = L->tiles, p.blocks = L->blocks, p.items = L->items, p.whole = L->whole, p.cluster = L->cluster;
+  const int units = L->grid / p.blocks;
+  p.step_block = L->grid - units * p.blocks, p.step_b = units / p.hk, p.step_kvh = units - p.step_b * p.hk;
   return handle.launch(kernel, device, dim3(L->grid), C::kThreads, C::kSmem, cluster, stream, L->map_q, L->map_k, L->map_v,
                        L->map_o, p);
 }

@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kChunk = 16;  // keys of one step of a warp
 constexpr int kStages = 3;  // chunks in flight and at work
+constexpr int kMostSplit = 8;  // CTAs of a cluster
 
 template <int DP, int MT> struct Tok {
   static constexpr int kWarps = DP == 256 ? 4 : 8;        // as many rings as shared memory holds
@@ -294,29 +295,37 @@ __global__ void __launch_bounds__(Tok<DP, MT>::kWarps * 32, Tok<DP, MT>::kCtas)
     const float* at = part_o + r * DP + c * 8;
     const float2* st_at = &stats[kWarps * C::kRows + r];
     // every part's loads before the first use (a remote load takes 0.7 us)
-    float2 st[8];
-    float4 u[8], v[8];
+    float m = -INFINITY;
+    float2 st[kMostSplit];
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
+    for (int s = 0; s < kMostSplit; ++s) {
       st[s] = make_float2(-INFINITY, 0.f);
+      if (s >= split) continue;
+      if (split > 1) {
+        const uint32_t sa = map_to_rank(st_at, s);
+        st[s].x = ld_cluster_f32(sa), st[s].y = ld_cluster_f32(sa + 4);
+      } else {
+        st[s] = *st_at;
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kMostSplit; ++s) m = fmaxf(m, st[s].x);
+    const float base = m == -INFINITY ? 0.f : m;
+    float acc[8] = {}, l = 0.f;
+    float4 u[kMostSplit], v[kMostSplit];
+#pragma unroll
+    for (int s = 0; s < kMostSplit; ++s) {
       u[s] = v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (s >= split) continue;
       if (split > 1) {
-        const uint32_t sa = map_to_rank(st_at, s), oa = map_to_rank(at, s);
-        st[s].x = ld_cluster_f32(sa), st[s].y = ld_cluster_f32(sa + 4);
+        const uint32_t oa = map_to_rank(at, s);
         u[s] = ld_cluster_f4(oa), v[s] = ld_cluster_f4(oa + 16);
       } else {
-        st[s] = *st_at;
         u[s] = *reinterpret_cast<const float4*>(at), v[s] = *reinterpret_cast<const float4*>(at + 4);
       }
     }
-    float m = -INFINITY;
 #pragma unroll
-    for (int s = 0; s < 8; ++s) m = fmaxf(m, st[s].x);
-    const float base = m == -INFINITY ? 0.f : m;
-    float acc[8] = {}, l = 0.f;
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
+    for (int s = 0; s < kMostSplit; ++s) {
       const float f = exp2_fast(st[s].x - base);
       l = fmaf(st[s].y, f, l);
       acc[0] = fmaf(u[s].x, f, acc[0]), acc[1] = fmaf(u[s].y, f, acc[1]);
@@ -337,45 +346,61 @@ __global__ void __launch_bounds__(Tok<DP, MT>::kWarps * 32, Tok<DP, MT>::kCtas)
   if (split > 1) cluster_sync();  // a part stays until everyone has read it
 }
 
-// The parts of a row, joined by one warp: eight values a lane.
-template <typename T> __global__ void __launch_bounds__(128) cross_join_kernel(const CrossParams p, const int parts, const float* work) {
+// The parts of a row, joined by a CTA: eight values a thread, as many threads for a
+// piece as there are parts to share among them, so that all loads are in flight.
+constexpr int kJoinThreads = 256;
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const CrossParams p, const int parts, const float* work) {
+  __shared__ float top[kJoinThreads / 32];
+  __shared__ __align__(16) float sums[kJoinThreads][12];  // l and eight values
+  const int tid = threadIdx.x;
+  const int rows = p.tq * p.group, unit = blockIdx.x / rows, row = blockIdx.x - unit * rows;
+  const int size = p.d + 8, pieces = p.d / 8, sharing = kJoinThreads / pieces;
+  const float* at = work + static_cast<int64_t>(blockIdx.x) * parts * size;
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int rows = p.tq * p.group;
-  if (item >= static_cast<int64_t>(p.b) * p.hk * rows) return;
-  const int unit = static_cast<int>(item / rows), row = static_cast<int>(item - static_cast<int64_t>(unit) * rows);
-  const int size = p.d + 8;
-  const float* at = work + item * parts * size;
   float m = -INFINITY;
-  for (int s = lane; s < parts; s += 32) m = fmaxf(m, at[s * size]);
+  for (int s = tid; s < parts; s += kJoinThreads) m = fmaxf(m, at[s * size]);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+  if ((tid & 31) == 0) top[tid >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, top[i]);
   const float base = m == -INFINITY ? 0.f : m;
+  const int c = tid % pieces, first = tid / pieces;
   float acc[8] = {}, l = 0.f;
-  const int c = lane * 8;
+  if (first < sharing) {
 #pragma unroll 4
-  for (int s = 0; s < parts; ++s) {
-    const float2 st = *reinterpret_cast<const float2*>(at + s * size);
-    const float f = exp2_fast(st.x - base);
-    l = fmaf(st.y, f, l);
-    if (c < p.d) {
-      const float4 u = *reinterpret_cast<const float4*>(at + s * size + 8 + c);
-      const float4 v = *reinterpret_cast<const float4*>(at + s * size + 12 + c);
+    for (int s = first; s < parts; s += sharing) {
+      const float2 st = *reinterpret_cast<const float2*>(at + s * size);
+      const float4 u = *reinterpret_cast<const float4*>(at + s * size + 8 + c * 8);
+      const float4 v = *reinterpret_cast<const float4*>(at + s * size + 12 + c * 8);
+      const float f = exp2_fast(st.x - base);
+      l = fmaf(st.y, f, l);
       acc[0] = fmaf(u.x, f, acc[0]), acc[1] = fmaf(u.y, f, acc[1]);
       acc[2] = fmaf(u.z, f, acc[2]), acc[3] = fmaf(u.w, f, acc[3]);
       acc[4] = fmaf(v.x, f, acc[4]), acc[5] = fmaf(v.y, f, acc[5]);
       acc[6] = fmaf(v.z, f, acc[6]), acc[7] = fmaf(v.w, f, acc[7]);
     }
   }
+  sums[tid][0] = l;
+  *reinterpret_cast<float4*>(&sums[tid][4]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  *reinterpret_cast<float4*>(&sums[tid][8]) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+  __syncthreads();
+  if (tid >= pieces) return;
+  for (int i = 1; i < sharing; ++i) {
+    const float* other = sums[tid + i * pieces];
+    l += other[0];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] += other[4 + k];
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] *= inv;
   const int b = unit / p.hk, i = row / p.group, h = (unit - b * p.hk) * p.group + row - i * p.group;
-  if (c < p.d)
-    *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + b * p.o_s[0] + i * p.o_s[1] + h * p.o_s[2] + c) = Vec16<T>::pack(acc);
-  if (p.lse && lane == 0)
+  *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + b * p.o_s[0] + i * p.o_s[1] + h * p.o_s[2] + c * 8) = Vec16<T>::pack(acc);
+  if (p.lse && tid == 0)
     p.lse[(static_cast<int64_t>(b) * p.hq + h) * p.tq + i] =
         l == 0.f ? -INFINITY : (m - kLift<T> + log2f(l)) * 0.69314718055994531f;
 }
@@ -411,7 +436,7 @@ template <typename T> cudaError_t launch_both(const CrossTokenLaunch& L, cudaStr
   if (e != cudaSuccess || L.parts == 1) return e;
   static Kernel handle;
   const int64_t rows = static_cast<int64_t>(L.p.b) * L.p.hk * L.p.tq * L.p.group;
-  return handle.launch(cross_join_kernel<T>, L.device, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, 1, stream, L.p,
+  return handle.launch(cross_join_kernel<T>, L.device, dim3(static_cast<unsigned>(rows)), kJoinThreads, 0, 1, stream, L.p,
                        L.parts, static_cast<const float*>(L.work));
 }
 
