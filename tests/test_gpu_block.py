@@ -493,3 +493,129 @@ def test_cross_repeated_tokens_and_heads(tq):
     done()
     ref = tokens.cross_attention(f64(q), f64(back.flip(1)), f64(v), [tq] * 2, [90] * 2, None, 0.125)
     check_cross_result(f64(o), lse, *ref, "fp16", 64, 90)
+
+
+# ---------------------------------------------------------------- all of them
+def example_of(name):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", name + ".py")
+    spec = importlib.util.spec_from_file_location(name, path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("sizes", [dict(), dict(channels=384, heads=6, key_heads=2, head=80, text=200, length=130),
+                                   dict(batch=3, shape=(1, 7, 9), length=1)])
+def test_a_block_of_them_follows_its_definition(sizes, dtype):
+    """The example's block against 64 bits: twelve roundings to 16 bits lie on the way of the last norm, none of whose
+    relative errors (half a unit at most) a norm, an average or a projection of random weights enlarges beyond its factor
+    of at most 2 (scale, gate and weights together)."""
+    total, normed = example_of("video_block").run(dtype=dtype, **sizes)
+    unit = UNIT["fp16" if dtype == torch.float16 else "bf16"]
+    assert total <= 24 * unit and normed <= 24 * unit
+
+
+def calls_of_every_form():
+    """One call of each form, each writing the returned tensors."""
+    out = []
+
+    def cross(b, tq, kv, hq, hk, d, pad=0, mask=False):
+        q, k, v = strided((b, tq, hq, d), "bf16", tq, [0, 0, 0, pad]), strided((b, kv, hk, d), "bf16", kv), strided((b, kv, hk, d), "bf16", 3)
+        o, lse = strided((b, tq, hq, d), "bf16", 4, [0, 0, 0, pad]), torch.empty(b, hq, tq, device="cuda")
+        seen = (torch.arange(kv, device="cuda") % 5 > 0).to(torch.uint8)[None].repeat(b, 1) if mask else None
+        out.append((lambda: cross_attention(q, k, v, o, lse, None, None, seen, d ** -0.5, "bf16"), (o, lse)))
+
+    cross(2, 1, 300, 4, 2, 64)              # few queries
+    cross(1, 1, 3000, 4, 4, 128)            # divided over a cluster
+    cross(1, 1, 30000, 2, 1, 128)           # over many CTAs, with a kernel that joins them
+    cross(3, 700, 333, 6, 2, 80, mask=True) # tiles
+    cross(1, 300, 5000, 2, 2, 64)           # tiles divided over a cluster
+    cross(2, 200, 150, 4, 4, 60, pad=1)     # copied first
+    for t, n in ((3, 500), (3, 501), (900, 1024), (900, 1001), (400, 17000)):
+        x, w = strided((t, n), "bf16", t), strided((n,), "bf16", n)
+        r, s, y = strided((t, n), "fp32", 2), torch.empty(t, n, device="cuda"), torch.empty(t, n, dtype=torch.bfloat16, device="cuda")
+        out.append((lambda x=x, r=r, s=s, y=y, w=w, t=t: block_norm(x, r, s, y, "rms", w, None, "layer", w, w, 1e-6, None, "plain",
+                                                               None, None, None, t, 1, 1.0, 0.5, "bf16", "fp32"), (s, y)))
+    for d in (128, 66):
+        q, k, v = (strided((50, h, d), "bf16", h) for h in (4, 2, 2))
+        got = [torch.empty_like(z) for z in (q, k, v)]
+        table = torch.randn(60, 24, device="cuda")
+        at = torch.arange(150, dtype=torch.int32, device="cuda").view(3, 50) % 60
+        out.append((lambda q=q, k=k, v=v, got=got, table=table, at=at: norm_rope_axes(
+            q, got[0], k, got[1], v, got[2], True, None, None, 1e-6, table, table, at, [r % 3 for r in range(24)], None, False, "bf16"), got))
+    return out
+
+
+def test_block_calls_captured_and_replayed_on_two_streams_at_once():
+    """Two graphs of every form, each with its own outputs, replayed at the same time, give what the calls gave."""
+    sets = [calls_of_every_form() for _ in range(2)]
+    graphs, refs = [], []
+    for calls in sets:
+        for call, _ in calls:
+            call()
+        done()
+        refs.append([t.clone() for _, outs in calls for t in outs])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for call, _ in calls:
+                call()
+        graphs.append(g)
+        for _, outs in calls:
+            for t in outs:
+                t.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for calls, ref in zip(sets, refs):
+        assert all(torch.equal(a, b) for a, b in zip([t for _, outs in calls for t in outs], ref))
+
+
+def test_block_results_do_not_depend_on_the_stream_or_on_what_ran_before():
+    calls = calls_of_every_form()
+    loud = [strided((2, 300, 4, d), "fp16", 4, scale=30.0) for d in (64, 128, 256)]
+    first = None
+    side = torch.cuda.Stream()
+    for s in (torch.cuda.current_stream(), side, side, torch.cuda.current_stream()):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            for x in loud:
+                cross_attention(x, x, x, torch.empty_like(x), None, None, None, None, 1.0, "fp16")
+            for call, _ in calls:
+                call()
+            done()
+            got = [t.clone() for _, outs in calls for t in outs]
+        torch.cuda.synchronize()
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
+def test_block_calls_from_a_thread_of_its_own():
+    import threading
+    calls = calls_of_every_form()
+    for call, _ in calls:
+        call()
+    done()
+    ref = [t.clone() for _, outs in calls for t in outs]
+    failed = []
+
+    def work():
+        try:
+            for call, _ in calls:
+                call()
+            done()
+        except Exception as e:
+            failed.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    assert all(torch.equal(a, b) for a, b in zip([t for _, outs in calls for t in outs], ref))
