@@ -43,6 +43,7 @@ template <int DB> struct Shape {
   static constexpr int QB = DB == 1 ? 2 : 1;                // buffers of queries; with two the output takes its own queries' place
   static constexpr int NM = DB == 4 ? 1 : 2;                // issuing warps
   static constexpr int TPW = NT / NM;                       // row tiles of one
+  static constexpr bool kGives = TPW == 1;                  // it hands the stages back itself (commits); else the softmax warps do
   static constexpr int kBlock = UPS * kUnit * 128;          // bytes of a stage's 64-value block
   static constexpr int kStage = DB * kBlock;
   static constexpr int kQTile = DB * 16384;
@@ -301,6 +302,7 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
             tc_fence_after();
             score(t, u, min(left - u * kUnit, kUnit), stage_of(g + u / UPS), s_col(t, u % SB));
             mma_commit(&sfull[t * SB + u % SB]);
+            if (C::kGives && (u % UPS == UPS - 1 || u == U - 1)) mma_commit(&kempty[stage_of(g + u / UPS)]);
           }
         }
         for (int u = 0; u < U && ok; ++u) {
@@ -329,9 +331,11 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kUnit / 16; ++i)
               if (i < steps) mma_ts(o_col(t), s_col(t, u % SB) + i * 8, vt + i * (2048 >> 4), id_pv, u > 0 || i > 0);
+            if (C::kGives && (u % UPS == UPS - 1 || u == U - 1)) mma_commit(&vempty[s]);
             if (nu < U) {
               score(t, nu, min(left - nu * kUnit, kUnit), stage_of(gn), s_col(t, nu % SB));
               mma_commit(&sfull[t * SB + nu % SB]);
+              if (C::kGives && (nu % UPS == UPS - 1 || nu == U - 1)) mma_commit(&kempty[stage_of(gn)]);
             } else if (SB > 1 && u + 2 == U) {
               mma_commit(&plast[t]);
             }
@@ -425,17 +429,18 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
         phase ^= 1u << buf;
         tc_fence_after();
         if ((warp & 3) == 0) {  // (whole warps: what follows reads tensor memory)
-          mbar_arrive_if(lane == 0 && (u % UPS == UPS - 1 || u == U - 1), &kempty[(g + u / UPS) % NS]);
-          const int before = u - SB;  // its values have been read
-          if (before >= 0) mbar_arrive_if(lane == 0 && before % UPS == UPS - 1, &vempty[(g + before / UPS) % NS]);
+          if constexpr (!C::kGives) {
+            mbar_arrive_if(lane == 0 && (u % UPS == UPS - 1 || u == U - 1), &kempty[(g + u / UPS) % NS]);
+            const int before = u - SB;  // its values have been read
+            if (before >= 0) mbar_arrive_if(lane == 0 && before % UPS == UPS - 1, &vempty[(g + before / UPS) % NS]);
+          }
           if constexpr (QB == 1) mbar_arrive_if(lane == 0 && u == U - 1, &qempty[t]);
         }
         const auto hide = [](uint32_t seen, uint32_t (&s)[32]) {
-          if (seen != 0xFFFFFFFFu) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = seen >> e & 1u ? s[e] : 0xFF800000u;
-          }
+          for (int e = 0; e < 32; ++e) s[e] = seen >> e & 1u ? s[e] : 0xFF800000u;
         };
+        const bool hidden = (bits[0] & bits[1]) != 0xFFFFFFFFu;
         const auto largest = [](const uint32_t (&s)[32]) {
           float m2[2];
 #pragma unroll
@@ -455,19 +460,18 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
           tmem_ld32_nowait(sc, raw[0]);
           tmem_ld32_nowait(sc + 32, raw[1]);
           tmem_wait_ld();
-          hide(bits[0], raw[0]);
-          hide(bits[1], raw[1]);
+          if (hidden) hide(bits[0], raw[0]), hide(bits[1], raw[1]);
           m = fmaxf(largest(raw[0]), largest(raw[1]));
         } else {
           if (keys > 32) {
             tmem_ld32_nowait(sc + 32, raw[0]);
             tmem_wait_ld();
-            hide(bits[1], raw[0]);
+            if (hidden) hide(bits[1], raw[0]);
             m = largest(raw[0]);
           }
           tmem_ld32_nowait(sc, raw[0]);
           tmem_wait_ld();
-          hide(bits[0], raw[0]);
+          if (hidden) hide(bits[0], raw[0]);
           m = fmaxf(m, largest(raw[0]));
         }
         // (lanes without a query hold whatever shared memory held, and must not
@@ -522,7 +526,7 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
           if (keys > 32) {
             tmem_ld32_nowait(sc + 32, raw[0]);
             tmem_wait_ld();
-            hide(bits[1], raw[0]);
+            if (hidden) hide(bits[1], raw[0]);
             weigh(1, raw[0]);
           }
         }
@@ -563,11 +567,13 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
         done_phase ^= 1;
         if (SB > 1 && U > 1) last_phase ^= 1;
         tc_fence_after();
-        if ((warp & 3) == 0) {
-          for (int u = max(U - SB, 0); u < U; ++u)
-            mbar_arrive_if(lane == 0 && (u % UPS == UPS - 1 || u == U - 1), &vempty[(g + u / UPS) % NS]);
+        if constexpr (!C::kGives) {
+          if ((warp & 3) == 0) {
+            for (int u = max(U - SB, 0); u < U; ++u)
+              mbar_arrive_if(lane == 0 && (u % UPS == UPS - 1 || u == U - 1), &vempty[(g + u / UPS) % NS]);
+          }
+          g += (U + UPS - 1) / UPS;
         }
-        g += (U + UPS - 1) / UPS;
       }
       if (part) break;  // joined below; always a CTA's last
       if (U == 0) continue;
