@@ -48,16 +48,16 @@ double traffic_ns(const CrossParams& p) {
 // Many queries: rounds of resident CTAs times an item's units of 64 keys, and its
 // ends; what does not fill a round divided over clusters of 2 to 8, if they all fit.
 // Measured, us a unit of one, two and four row tiles: heads of 64 values 0.85, 0.91,
-// 1.30; of 128 0.62, 0.79; of 256 2.1.  8160 queries and keys, 16 heads of 128: 426 in
-// four rounds, 388 with the last divided by two; 8 heads of 64 over 2040 keys: two row
-// tiles 34, divided by two 26.
+// 1.30; of 128 0.60, 0.78; of 256 1.6.  8160 queries and keys, 16 heads of 128: 398 in
+// four rounds, 363 with the last divided by two; 8 heads of 64 over 2040 keys: two row
+// tiles 36, divided by two 27.
 Tiles plan_tiles(const CrossParams& p, bool bf16, int device, int sms) {
   Tiles best;
   if (p.group > 128 || p.kv == 0) return best;
   const int per = 128 / p.group, most = cross_most_tiles(p.d);
   const int64_t row_tiles = (static_cast<int64_t>(p.tq) + per - 1) / per;
   const double units = std::max(1, (p.kv + 63) / 64);
-  static const double unit_ns[3][3] = {{850, 910, 1300}, {620, 790, 0}, {2100, 0, 0}};
+  static const double unit_ns[3][3] = {{850, 910, 1300}, {600, 780, 0}, {1600, 0, 0}};
   const double start_ns = 3000, item_ns = 3000, join_ns = 4000;
   for (int tiles = 1, at = 0; tiles <= most; tiles *= 2, ++at) {
     const int64_t blocks = (row_tiles + tiles - 1) / tiles, items = blocks * p.b * p.hk;
@@ -327,6 +327,8 @@ oidnx_status oidnx_cross_attention(const void* q, long long q_sb, long long q_st
   if (b == 0 || tq == 0 || hq == 0) return finish(cudaSuccess, "cross_attention");
   if (static_cast<double>(b) * tq * hq > 4e9)
     return fail(OIDNX_ERR_UNSUPPORTED, "cross_attention: more than 4e9 query heads");
+  if (static_cast<int64_t>(tq) * (hq / hk) > kMost)
+    return fail(OIDNX_ERR_UNSUPPORTED, "cross_attention: more than 2^30 queries of a key head");
   if (!q || !o || (kv > 0 && (!k || !v))) return fail(OIDNX_ERR_INVALID_ARGUMENT, "cross_attention: NULL q, k, v or o");
   if (!aligned(q, 2) || !aligned(k, 2) || !aligned(v, 2) || !aligned(o, 2) || !aligned(lse, 4) || !aligned(q_lens, 4) ||
       !aligned(kv_lens, 4))

@@ -468,7 +468,9 @@ enum { OIDNX_GATE_PLAIN = 0, OIDNX_GATE_TANH = 1, OIDNX_GATE_SIGMOID = 2 };
  * scale and shift 0).  residual NULL: none.  sum and y receive s and y; either
  * may be NULL.  pre works on s before its rounding.  A row whose m is outside
  * [0, count) is padding: nothing of it is written.  sum may be the residual and
- * y may be x (same pointer, stride and type); they overlap nothing else.
+ * y may be x (same pointer, stride and type); they overlap nothing else.  (Rows
+ * off 16 bytes are read from the 16 bytes that they start in to those that they
+ * end in; what lies around them there is not used.)
  * precision: OIDNX_PRECISION_FP32, _FP16 or _BF16, of x, y and the vectors;
  * sum_precision, of residual and sum: the same, or _FP32, or _AUTO (the same).
  * Errors: INVALID_ARGUMENT (NULL, sizes, strides shorter than rows, misaligned
@@ -519,7 +521,8 @@ oidnx_status oidnx_qk_norm_rope_axes(const void* q, long long q_st, long long q_
  * heads are not whole 16-byte pieces on 16 bytes are copied first.
  * Errors: INVALID_ARGUMENT (NULL, sizes, hq not a multiple of hk, scale, mask
  * stride below kv and not 0, misaligned pointers, unknown precision), UNSUPPORTED
- * (fp32, d > 256, over 4e9 query heads), OUT_OF_MEMORY, CUDA.  */
+ * (fp32, d > 256, over 4e9 query heads, over 2^30 queries of a key head),
+ * OUT_OF_MEMORY, CUDA.  */
 oidnx_status oidnx_cross_attention(const void* q, long long q_sb, long long q_st, long long q_sh, const void* k,
                                    long long k_sb, long long k_st, long long k_sh, const void* v, long long v_sb,
                                    long long v_st, long long v_sh, void* o, long long o_sb, long long o_st,

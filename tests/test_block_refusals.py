@@ -82,7 +82,7 @@ def test_axes_of_too_few_pairs_or_of_no_bytes(ox):
     (dict(v=0), INVALID), (dict(o=0), INVALID), (dict(k=P + 1), INVALID), (dict(lse=P + 2), INVALID),
     (dict(kv_lens=P + 1), INVALID), (dict(mask=P, mask_sb=15), INVALID), (dict(precision=0), INVALID),
     (dict(precision=1), UNSUPPORTED), (dict(d=257), UNSUPPORTED), (dict(b=100000, tq=100000), UNSUPPORTED),
-    (dict(kv=2 ** 30 + 1), UNSUPPORTED),
+    (dict(kv=2 ** 30 + 1), UNSUPPORTED), (dict(tq=2 ** 29, hq=4, hk=1), UNSUPPORTED),
 ])
 def test_cross_attention_refuses(ox, change, status):
     with pytest.raises(ox.OidnxError) as e:

@@ -26,7 +26,7 @@ def check_block(t, n, kind, total_kind=None, post="rms", pre="rms", gate="groups
                 bias=True, weight=True, residual=True, total=True, y=True, per=None, count=None, groups=None, alpha=1.0,
                 beta=1.0, pad=0, shift_at=0, seed=0, inplace=False, mean=0.3, eps=1e-5):
     total_kind = total_kind or kind
-    per = per or max(1, t)
+    per = max(1, t) if per is None else per
     count = count if count is not None else (t + per - 1) // per
 
     def vector(i, **how):
@@ -619,3 +619,63 @@ def test_block_calls_from_a_thread_of_its_own():
     torch.cuda.synchronize()
     assert not failed
     assert all(torch.equal(a, b) for a, b in zip([t for _, outs in calls for t in outs], ref))
+
+
+# ---------------------------------------------------------------- what the calls take besides
+@pytest.mark.parametrize("tq", [1, 300])
+def test_cross_lengths_outside_the_buffers(tq):
+    """More keys or queries than there is room for are read as what there is; fewer than none as none."""
+    q, k, v = strided((4, tq, 2, 64), "bf16", 1), strided((4, 100, 2, 64), "bf16", 2), strided((4, 100, 2, 64), "bf16", 3)
+    ql, kl = [tq + 5, tq, -3, 2 ** 31 - 1], [101, -1, 50, 2 ** 31 - 1]
+    o, lse = torch.full_like(q, 9), torch.full((4, 2, tq), 9.0, device="cuda")
+    cross_attention(q, k, v, o, lse, torch.tensor(ql, dtype=torch.int32, device="cuda"),
+                    torch.tensor(kl, dtype=torch.int32, device="cuda"), None, 0.125, "bf16")
+    done()
+    ref = tokens.cross_attention(f64(q), f64(k), f64(v), [tq, tq, 0, tq], [100, 0, 50, 100], None, 0.125)
+    check_cross_result(f64(o), lse, *ref, "bf16", 64, 100)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_cross_one_mask_row_and_no_statistics(d):
+    """A mask shared by all sequences through a stride of 0, lse left out."""
+    q, k, v = strided((3, 200, 4, d), "fp16", 1), strided((3, 140, 4, d), "fp16", 2), strided((3, 140, 4, d), "fp16", 3)
+    mask = (torch.arange(140, device="cuda") % 7 > 2).to(torch.uint8)
+    o = torch.zeros_like(q)
+    cross_attention(q, k, v, o, None, None, None, mask[None].expand(3, 140), d ** -0.5, "fp16")
+    done()
+    ref = tokens.cross_attention(f64(q), f64(k), f64(v), [200] * 3, [140] * 3, np.broadcast_to(mask.cpu().numpy(), (3, 140)), d ** -0.5)
+    check_cross_result(f64(o), None, *ref, "fp16", d, 140)
+
+
+def test_cross_more_heads_a_key_head_than_a_row_tile_has_rows():
+    check_cross(1, 70, 333, 200, 1, 128, "bf16", seed=2)
+
+
+@pytest.mark.parametrize("tq", [1, 200])
+def test_cross_queries_of_a_fused_projection(tq):
+    """Queries, keys and values as one projection wrote them, in one buffer."""
+    qkv = strided((2, tq, 12, 64), "bf16", 1)
+    q, k, v = qkv[:, :, :8], qkv[:, :, 8:10], qkv[:, :, 10:]
+    o, lse = torch.empty(2, tq, 8, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 8, tq, device="cuda")
+    cross_attention(q, k, v, o, lse, None, None, None, 0.125, "bf16")
+    done()
+    ref = tokens.cross_attention(f64(q), f64(k), f64(v), [tq] * 2, [tq] * 2, None, 0.125)
+    check_cross_result(f64(o), lse, *ref, "bf16", 64, tq)
+
+
+@pytest.mark.parametrize("t,n", [(5, 320), (1000, 321)])
+def test_block_norm_groups_without_a_count_of_rows(t, n):
+    """Rows named by groups need no per; the same group may come back."""
+    rng = np.random.default_rng(t)
+    check_block(t, n, "fp16", per=0, count=4, groups=np.sort(rng.integers(0, 4, t))[rng.permutation(t)])
+
+
+def test_block_norm_small_values_and_no_eps():
+    """Values whose squares are far below 1, and eps = 0."""
+    x = strided((400, 512), "bf16", 1, scale=1e-12)
+    y = torch.empty_like(x)
+    block_norm(x, None, None, y, "none", None, None, "layer", None, None, 0.0, None, "plain", None, None, None, 400, 1, 1.0, 1.0,
+               "bf16", "bf16")
+    done()
+    _, ref, _, size = tokens.block_norm(f64(x), None, "none", None, None, "layer", None, None, 0.0, None, "plain", None, None, 1.0, 1.0)
+    assert_within(f64(y), ref, UNIT["bf16"] * np.abs(ref) + 96 * 2.0 ** -24 * size)
