@@ -233,8 +233,7 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
           if (q.units > 0) return true;
         return false;
       };
-      bool more = next_with_keys(w);
-      if (QB == 2 && more) queries(w);
+      bool more = next_with_keys(w), first = true;
       while (ok && more) {
         const int tiles = (w.units + UPS - 1) / UPS;
         Work after;
@@ -248,7 +247,7 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
           for (int d = 0; d < DB; ++d)
             tma_load_4d(Ks + s * C::kStage + d * C::kBlock, &map_k, &kfull[s], d * 64, key, p.k_s[2] ? w.kvh : 0,
                         p.k_s[0] ? w.b : 0, pol);
-          if (QB == 1 && j == 0) queries(w);
+          if ((QB == 1 || first) && j == 0) queries(w);
           if (!ok) break;
           ok = mbar_wait_soon(&vempty[s], ph ^ 1, p.status, kErrTimeoutProducer);
           if (!ok) break;
@@ -262,7 +261,7 @@ __global__ void __launch_bounds__(Shape<DB>::kThreads, 1)
         if (!ok) break;
         another = next_with_keys(after);
         if (QB == 2 && another) queries(after);
-        w = after, more = another;
+        w = after, more = another, first = false;
       }
     }
   } else if (warp >= C::kMmaWarp && warp < C::kLookWarp) {
