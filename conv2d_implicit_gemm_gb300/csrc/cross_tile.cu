@@ -24,6 +24,22 @@
 //    does not fill a round of CTAs is divided: a cluster takes an item, each CTA a
 //    part of its keys, and the parts are joined over distributed shared memory.
 //
+// Heads of over 64 values are bound by the tensor cores: for 64 keys the operands of a
+// row tile's two products take 640 cycles through shared memory (its queries are read
+// again for each unit), two tiles 1280 of some 1500, and a long run lowers the clock:
+// 8160 queries and keys, 16 heads of 128, 363 us, 1500 TFLOP/s, 398 without the last
+// round divided; 392 with all of the softmax's arithmetic left out.  Stages handed back
+// by the softmax warps instead of the issuing threads: 423.  2040 x 2040, 4 heads of
+// 256: 39 us (47).
+// Heads of up to 64 are bound by the chain from scores to weights to the next scores,
+// four of which share an SM's issue slots: 8160 x 8160, 16 heads of 64, 326 us, 840
+// TFLOP/s (276 without the softmax's arithmetic).  Four row tiles of 8160 queries to 77
+// keys, 4 x 16 heads of 64: 38 us, of which 5 are a CTA's start and 3.7 each of seven
+// items, 5.3 TB/s.  Not kept: weights in columns of their own, with the next scores made
+// under the softmax, for three tiles (431 us); one issuing thread for four tiles (477);
+// two tiles of two buffers (403); outputs sent off by a warp of their own (text 43); both
+// units of a short text at once (no faster).
+//
 // Warps 4 t .. 4 t + 3: softmax of row tile t, rescaling, output; then a warp that
 // loads (TMA), one or two that issue the products, one that clears values.
 #include "attn_prompt.cuh"

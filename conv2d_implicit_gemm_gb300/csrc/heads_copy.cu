@@ -1,7 +1,7 @@
 // Copies of heads [sequence][token][head][value] of any strides and alignment to
 // heads of whole 16-byte pieces, or back: for operands that the tensor-core forms
-// cannot load as they lie.  Values past the source's are zeros.  Bound by memory,
-// at two bytes a lane and request on the unaligned side.
+// cannot load as they lie.  Values past the source's are zeros.  Bound by its
+// requests, two bytes a lane: a slow way in for calls that are rare.
 #include <algorithm>
 
 #include "cross.h"

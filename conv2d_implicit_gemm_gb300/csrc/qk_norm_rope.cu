@@ -12,6 +12,9 @@
 // every head, and with one head a lane group of a persistent CTA, it took 90 us.
 // One token: 1.9 us on the device.  8192 tokens in fp32: 65 us, 6.3 TB/s, 93% (bf16 42,
 // where each byte costs twice the arithmetic).
+// Positions of several axes: 32640 tokens of three axes, 48 heads of 128, bf16, 142 us,
+// 5.7 TB/s, 84%, whether the axes take turns over the pairs or follow one another (fp32
+// 95%); one token 2.1 us.
 #include <algorithm>
 #include <type_traits>
 
