@@ -30,18 +30,24 @@ __device__ __forceinline__ float gate_of(float g, int act) {
 template <int V, int E> struct Mine {
   static constexpr int PAIRS = E / 2, N = E / V;
   int first, step, count;  // pieces first, first + step, ..; those within the row
-  __device__ __forceinline__ Mine(int tid, int team, int n) : first(tid * V), step(team * V) {
-    count = first < n ? (n - first + step - 1) / step : 0;
+  bool full;               // single ones, all of the warp's within it
+  __device__ __forceinline__ Mine(int first, int step, int n) : first(first), step(step) {
+    count = first < n ? min((n - first + step - 1) / step, N) : 0;
+    full = V == 1 && (first | (min(step, 32) - 1)) + step * (N - 1) < n;
   }
   template <typename U> static constexpr int kWords = V == 8 ? E * static_cast<int>(sizeof(U)) / 4 : E;
 
   // (words past the row are left alone)
   template <typename U, int W> __device__ __forceinline__ void fetch(const U* p, uint32_t (&w)[W]) const {
+    if (full) fetch_part<true>(p, w);
+    else fetch_part<false>(p, w);
+  }
+  template <bool ALL, typename U, int W> __device__ __forceinline__ void fetch_part(const U* p, uint32_t (&w)[W]) const {
     static_assert(W == kWords<U>, "");
     p += first;
 #pragma unroll
     for (int c = 0; c < N; ++c, p += step) {
-      if (c < count) {
+      if (ALL || c < count) {
         if constexpr (V == 8) {
           constexpr int Q = sizeof(U) / 2;
 #pragma unroll
@@ -62,8 +68,10 @@ template <int V, int E> struct Mine {
     for (int i = 0; i < PAIRS; ++i) {
       if constexpr (sizeof(U) == 4) {
         v[i] = f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+      } else if constexpr (V == 1) {
+        v[i] = f2(unpack2<U>(w[2 * i]).x, unpack2<U>(w[2 * i + 1]).x);
       } else {
-        const float2 u = unpack2<U>(V == 8 ? w[i] : w[2 * i] | w[2 * i + 1] << 16);
+        const float2 u = unpack2<U>(w[i]);
         v[i] = f2(u.x, u.y);
       }
     }
@@ -81,10 +89,14 @@ template <int V, int E> struct Mine {
       if constexpr (sizeof(U) == 4) w[2 * i] = __float_as_uint(u.x), w[2 * i + 1] = __float_as_uint(u.y);
       else w[i] = pack2<U>(u.x, u.y);
     }
+    if (full) store_part<true>(p, w);
+    else store_part<false>(p, w);
+  }
+  template <bool ALL, typename U, int W> __device__ __forceinline__ void store_part(U* p, const uint32_t (&w)[W]) const {
     p += first;
 #pragma unroll
     for (int c = 0; c < N; ++c, p += step) {
-      if (c < count) {
+      if (ALL || c < count) {
         if constexpr (V == 8) {
           constexpr int Q = sizeof(U) / 2;
 #pragma unroll
@@ -101,6 +113,7 @@ template <int V, int E> struct Mine {
   }
   // zeros in the places past the row
   __device__ __forceinline__ void clear(uint64_t (&v)[PAIRS]) const {
+    if (full) return;
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) {
       if constexpr (V == 8) {
@@ -139,7 +152,7 @@ template <typename T, typename S, int V, int E>
 __global__ void __launch_bounds__(kMostThreads) block_norm_kernel(const BlockParams p) {
   constexpr int TH = kMostThreads, PAIRS = E / 2;
   __shared__ __align__(16) float parts[2][kMostThreads / 32];
-  const Mine<V, E> own(threadIdx.x, TH, p.n);
+  const Mine<V, E> own(threadIdx.x * V, TH * V, p.n);
   const float inv_n = 1.f / static_cast<float>(p.n);
   int flip = 0;
   griddep_launch_dependents();
@@ -230,38 +243,50 @@ __global__ void __launch_bounds__(kMostThreads) block_norm_kernel(const BlockPar
   }
 }
 
-// Many rows of up to 8192 values: teams of `team` threads take consecutive rows, 16
-// values a thread.  Rows come through a ring in shared memory (cp.async, several
-// rows ahead), and what stands beside a row (weights, gate, modulation) is
-// multiplied together once a group and stays in registers:
+// Many rows of up to 8192 values: teams of 8 or 16 lanes of a warp or of whole warps
+// take consecutive rows, 16 values a thread.  Rows come through a ring in shared memory
+// (cp.async, several rows ahead), and what stands beside a row (weights, gate,
+// modulation) is multiplied together once a group and stays in registers:
 //
 //   s = alpha r + a (x - mean) root + b,   a = beta g w_post,   b = beta g b_post
 //   y = (s - mean) root c + d,             c = (1 + scale) w_pre, d = (1 + scale) b_pre + shift
 //
 // A thread copies the pieces that it will read itself.  Rows that do not start on 16
-// bytes are copied by the whole team, from the 16 bytes that they start in to the 16
-// that they end in (which are in their pages).
+// bytes are copied by each warp for itself, from the 16 bytes that its 512 values start
+// in to the 16 that they end in (which are in their pages).
 //
-// 16384 rows of 4096 in bf16: 101 us, 5.3 TB/s, 78% of the measured copy rate (of 2048:
-// 92 us, of 512: 101); with an fp32 sum 143 us, 83%; odd widths half of that, a value at
-// a time.  Without the sums' waits 4096 took 99: what is left is instructions (32 a
-// value).  Not kept: rows side by side sharing a wait (105 to 127 us, as registers
-// spilled into what shared memory leaves of L1), what stands beside the rows in shared
-// memory (124 and up, the same), rows copied whole by one thread (178).
+// 16384 rows of 4096 in bf16: 93 us, 5.8 TB/s, 85% of the measured copy rate (8192 of
+// 8192 100, 131072 of 512 101, 262144 of 128 50); with an fp32 sum 136 us, 88%.  Odd
+// widths, a value at a time: 16384 of 4095 142 us, 65536 of 1001 123.  What is left is
+// instructions.  All 128 registers are taken, and one spilled word costs 15 to 20%
+// beside what the ring leaves of L1: what can be made again from the row is.  Not kept:
+// teams of powers of two in warps, their values apart by the team's width (101, 143, 219,
+// and 140 for rows of 128 on a whole warp), rows side by side sharing a wait (105 to 127
+// us), what stands beside the rows in shared memory (124 and up), rows copied whole by
+// one thread (178), a check of the team's width in one kernel for all (17% more).
 constexpr int kMostStages = 8;
 constexpr int kRingThreads = 512;
+constexpr int kMostParts = 32;  // 8 teams of 2 warps, in fours
 struct RingParams : BlockParams {
   int team, stages;
   int x_bytes, stage_bytes;  // of a stage: x, then the residual
 };
 constexpr int kRingBytes = 200 * 1024;  // of an SM's shared memory
 
-template <typename T, typename S, int V>
+// Teams of LANES threads, or of warps, each with 16 x 32 consecutive values.
+template <typename T, typename S, int V, int LANES>
 __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const RingParams p) {
   constexpr int PAIRS = 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) float parts[2][kRingThreads / 32];
-  const int team = p.team, mine = threadIdx.x / team, tid = threadIdx.x - mine * team, warps = team / 32;
+  __shared__ __align__(16) float parts[2][kMostParts];
+  const int team = LANES < 32 ? LANES : p.team, mine = threadIdx.x / team, tid = threadIdx.x - mine * team;
+  const int warps = team / 32, slots = (warps + 3) & ~3;
+  // the team's lanes of its warp
+  const uint32_t lanes = LANES < 32 ? ((1u << (LANES & 31)) - 1u) << (threadIdx.x & 31 & ~(LANES - 1)) : 0xFFFFFFFFu;
+  if constexpr (LANES == 32) {  // (those of no warp stay zero)
+    if (threadIdx.x < 2 * kMostParts) parts[0][threadIdx.x] = 0.f;
+    __syncthreads();
+  }
   uint8_t* ring = smem + mine * p.stages * p.stage_bytes;
   const int64_t teams = static_cast<int64_t>(gridDim.x) * (blockDim.x / team);
   const int64_t at = static_cast<int64_t>(blockIdx.x) * (blockDim.x / team) + mine;
@@ -269,12 +294,15 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
   griddep_launch_dependents();
   griddep_wait();
 
-  const Mine<V, 16> own(tid, team, p.n);
+  const Mine<V, 16> own(tid / LANES * (LANES * 16) + tid % LANES * V, LANES * V, p.n);
   // bytes of a row's first 16 that stand before it
-  const auto skip = [](const void* q) { return V == 8 ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(q) & 15u); };
+  const auto skip = [](const auto* q, int row, int64_t ld) {
+    const uint32_t start = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(q));
+    return V == 8 ? 0u : (start + row * static_cast<uint32_t>(ld * sizeof(*q))) & 15u;
+  };
+  const uint32_t warp = V == 8 ? 0u : tid / LANES;
   const T* x_next = static_cast<const T*>(p.x) + begin * p.ldx;  // the row that is fetched next
   const S* r_next = static_cast<const S*>(p.residual) + (p.residual ? begin * p.ldr : 0);
-  int fetched = begin, to_stage = 0;
   const auto copy_row = [&](uint32_t to, const auto* row) {
     constexpr int size = sizeof(*row);
     if constexpr (V == 8) {
@@ -287,40 +315,40 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
                        reinterpret_cast<const uint8_t*>(row + own.first + c * own.step) + 16 * k, 16u);
         }
     } else {
-      const uint32_t before = skip(row), bytes = before + p.n * size;
+      // (a warp's part starts 16 bytes further on than the last one's, which its first 16 bytes end)
+      const uint32_t before = reinterpret_cast<uintptr_t>(row) & 15u;
+      const uint32_t most = before + min(static_cast<uint32_t>(p.n), (warp + 1) * 16 * LANES) * size;
       const uint8_t* from = reinterpret_cast<const uint8_t*>(row) - before;
-      for (uint32_t k = tid * 16; k < bytes; k += team * 16) cp_async16(to + k, from + k, 16u);
+      for (uint32_t k = warp * 16 * LANES * size + tid % LANES * 16; k < most; k += LANES * 16)
+        cp_async16(to + k + warp * 16, from + k, 16u);
     }
   };
-  const auto fetch = [&] {
-    if (fetched < end) {
-      const uint32_t to = smem_u32(ring + to_stage * p.stage_bytes);
+  const auto fetch = [&](int row, int stage) {
+    if (row < end) {
+      const uint32_t to = smem_u32(ring + stage * p.stage_bytes);
       copy_row(to, x_next);
       x_next += p.ldx;
       if (p.residual) {
         copy_row(to + p.x_bytes, r_next);
         r_next += p.ldr;
       }
-      ++fetched;
-      if (++to_stage == p.stages) to_stage = 0;
     }
     cp_async_commit();
   };
-  for (int s = 0; s + 1 < p.stages; ++s) fetch();
+  for (int s = 0; s + 1 < p.stages; ++s) fetch(begin + s, s);
 
   const float inv_n = 1.f / static_cast<float>(p.n);
   int flip = 0;
   // sum over the team, the same in all its threads
   const auto team_sum = [&](float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if (warps == 1) return v;
-    float* to = parts[flip] + mine * warps;
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(lanes, v, o);
+    if (LANES < 32 || warps == 1) return v;
+    float* to = parts[flip] + mine * slots;
     flip ^= 1;
     if ((threadIdx.x & 31) == 0) to[tid >> 5] = v;
     __syncwarp();
     named_barrier_sync(1 + mine, team);
-    if (warps == 2) return to[0] + to[1];
     float4 q = *reinterpret_cast<const float4*>(to);
     v = (q.x + q.y) + (q.z + q.w);
     for (int i = 4; i < warps; i += 4) {
@@ -370,8 +398,6 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
   bool kept = false;
   S* sum_row = static_cast<S*>(p.sum) + (p.sum ? begin * p.ld_sum : 0);
   T* y_row = static_cast<T*>(p.y) + (p.y ? begin * p.ldy : 0);
-  const T* x_row = static_cast<const T*>(p.x) + begin * p.ldx;
-  const S* r_row = static_cast<const S*>(p.residual) + (p.residual ? begin * p.ldr : 0);
   int stage = 0;
 #pragma unroll 1
   for (int row = begin; row < end; ++row) {
@@ -420,21 +446,18 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
       case 7: cp_async_wait<5>(); break;
       default: cp_async_wait<6>(); break;
     }
-    if constexpr (V == 1) {  // the team has copied it together
-      __syncwarp();
-      if (warps > 1) named_barrier_sync(1 + mine, team);
-    }
-    fetch();  // over the last row, which every reader is done with
-    const uint8_t* from = ring + stage * p.stage_bytes;
+    if constexpr (V == 1) __syncwarp(lanes);  // its lanes have copied its part together
+    fetch(row + p.stages - 1, (stage == 0 ? p.stages : stage) - 1);  // over the last row, which every reader is done with
+    const uint8_t* from = ring + stage * p.stage_bytes + warp * 16;
     if (kept) {
-      own.load(reinterpret_cast<const T*>(from + skip(x_row)), v);
+      own.load(reinterpret_cast<const T*>(from + skip(static_cast<const T*>(p.x), row, p.ldx)), v);
       statistics(p.norm[0]);
       const uint64_t roots = f2(root, root), shifts = f2(-mean * root, -mean * root);
 #pragma unroll
       for (int i = 0; i < PAIRS; ++i) v[i] = fma2(fma2(v[i], roots, shifts), ca[i], cb[i]);
       if (p.residual) {
         uint64_t r[PAIRS];
-        own.load(reinterpret_cast<const S*>(from + p.x_bytes + skip(r_row)), r);
+        own.load(reinterpret_cast<const S*>(from + p.x_bytes + skip(static_cast<const S*>(p.residual), row, p.ldr)), r);
         const uint64_t alpha = f2(p.alpha, p.alpha);
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) v[i] = fma2(r[i], alpha, v[i]);
@@ -451,7 +474,6 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
       own.store(y_row, v);
     }
     sum_row += p.ld_sum, y_row += p.ldy;
-    if constexpr (V == 1) x_row += p.ldx, r_row += p.ldr;
     if (++stage == p.stages) stage = 0;
   }
 }
@@ -520,30 +542,39 @@ cudaError_t launch_rows(const BlockParams& p, int device, int sms, cudaStream_t 
   return handle.launch(block_norm_kernel<T, S, V, E>, device, dim3(std::min(p.t, 4 * sms)), kMostThreads, 0, 1, stream, p);
 }
 
-template <typename T, typename S, int V>
-cudaError_t launch_ring(const BlockParams& p, int device, int sms, cudaStream_t stream) {
+template <typename T, typename S, int V, int LANES>
+cudaError_t launch_teams(const BlockParams& p, int device, int sms, cudaStream_t stream) {
   RingParams q;
   static_cast<BlockParams&>(q) = p;
-  q.team = 32;
-  while (q.team * 16 < p.n) q.team *= 2;
-  const int threads = std::max(q.team, 256), teams = threads / q.team;
-  q.x_bytes = (p.n * static_cast<int>(sizeof(T)) + 31) / 16 * 16;
-  q.stage_bytes = q.x_bytes + (p.residual ? (p.n * static_cast<int>(sizeof(S)) + 31) / 16 * 16 : 0);
-  const int budget = kRingBytes / (kRingThreads / threads) / teams;
-  q.stages = std::min(kMostStages, budget / q.stage_bytes);
-  const int64_t most = static_cast<int64_t>(sms) * (kRingThreads / threads), want = (static_cast<int64_t>(p.t) + teams - 1) / teams;
+  q.team = LANES < 32 ? LANES : (p.n + 511) / 512 * 32;
+  // two CTAs an SM, or one where that holds more teams
+  const int ctas = kRingThreads / q.team > kRingThreads / 2 / q.team * 2 ? 1 : 2, teams = kRingThreads / ctas / q.team;
+  const int beside = V == 8 ? 0 : 15 + 16 * std::max(1, q.team / 32);  // before a row, and between its warps' parts
+  const auto bytes = [&](int size) { return (p.n * size + beside + 15) / 16 * 16; };
+  q.x_bytes = bytes(sizeof(T));
+  q.stage_bytes = q.x_bytes + (p.residual ? bytes(sizeof(S)) : 0);
+  q.stages = std::min(kMostStages, kRingBytes / ctas / teams / q.stage_bytes);
+  const int64_t most = static_cast<int64_t>(sms) * ctas, want = (static_cast<int64_t>(p.t) + teams - 1) / teams;
   static Kernel handle(kRingBytes);
-  return handle.launch(block_norm_ring_kernel<T, S, V>, device, dim3(static_cast<unsigned>(std::min(most, want))), threads,
-                       teams * q.stages * q.stage_bytes, 1, stream, q);
+  return handle.launch(block_norm_ring_kernel<T, S, V, LANES>, device, dim3(static_cast<unsigned>(std::min(most, want))),
+                       teams * q.team, teams * q.stages * q.stage_bytes, 1, stream, q);
+}
+
+template <typename T, typename S, int V>
+cudaError_t launch_ring(const BlockParams& p, int device, int sms, cudaStream_t stream) {
+  if (p.n <= 128) return launch_teams<T, S, V, 8>(p, device, sms, stream);
+  if (p.n <= 256) return launch_teams<T, S, V, 16>(p, device, sms, stream);
+  return launch_teams<T, S, V, 32>(p, device, sms, stream);
 }
 
 template <typename T, typename S>
 cudaError_t launch_t(const BlockParams& p, bool vector, int device, int sms, cudaStream_t stream) {
   const int n = p.n;
   // Rows of a CTA each start sooner, teams keep what stands beside the rows: us, bf16,
-  // 153, 300 and 608 rows of 1024 values 3.3, 3.4, 6.2 and 3.7, 3.8, 3.8; of 4096 3.6,
-  // 5.0, 9.1 and 4.3, 5.8, 8.4; 153 and 300 rows of 8192 9.3, 10.4 and 7.7, 8.8.
-  if (p.t > (n <= kMostThreads * 8 ? 2 : 1) * sms && n <= kRingThreads * 16)
+  // 153, 300 and 608 rows of 1024 values 3.3, 3.4, 6.2 and 3.4, 3.6, 3.6; of 4096 3.6,
+  // 4.8, 9.1 and 4.1, 5.4, 7.7; 153 and 300 rows of 8192 9.3, 10.4 and 7.2, 8.2, of 128
+  // 3.3, 3.4 and 3.1, 3.1.
+  if (p.t > (n > 256 && n <= kMostThreads * 8 ? 2 : 1) * sms && n <= kRingThreads * 16)
     return vector ? launch_ring<T, S, 8>(p, device, sms, stream) : launch_ring<T, S, 1>(p, device, sms, stream);
   if (n <= kMostThreads * 8)
     return vector ? launch_rows<T, S, 8, 8>(p, device, sms, stream) : launch_rows<T, S, 1, 8>(p, device, sms, stream);

@@ -110,6 +110,15 @@ def test_block_norm_strides_and_alignment(n, pad, shift_at):
     check_block(5, n, "fp16", per=2, pad=pad, shift_at=shift_at)
 
 
+@pytest.mark.parametrize("pad,shift_at", [(0, 0), (8, 8), (3, 1)])
+@pytest.mark.parametrize("n", [1, 8, 15, 16, 120, 128, 129, 136, 248, 256, 257, 264, 504, 512, 513, 520, 1024, 1025, 1032, 1544,
+                               2600, 4104, 4609, 7680, 7681, 8191, 8192])
+@pytest.mark.parametrize("kind,total_kind", [("fp16", "fp16"), ("bf16", "fp32"), ("fp32", "fp32")])
+def test_block_norm_many_rows_of_each_width(n, pad, shift_at, kind, total_kind):
+    """Rows of a part of a warp, of one warp, of two to sixteen, on and off 16 bytes."""
+    check_block(641, n, kind, total_kind, post="layer", pre="rms", per=200, pad=pad, shift_at=shift_at, seed=n)
+
+
 @pytest.mark.parametrize("n", [64, 1001, 4096, 17001])
 @pytest.mark.parametrize("t", [3, 700])
 def test_block_norm_in_place(n, t):
