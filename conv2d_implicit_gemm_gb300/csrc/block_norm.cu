@@ -81,13 +81,27 @@ template <int V, int E> struct Mine {
     fetch(p, w);
     pairs<U>(w, v);
   }
-  template <typename U> __device__ __forceinline__ void store(U* p, const uint64_t (&v)[PAIRS]) const {
+  // (whole: fp32 rows that start on 32 bytes)
+  template <typename U> __device__ __forceinline__ void store(U* p, const uint64_t (&v)[PAIRS], bool whole = false) const {
     uint32_t w[E * sizeof(U) / 4];
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) {
       const float2 u = f2_of(v[i]);
       if constexpr (sizeof(U) == 4) w[2 * i] = __float_as_uint(u.x), w[2 * i + 1] = __float_as_uint(u.y);
       else w[i] = pack2<U>(u.x, u.y);
+    }
+    if constexpr (V == 8 && sizeof(U) == 4) {
+      if (whole) {
+        p += first;
+#pragma unroll
+        for (int c = 0; c < N; ++c, p += step)
+          if (c < count)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[c * 8]), "r"(w[c * 8 + 1]),
+                         "r"(w[c * 8 + 2]), "r"(w[c * 8 + 3]), "r"(w[c * 8 + 4]), "r"(w[c * 8 + 5]), "r"(w[c * 8 + 6]),
+                         "r"(w[c * 8 + 7])
+                         : "memory");
+        return;
+      }
     }
     if (full) store_part<true>(p, w);
     else store_part<false>(p, w);
@@ -255,23 +269,23 @@ __global__ void __launch_bounds__(kMostThreads) block_norm_kernel(const BlockPar
 // bytes are copied by each warp for itself, from the 16 bytes that its 512 values start
 // in to the 16 that they end in (which are in their pages).
 //
-// 16384 rows of 4096 in bf16: 93 us, 5.8 TB/s, 85% of the measured copy rate (8192 of
-// 8192 100, 131072 of 512 101, 262144 of 128 50); with an fp32 sum 136 us, 88%.  Odd
-// widths, a value at a time: 16384 of 4095 142 us, 65536 of 1001 123.  What is left is
-// instructions.  All 128 registers are taken, and one spilled word costs 15 to 20%
-// beside what the ring leaves of L1: what can be made again from the row is.  Not kept:
-// teams of powers of two in warps, their values apart by the team's width (101, 143, 219,
-// and 140 for rows of 128 on a whole warp), rows side by side sharing a wait (105 to 127
-// us), what stands beside the rows in shared memory (124 and up), rows copied whole by
-// one thread (178), a check of the team's width in one kernel for all (17% more).
-constexpr int kMostStages = 8;
+// 16384 rows of 4096 in bf16: 89 us, 6.0 TB/s, 89% of the measured copy rate (8192 of
+// 8192 98, 131072 of 512 86, 262144 of 128 47); with an fp32 sum 126 us, 94%.  Odd
+// widths, a value at a time: 16384 of 4095 139 us, 65536 of 1001 119; what bounds these
+// is instructions.  All 128 registers are taken, so what can be made again from the row
+// is (3 to 7% of an odd width).  Not kept: teams of powers of two in warps, their values
+// apart by the team's width (101, 143, 219, and 140 for rows of 128 on a whole warp),
+// rows side by side sharing a wait (105 to 127 us), what stands beside the rows in shared
+// memory (124 and up), rows copied whole by one thread (178), a check of the team's width
+// in one kernel for all (17% more), fp32 rows copied lane by lane (1% either way).
 constexpr int kRingThreads = 512;
 constexpr int kMostParts = 32;  // 8 teams of 2 warps, in fours
 struct RingParams : BlockParams {
   int team, stages;
   int x_bytes, stage_bytes;  // of a stage: x, then the residual
+  bool whole_sum, whole_y;   // fp32 rows that start on 32 bytes
 };
-constexpr int kRingBytes = 200 * 1024;  // of an SM's shared memory
+constexpr int kRingBytes = 144 * 1024;  // 8192 fp32 values and their residuals twice, and what stands beside rows
 
 // Teams of LANES threads, or of warps, each with 16 x 32 consecutive values.
 template <typename T, typename S, int V, int LANES>
@@ -437,15 +451,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
       }
     }
     // rows stages - 1 at most are in flight: this one is the oldest
-    switch (p.stages) {
-      case 2: cp_async_wait<0>(); break;
-      case 3: cp_async_wait<1>(); break;
-      case 4: cp_async_wait<2>(); break;
-      case 5: cp_async_wait<3>(); break;
-      case 6: cp_async_wait<4>(); break;
-      case 7: cp_async_wait<5>(); break;
-      default: cp_async_wait<6>(); break;
-    }
+    if (p.stages == 2) cp_async_wait<0>();
+    else cp_async_wait<1>();
     if constexpr (V == 1) __syncwarp(lanes);  // its lanes have copied its part together
     fetch(row + p.stages - 1, (stage == 0 ? p.stages : stage) - 1);  // over the last row, which every reader is done with
     const uint8_t* from = ring + stage * p.stage_bytes + warp * 16;
@@ -462,7 +469,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) v[i] = fma2(r[i], alpha, v[i]);
       }
-      if (p.sum) own.store(sum_row, v);
+      if (p.sum) own.store(sum_row, v, p.whole_sum);
       if (p.y) {
         statistics(p.norm[1]);
       }
@@ -471,7 +478,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
       const uint64_t roots = f2(root, root), shifts = f2(-mean * root, -mean * root);
 #pragma unroll
       for (int i = 0; i < PAIRS; ++i) v[i] = fma2(fma2(v[i], roots, shifts), cc[i], cd[i]);
-      own.store(y_row, v);
+      own.store(y_row, v, p.whole_y);
     }
     sum_row += p.ld_sum, y_row += p.ldy;
     if (++stage == p.stages) stage = 0;
@@ -553,7 +560,14 @@ cudaError_t launch_teams(const BlockParams& p, int device, int sms, cudaStream_t
   const auto bytes = [&](int size) { return (p.n * size + beside + 15) / 16 * 16; };
   q.x_bytes = bytes(sizeof(T));
   q.stage_bytes = q.x_bytes + (p.residual ? bytes(sizeof(S)) : 0);
-  q.stages = std::min(kMostStages, kRingBytes / ctas / teams / q.stage_bytes);
+  // One row ahead, for one or two teams two while that is 64 KB at most: more in flight
+  // slows the writes down (us with 2, 3 and as many stages as fit: 131072 rows of 512 86,
+  // 100, 101, of 2048 89, 92, 94, with an fp32 sum 16384 of 4096 126, 147, 146; but 16384
+  // of 4096 95, 91, 93 and 8192 of 8192 98, 97, 100).
+  const int all = teams * ctas;
+  q.stages = all <= 2 && 2 * all * q.stage_bytes <= 64 * 1024 ? 3 : 2;
+  const auto whole = [](const void* q, int64_t ld) { return (reinterpret_cast<uintptr_t>(q) | ld * sizeof(float)) % 32 == 0; };
+  q.whole_sum = whole(p.sum, p.ld_sum), q.whole_y = whole(p.y, p.ldy);
   const int64_t most = static_cast<int64_t>(sms) * ctas, want = (static_cast<int64_t>(p.t) + teams - 1) / teams;
   static Kernel handle(kRingBytes);
   return handle.launch(block_norm_ring_kernel<T, S, V, LANES>, device, dim3(static_cast<unsigned>(std::min(most, want))),
