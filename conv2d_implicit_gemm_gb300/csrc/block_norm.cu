@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kMostThreads) block_norm_kernel(const BlockPar
 // memory (124 and up), rows copied whole by one thread (178), a check of the team's width
 // in one kernel for all (17% more), fp32 rows copied lane by lane (1% either way).
 constexpr int kRingThreads = 512;
-constexpr int kMostParts = 32;  // 8 teams of 2 warps, in fours
+constexpr int kMostParts = 32;  // in fours a team: 8 teams of a warp, 3 of 5
 struct RingParams : BlockParams {
   int team, stages;
   int x_bytes, stage_bytes;  // of a stage: x, then the residual
@@ -585,9 +585,9 @@ template <typename T, typename S>
 cudaError_t launch_t(const BlockParams& p, bool vector, int device, int sms, cudaStream_t stream) {
   const int n = p.n;
   // Rows of a CTA each start sooner, teams keep what stands beside the rows: us, bf16,
-  // 153, 300 and 608 rows of 1024 values 3.3, 3.4, 6.2 and 3.4, 3.6, 3.6; of 4096 3.6,
-  // 4.8, 9.1 and 4.1, 5.4, 7.7; 153 and 300 rows of 8192 9.3, 10.4 and 7.2, 8.2, of 128
-  // 3.3, 3.4 and 3.1, 3.1.
+  // 153, 300 and 608 rows of 1024 values 3.3, 3.4, 6.2 and 3.4, 3.4, 3.4; of 4096 3.6,
+  // 4.8, 9.1 and 3.9, 5.3, 7.6; 153 and 300 rows of 8192 9.3, 10.4 and 7.1, 8.1, of 128
+  // 3.3, 3.4 and 2.9, 2.9.
   if (p.t > (n > 256 && n <= kMostThreads * 8 ? 2 : 1) * sms && n <= kRingThreads * 16)
     return vector ? launch_ring<T, S, 8>(p, device, sms, stream) : launch_ring<T, S, 1>(p, device, sms, stream);
   if (n <= kMostThreads * 8)
