@@ -294,7 +294,9 @@ oidnx_status oidnx_block_norm(const void* x, long long ldx, const void* residual
   BlockParams p = {};
   p.x = x, p.residual = residual, p.sum = sum, p.y = y;
   p.ldx = ldx, p.ldr = ldr, p.ld_sum = ld_sum, p.ldy = ldy;
-  p.weight[0] = post_weight, p.weight[1] = pre_weight, p.bias[0] = post_bias, p.bias[1] = pre_bias;
+  // without a norm there is nothing that its weight and bias go to
+  if (post != OIDNX_NORM_NONE) p.weight[0] = post_weight, p.bias[0] = post_bias;
+  if (pre != OIDNX_NORM_NONE) p.weight[1] = pre_weight, p.bias[1] = pre_bias;
   p.gate = gate, p.scale = scale, p.shift = shift;
   p.ldg = ldg, p.lds = lds, p.ldh = ldh;
   p.groups = groups, p.per = per, p.count = count;

@@ -459,7 +459,7 @@ enum { OIDNX_GATE_PLAIN = 0, OIDNX_GATE_TANH = 1, OIDNX_GATE_SIGMOID = 2 };
  *   y[i] = pre(s[i]) (1 + scale[m]) + shift[m]
  * for the rows i < t of n values, with m = groups[i], or i / per where groups is
  * NULL.  post and pre are
- *   OIDNX_NORM_NONE   z
+ *   OIDNX_NORM_NONE   z (its weight and bias are not used)
  *   OIDNX_NORM_RMS    z / sqrt(mean(z^2) + eps) weight + bias
  *   OIDNX_NORM_LAYER  (z - mean(z)) / sqrt(mean((z - mean(z))^2) + eps) weight + bias
  * (weight, bias [n]; NULL: 1 and 0) and g is the value itself, its tanh or its
