@@ -161,6 +161,61 @@ template <int TH> __device__ __forceinline__ float row_sum(float v, float (*part
   return v;
 }
 
+// A row a value at a time, made again from x and the residual for each sum over it, its
+// factors one after the other: the thread's pieces of V values from `first` on, `step`
+// apart, below `end`.  sum_of adds over the row's threads.  (A value is written by the
+// thread that read it last, so outputs may be their inputs here too.)
+template <typename T, typename S, int V, typename Sum>
+__device__ __forceinline__ void by_values(const BlockParams& p, int64_t row, int m, int first, int step, int end, const Sum& sum_of) {
+  const float inv_n = 1.f / static_cast<float>(p.n);
+  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+  const S* residual = p.residual ? static_cast<const S*>(p.residual) + row * p.ldr : nullptr;
+  float mean[2] = {0.f, 0.f}, scale[2] = {1.f, 1.f};
+  const auto normed = [&](int which, float v, int e) {
+    if (p.norm[which] == OIDNX_NORM_NONE) return v;
+    v = (v - mean[which]) * scale[which];
+    if (p.weight[which]) v *= to_f32<T>(static_cast<const T*>(p.weight[which])[e]);
+    if (p.bias[which]) v += to_f32<T>(static_cast<const T*>(p.bias[which])[e]);
+    return v;
+  };
+  const auto total = [&](int e) {
+    float v = normed(0, to_f32<T>(x[e]), e);
+    if (p.gate) v *= gate_of(to_f32<T>(static_cast<const T*>(p.gate)[m * p.ldg + e]), p.gate_act);
+    v *= p.beta;
+    return residual ? fmaf(p.alpha, to_f32<S>(residual[e]), v) : v;
+  };
+  for (int which = 0; which < (p.y ? 2 : 1); ++which) {
+    if (p.norm[which] == OIDNX_NORM_NONE) continue;
+    for (int power = p.norm[which] == OIDNX_NORM_LAYER ? 1 : 2; power <= 2; ++power) {
+      // sums of up to 2^30 / 512 values a thread: in parts of 256, so that small ones are not lost
+      float sum = 0.f, part = 0.f;
+      int k = 0;
+      for (int at = first; at < end; at += step) {
+        for (int e = at; e < at + V; ++e) {
+          const float v = which ? total(e) : to_f32<T>(x[e]);
+          const float c = v - mean[which];
+          part = power == 1 ? part + v : fmaf(c, c, part);
+          if ((++k & 255) == 0) sum += part, part = 0.f;
+        }
+      }
+      const float all = sum_of(sum + part) * inv_n;
+      if (power == 1) mean[which] = all;
+      else scale[which] = inverse_root(all + p.eps);
+    }
+  }
+  for (int at = first; at < end; at += step) {
+    for (int e = at; e < at + V; ++e) {
+      float v = total(e);
+      if (p.sum) static_cast<S*>(p.sum)[row * p.ld_sum + e] = from_f32<S>(v);
+      if (!p.y) continue;
+      v = normed(1, v, e);
+      if (p.scale) v *= 1.f + to_f32<T>(static_cast<const T*>(p.scale)[m * p.lds + e]);
+      if (p.shift) v += to_f32<T>(static_cast<const T*>(p.shift)[m * p.ldh + e]);
+      static_cast<T*>(p.y)[row * p.ldy + e] = from_f32<T>(v);
+    }
+  }
+}
+
 // Few rows, or long ones: a CTA a row of up to 512 x E values.
 template <typename T, typename S, int V, int E>
 __global__ void __launch_bounds__(kMostThreads) block_norm_kernel(const BlockParams p) {
@@ -245,8 +300,9 @@ __global__ void __launch_bounds__(kMostThreads) block_norm_kernel(const BlockPar
     normalise(1);
     if (p.scale) {
       own.load(static_cast<const T*>(p.scale) + m * p.lds, f);
+      const uint64_t one = f2(1.f, 1.f);  // (not v + v scale: an infinite v under a negative scale)
 #pragma unroll
-      for (int i = 0; i < PAIRS; ++i) v[i] = fma2(v[i], f[i], v[i]);
+      for (int i = 0; i < PAIRS; ++i) v[i] = mul2(v[i], add2(f[i], one));
     }
     if (p.shift) {
       own.load(static_cast<const T*>(p.shift) + m * p.ldh, f);
@@ -264,6 +320,10 @@ __global__ void __launch_bounds__(kMostThreads) block_norm_kernel(const BlockPar
 //
 //   s = alpha r + a (x - mean) root + b,   a = beta g w_post,   b = beta g b_post
 //   y = (s - mean) root c + d,             c = (1 + scale) w_pre, d = (1 + scale) b_pre + shift
+//
+// Where such a product is beyond fp32 (a gate of infinity; factors of 1e30 and 1e-30) the
+// team's rows from there on go value by value, their factors one after the other as in the
+// other kernels.
 //
 // A thread copies the pieces that it will read itself.  Rows that do not start on 16
 // bytes are copied by each warp for itself, from the 16 bytes that its 512 values start
@@ -287,14 +347,66 @@ struct RingParams : BlockParams {
 };
 constexpr int kRingBytes = 144 * 1024;  // 8192 fp32 values and their residuals twice, and what stands beside rows
 
+// Whether v is true for any of the barrier's threads.
+__device__ __forceinline__ bool named_barrier_any(int id, int threads, bool v) {
+  int r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n selp.s32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<int>(v))
+      : "memory");
+  return r != 0;
+}
+
+// Sum over a team, the same in all its threads.
+template <int LANES>
+__device__ __forceinline__ float sum_of_team(float v, int team, int mine, float (*parts)[kMostParts], int& flip) {
+  const int warps = team / 32, slots = (warps + 3) & ~3;
+  const uint32_t lanes = LANES < 32 ? ((1u << (LANES & 31)) - 1u) << (threadIdx.x & 31 & ~(LANES - 1)) : 0xFFFFFFFFu;
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(lanes, v, o);
+  if (LANES < 32 || warps == 1) return v;
+  float* to = parts[flip] + mine * slots;
+  flip ^= 1;
+  if ((threadIdx.x & 31) == 0) to[(threadIdx.x - mine * team) >> 5] = v;
+  __syncwarp();
+  named_barrier_sync(1 + mine, team);
+  float4 q = *reinterpret_cast<const float4*>(to);
+  v = (q.x + q.y) + (q.z + q.w);
+  for (int i = 4; i < warps; i += 4) {
+    q = *reinterpret_cast<const float4*>(to + i);
+    v += (q.x + q.y) + (q.z + q.w);
+  }
+  return v;
+}
+
+// The rows from `row` to `end` of a team value by value: outside the kernel, whose registers
+// it would take, where rows are whole pieces (16384 x 4096 86 us, within 92); within it for
+// single values, which lose more by the call (65536 x 1001 118 us, 124).
+template <typename T, typename S, int V, int LANES>
+__device__ __forceinline__ void rows_by_values(const RingParams& p, int row, int end, int first, int team, int mine,
+                                               float (*parts)[kMostParts], int flip) {
+  for (; row < end; ++row) {
+    const int m = p.groups ? p.groups[row] : row / p.per;
+    if (m >= 0 && m < p.count)
+      by_values<T, S, V>(p, row, m, first, LANES * V, min(first + 16 * LANES, p.n),
+                         [&](float v) { return sum_of_team<LANES>(v, team, mine, parts, flip); });
+  }
+}
+
+template <typename T, typename S, int V, int LANES>
+__device__ __noinline__ void rows_apart(const RingParams& p, int row, int end, int first, int team, int mine,
+                                        float (*parts)[kMostParts], int flip) {
+  rows_by_values<T, S, V, LANES>(p, row, end, first, team, mine, parts, flip);
+}
+
 // Teams of LANES threads, or of warps, each with 16 x 32 consecutive values.
 template <typename T, typename S, int V, int LANES>
-__global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const RingParams p) {
+__global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const __grid_constant__ RingParams p) {
   constexpr int PAIRS = 8;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float parts[2][kMostParts];
   const int team = LANES < 32 ? LANES : p.team, mine = threadIdx.x / team, tid = threadIdx.x - mine * team;
-  const int warps = team / 32, slots = (warps + 3) & ~3;
   // the team's lanes of its warp
   const uint32_t lanes = LANES < 32 ? ((1u << (LANES & 31)) - 1u) << (threadIdx.x & 31 & ~(LANES - 1)) : 0xFFFFFFFFu;
   if constexpr (LANES == 32) {  // (those of no warp stay zero)
@@ -353,24 +465,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
 
   const float inv_n = 1.f / static_cast<float>(p.n);
   int flip = 0;
-  // sum over the team, the same in all its threads
-  const auto team_sum = [&](float v) {
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(lanes, v, o);
-    if (LANES < 32 || warps == 1) return v;
-    float* to = parts[flip] + mine * slots;
-    flip ^= 1;
-    if ((threadIdx.x & 31) == 0) to[tid >> 5] = v;
-    __syncwarp();
-    named_barrier_sync(1 + mine, team);
-    float4 q = *reinterpret_cast<const float4*>(to);
-    v = (q.x + q.y) + (q.z + q.w);
-    for (int i = 4; i < warps; i += 4) {
-      q = *reinterpret_cast<const float4*>(to + i);
-      v += (q.x + q.y) + (q.z + q.w);
-    }
-    return v;
-  };
+  const auto team_sum = [&](float v) { return sum_of_team<LANES>(v, team, mine, parts, flip); };
   uint64_t v[PAIRS];
   float mean = 0.f, root = 1.f;
   const auto statistics = [&](int norm) {  // of v, which is zero past the row
@@ -432,6 +527,15 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
           }
           own.clear(g);
         }
+        bool lost = false;  // a gate's product with beta, below the normal values
+        if (fabsf(p.beta) < 1.f && p.beta != 0.f) {
+          constexpr float least = 1.17549435e-38f;
+#pragma unroll
+          for (int i = 0; i < PAIRS; ++i) {
+            const float2 u = f2_of(g[i]);
+            lost |= (u.x != 0.f && fabsf(u.x * p.beta) < least) || (u.y != 0.f && fabsf(u.y * p.beta) < least);
+          }
+        }
         read(p.weight[0], 0, f, 1.f);
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) g[i] = mul2(g[i], beta), ca[i] = mul2(f[i], g[i]);
@@ -448,6 +552,24 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
         read(p.shift, m * p.ldh, g, 0.f);
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) cd[i] = add2(cd[i], g[i]);
+        uint64_t none[2] = {0, 0};  // 0, or NaN where a product is infinite or none
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+          none[0] = fma2(ca[i], 0, fma2(cb[i], 0, none[0]));
+          none[1] = fma2(cc[i], 0, fma2(cd[i], 0, none[1]));
+        }
+        const float2 u = f2_of(add2(none[0], none[1]));
+        lost = __any_sync(lanes, lost || u.x + u.y != 0.f);
+        if (LANES == 32 && team > 32) {
+          __syncwarp();
+          lost = named_barrier_any(1 + mine, team, lost);
+        }
+        if (lost) {
+          if constexpr (V == 1) rows_by_values<T, S, V, LANES>(p, row, end, own.first, team, mine, parts, flip);
+          else rows_apart<T, S, V, LANES>(p, row, end, own.first, team, mine, parts, flip);
+          cp_async_wait<0>();
+          return;
+        }
       }
     }
     // rows stages - 1 at most are in flight: this one is the oldest
@@ -485,61 +607,17 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
   }
 }
 
-// Rows of any length: a CTA a row, the values made again from x and the residual
-// for each sum over them.  (A value is written by the thread that read it last, so
-// outputs may be their inputs here too.)
+// Rows of any length: a CTA a row, a value at a time.
 constexpr int kLongThreads = 512;
-template <typename T, typename S> __global__ void __launch_bounds__(kLongThreads) block_norm_long_kernel(const BlockParams p) {
+template <typename T, typename S> __global__ void __launch_bounds__(kLongThreads, 3) block_norm_long_kernel(const BlockParams p) {
   __shared__ __align__(16) float parts[2][kMostThreads / 32];
-  const float inv_n = 1.f / static_cast<float>(p.n);
   int flip = 0;
   griddep_launch_dependents();
   griddep_wait();
   for (int64_t row = blockIdx.x; row < p.t; row += gridDim.x) {
     const int m = p.groups ? p.groups[row] : static_cast<int>(row) / p.per;
     if (m < 0 || m >= p.count) continue;
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-    const S* residual = p.residual ? static_cast<const S*>(p.residual) + row * p.ldr : nullptr;
-    float mean[2] = {0.f, 0.f}, scale[2] = {1.f, 1.f};
-    const auto normed = [&](int which, float v, int e) {
-      if (p.norm[which] == OIDNX_NORM_NONE) return v;
-      v = (v - mean[which]) * scale[which];
-      if (p.weight[which]) v *= to_f32<T>(static_cast<const T*>(p.weight[which])[e]);
-      if (p.bias[which]) v += to_f32<T>(static_cast<const T*>(p.bias[which])[e]);
-      return v;
-    };
-    const auto total = [&](int e) {
-      float v = normed(0, to_f32<T>(x[e]), e);
-      if (p.gate) v *= gate_of(to_f32<T>(static_cast<const T*>(p.gate)[m * p.ldg + e]), p.gate_act);
-      v *= p.beta;
-      return residual ? fmaf(p.alpha, to_f32<S>(residual[e]), v) : v;
-    };
-    for (int which = 0; which < (p.y ? 2 : 1); ++which) {
-      if (p.norm[which] == OIDNX_NORM_NONE) continue;
-      for (int power = p.norm[which] == OIDNX_NORM_LAYER ? 1 : 2; power <= 2; ++power) {
-        // sums of up to 2^30 / 512 values a thread: in parts of 256, so that small ones are not lost
-        float sum = 0.f, part = 0.f;
-        int k = 0;
-        for (int e = threadIdx.x; e < p.n; e += kLongThreads) {
-          const float v = which ? total(e) : to_f32<T>(x[e]);
-          const float c = v - mean[which];
-          part = power == 1 ? part + v : fmaf(c, c, part);
-          if ((++k & 255) == 0) sum += part, part = 0.f;
-        }
-        const float all = row_sum<kLongThreads>(sum + part, parts, flip) * inv_n;
-        if (power == 1) mean[which] = all;
-        else scale[which] = inverse_root(all + p.eps);
-      }
-    }
-    for (int e = threadIdx.x; e < p.n; e += kLongThreads) {
-      float v = total(e);
-      if (p.sum) static_cast<S*>(p.sum)[row * p.ld_sum + e] = from_f32<S>(v);
-      if (!p.y) continue;
-      v = normed(1, v, e);
-      if (p.scale) v = fmaf(v, to_f32<T>(static_cast<const T*>(p.scale)[m * p.lds + e]), v);
-      if (p.shift) v += to_f32<T>(static_cast<const T*>(p.shift)[m * p.ldh + e]);
-      static_cast<T*>(p.y)[row * p.ldy + e] = from_f32<T>(v);
-    }
+    by_values<T, S, 1>(p, row, m, threadIdx.x, kLongThreads, p.n, [&](float v) { return row_sum<kLongThreads>(v, parts, flip); });
   }
 }
 

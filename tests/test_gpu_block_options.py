@@ -7,8 +7,10 @@ import torch
 
 pytestmark = pytest.mark.gpu
 
-from tests._tokens import block_norm, done, strided
+from oracle import tokens
+from tests._tokens import KINDS, TINY, UNIT, block_norm, done, f64, strided
 from tests.test_gpu_block import check_block
+from tests.test_gpu_tokens import assert_within
 
 
 # a part of a warp (8 and 16 lanes), one warp, several, of whole pieces and of single values; a CTA a row; long rows
@@ -101,3 +103,100 @@ def test_infinities_and_nan_of_many_rows_stay_in_theirs(n):
         for row in bad:
             assert not got[row, row % n].isfinite()
     assert call()[1][list(bad)].isnan().all()
+
+
+# ---------------------------------------------------------------- factors that no product of two of them holds
+def rare_rows(t, n, kind, post, pre, columns, alpha=1.0, beta=1.0, gates=True):
+    """(sum, y) and their definitions for normal values, but for `columns`: [{name: value}, ..] from the first on."""
+    x, r = strided((t, n), kind, 1, scale=2.0), strided((t, n), "fp32", 2)
+    named = {k: strided((n,), kind, i + 3, mean=1.0) for i, k in enumerate(("post_weight", "pre_weight", "post_bias", "pre_bias"))}
+    count = 3
+    named.update({k: strided((count, n), kind, i + 8) for i, k in enumerate(("gate", "scale", "shift"))})
+    for c, values in enumerate(columns):
+        for k, v in values.items():
+            (x if k == "x" else named[k])[..., c] = v
+    gate, scale, shift = (named[k] for k in ("gate", "scale", "shift"))
+    gate = gate if gates else None
+    per = (t + count - 1) // count
+    m = np.arange(t) // per
+    s, y = torch.empty(t, n, device="cuda"), torch.empty_like(x)
+    vectors = [named[k] for k in ("post_weight", "post_bias", "pre_weight", "pre_bias")]
+    block_norm(x, r, s, y, post, *vectors[:2], pre, *vectors[2:], 1e-5, gate, "plain", scale, shift, None, per, count, alpha, beta,
+               kind, "fp32")
+    done()
+    pw, pb, qw, qb = (f64(v) for v in vectors)
+    with np.errstate(all="ignore"):
+        ref = tokens.block_norm(f64(x), f64(r), post, pw, pb, pre, qw, qb, 1e-5, None if gate is None else f64(gate)[m], "plain",
+                                f64(scale)[m], f64(shift)[m], alpha, beta)
+    return (s, "fp32", ref[0], ref[2]), (y, kind, ref[1], ref[3])
+
+
+def assert_rare(results, first):
+    """Values within the tolerance, infinities and NaN where the definition has them; the `first` columns hold what the test is
+    about.  The largest value is (2 - 2 UNIT) 2^127, so that infinities begin half a step above it, at (2 - UNIT) 2^127; what
+    lies within fp32's losses of that border may go either way."""
+    for out, kind, ref, size in results:
+        border = (2 - UNIT[kind]) * 2.0 ** 127
+        with np.errstate(invalid="ignore"):
+            ref = np.where(np.abs(ref) >= border, np.copysign(np.inf, ref), ref)
+            either = np.abs(np.abs(ref) / border - 1) < 2.0 ** -16
+        got = np.where(either, ref, f64(out))
+        fine = np.isfinite(ref)
+        assert np.array_equal(got[~fine], ref[~fine], equal_nan=True), (got[:2, :first], ref[:2, :first])
+        assert_within(got[fine], ref[fine], (UNIT[kind] * np.abs(ref) + TINY[kind] + 96 * 2.0 ** -24 * size)[fine])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("t", [5, 700])
+@pytest.mark.parametrize("n", WIDTHS)
+def test_gates_whose_products_leave_fp32(t, n, kind):
+    """(post(x) gate beta, a factor after the other: infinite gates, factors of 0 beside them, products
+    of two vectors or of a gate and the branch's scale that are too large or too small while the value is neither."""
+    inf, nan = float("inf"), float("nan")
+    columns = [dict(gate=inf, post_weight=1.0, post_bias=-3.0), dict(gate=-inf, post_weight=0.0, post_bias=2.0),
+               dict(gate=inf, post_weight=0.0, post_bias=0.0), dict(gate=1e25, post_weight=1e-30, post_bias=0.0),
+               dict(gate=1e-25, post_weight=1e-20, post_bias=1e20), dict(gate=0.0, post_weight=1e30, post_bias=0.0),
+               dict(gate=nan), dict(gate=0.0, post_weight=inf), dict(gate=1e-20, post_weight=1e30, post_bias=0.0)]
+    for beta in (1.0, 1e20, 1e-25):
+        assert_rare(rare_rows(t, n, kind, "rms", "none", columns, beta=beta), len(columns))
+    # without a norm: values beside which only the gate's product with beta is off
+    columns = [dict(x=1e-30, gate=1e30), dict(x=1e30, gate=1e-30), dict(x=inf, gate=-2.0), dict(x=-inf, gate=0.0)]
+    for beta in (1.0, 1e30, 1e-25):
+        assert_rare(rare_rows(t, n, kind, "none", "none", columns, beta=beta), len(columns))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("t", [5, 700])
+@pytest.mark.parametrize("n", WIDTHS)
+def test_modulations_whose_products_leave_fp32(t, n, kind):
+    """pre(s) (1 + scale) + shift: infinite scales, weights and biases, values of infinity under a negative scale, weights whose
+    product with 1 + scale is too large."""
+    inf = float("inf")
+    columns = [dict(scale=inf, pre_weight=1.0, pre_bias=-3.0), dict(scale=-inf, pre_weight=0.0, pre_bias=1.0),
+               dict(scale=-0.5, pre_weight=inf, pre_bias=0.0), dict(scale=-1.0), dict(scale=-0.5, pre_bias=inf),
+               dict(shift=inf), dict(scale=1.0, pre_weight=3e38, pre_bias=0.0), dict(scale=-1.0, pre_weight=inf)]
+    assert_rare(rare_rows(t, n, kind, "none", "rms", columns, gates=False), len(columns))
+    columns = [dict(x=inf, scale=-0.5), dict(x=-inf, scale=-3.0), dict(x=inf, scale=-1.0), dict(scale=inf), dict(x=3e38, scale=1.0)]
+    assert_rare(rare_rows(t, n, kind, "none", "none", columns, gates=False), len(columns))
+
+
+@pytest.mark.parametrize("n", WIDTHS)
+def test_rows_around_one_group_of_an_infinite_gate(n):
+    """One group of four with a gate of infinity, rows of all groups and padding mixed, in place: each row as it is defined,
+    padding as it was."""
+    t, count = 700, 4
+    m = np.random.default_rng(n).integers(-1, count + 1, t)
+    x, r = strided((t, n), "bf16", 1), strided((t, n), "fp32", 2)
+    w, b, gate, shift = strided((n,), "bf16", 3), strided((n,), "bf16", 4), strided((count, n), "bf16", 5), strided((count, n), "bf16", 6)
+    gate[2, n // 2], b[n // 2] = float("inf"), -0.5
+    use = (m >= 0) & (m < count)
+    at = np.where(use, m, 0)
+    with np.errstate(all="ignore"):
+        s, y, size_s, size_y = tokens.block_norm(f64(x), f64(r), "rms", f64(w), f64(b), "none", None, None, 1e-5, f64(gate)[at], "plain",
+                                                 None, f64(shift)[at], 1.0, 1.0)
+    s[~use], y[~use], size_s[~use], size_y[~use] = f64(r)[~use], f64(x)[~use], 0, 0
+    block_norm(x, r, r, x, "rms", w, b, "none", None, None, 1e-5, gate, "plain", None, shift,
+               torch.tensor(m, dtype=torch.int32, device="cuda"), 0, count, 1.0, 1.0, "bf16", "fp32")
+    done()
+    assert np.isinf(s[at == 2][:, n // 2]).any()
+    assert_rare(((r, "fp32", s, size_s), (x, "bf16", y, size_y)), 4)
