@@ -4,6 +4,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <limits>
 
 #include "cross.h"
 #include "token_host.h"
@@ -191,7 +192,9 @@ cudaError_t run_cross(CrossParams& p, int precision, cudaStream_t stream) {
   if (p.hq == 1) p.q_s[2] = p.o_s[2] = ld;
   if (p.hk == 1) p.k_s[2] = p.v_s[2] = ld;
   const bool negative = p.scale < 0.f;
-  if (p.scale == 0.f) p.scale = 1e-37f;  // equal weights all the same, and a product with -infinity stays one
+  // The smallest number of fp32 for 0: a product with -infinity stays one, and the largest score
+  // comes to 5e-7, less than a weight can show.
+  if (p.scale == 0.f) p.scale = std::numeric_limits<float>::denorm_min();
   constexpr unsigned kSequences = 1, kHeads = 4;
   const bool move_q = negative || !fits(p.q, p.q_s, p.d, kSequences);
   const bool move_k = p.kv > 0 && !fits(p.k, p.k_s, p.d, kSequences | kHeads);

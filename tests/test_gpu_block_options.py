@@ -1,5 +1,6 @@
-"""What the norms around a branch take beside the plain call, over few rows, many rows (teams with a ring) and long rows:
-kinds, gates and absent parts against the definitions in 64 bits, with the tolerances of tests/test_gpu_block.py."""
+"""What a conditioned block's operators take beside the plain call, against the definitions in 64 bits, with the tolerances of
+tests/test_gpu_block.py: the norms around a branch over few rows, many rows (teams with a ring) and long rows, with every kind,
+gate and absent part; attention of a scale of 0."""
 
 import numpy as np
 import pytest
@@ -8,8 +9,8 @@ import torch
 pytestmark = pytest.mark.gpu
 
 from oracle import tokens
-from tests._tokens import KINDS, TINY, UNIT, block_norm, done, f64, strided
-from tests.test_gpu_block import check_block
+from tests._tokens import KINDS, TINY, UNIT, block_norm, cross_attention, done, f64, strided
+from tests.test_gpu_block import check_block, check_cross_result
 from tests.test_gpu_tokens import assert_within
 
 
@@ -200,3 +201,16 @@ def test_rows_around_one_group_of_an_infinite_gate(n):
     done()
     assert np.isinf(s[at == 2][:, n // 2]).any()
     assert_rare(((r, "fp32", s, size_s), (x, "bf16", y, size_y)), 4)
+
+
+# ---------------------------------------------------------------- attention
+@pytest.mark.parametrize("tq", [1, 400])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attention_of_scale_0_weighs_keys_alike_however_large_their_products(tq, d):
+    q, k = strided((2, tq, 4, d), "bf16", 1, scale=1e18), strided((2, 190, 2, d), "bf16", 2, scale=1e18)
+    v = strided((2, 190, 2, d), "bf16", 3)
+    o, lse = torch.empty_like(q), torch.empty(2, 4, tq, device="cuda")
+    cross_attention(q, k, v, o, lse, None, None, None, 0.0, "bf16")
+    done()
+    ref = tokens.cross_attention(f64(q), f64(k), f64(v), [tq] * 2, [190] * 2, None, 0.0)
+    check_cross_result(f64(o), lse, *ref, "bf16", d, 190)
