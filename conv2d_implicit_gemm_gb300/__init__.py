@@ -301,9 +301,10 @@ def oidnx_qk_norm_rope_axes(q, q_st, q_sh, q_out, qo_st, qo_sh, k, k_st, k_sh, k
                             v, v_st, v_sh, v_out, vo_st, vo_sh, norm, q_weight, k_weight, eps, cos_table,
                             sin_table, table_rows, positions, positions_stride, axes, pair_axes, slots,
                             cache_rows, t, hq, hk, d, rot, interleaved, precision, stream=0):
-    """oidnx_qk_norm_rope with a position an axis: pair_axes is a bytes object of rot / 2 axis numbers."""
-    if len(pair_axes) < rot // 2:
-        raise ValueError(f"pair_axes holds {len(pair_axes)} of {rot // 2} pairs")
+    """oidnx_qk_norm_rope with a position an axis: pair_axes is a bytes object of rot / 2 axis numbers (None: of none)."""
+    held = 0 if pair_axes is None else len(pair_axes)
+    if held < rot // 2:
+        raise ValueError(f"pair_axes holds {held} of {rot // 2} pairs")
     _check(_calls.oidnx_qk_norm_rope_axes(q, q_st, q_sh, q_out, qo_st, qo_sh, k, k_st, k_sh, k_out, ko_st, ko_sh,
                                           v, v_st, v_sh, v_out, vo_st, vo_sh, norm, q_weight, k_weight, eps,
                                           cos_table, sin_table, table_rows, positions, positions_stride, axes,
