@@ -171,7 +171,7 @@ cudaError_t run_aligned(CrossParams& p, bool bf16, int device, int sms, cudaStre
   L.p = p, L.split = parts.split, L.parts = parts.parts, L.device = device;
   if (parts.parts == 1) return launch_cross_token(L, bf16, stream);
   Scratch work;
-  cudaError_t e = work.take(device, static_cast<int64_t>(p.b) * p.hq * p.tq * parts.parts * (p.d + 8) * 4, stream);
+  cudaError_t e = work.take(device, static_cast<int64_t>(p.b) * p.hq * p.tq * parts.parts * cross_part_floats(p.d) * 4, stream);
   if (e != cudaSuccess) return e;
   L.work = static_cast<float*>(work.at);
   e = launch_cross_token(L, bf16, stream);

@@ -50,12 +50,15 @@ cudaError_t launch_cross_tile(const CrossTileLaunch& L, bool bf16, cudaStream_t 
 // CTAs in clusters of `cluster` that the device holds at once.
 int cross_tile_slots(int d, bool bf16, int cluster, int device);
 
-// Few queries: a CTA for each part of a key head's keys.
+// Few queries: a CTA for each part of a key head's keys.  A part of a row: maximum, sum, six
+// floats that nobody reads, and from kPartValues on d values, on 16 bytes.
+constexpr int kPartValues = 8;
+__host__ __device__ constexpr int cross_part_floats(int d) { return kPartValues + d; }
 struct CrossTokenLaunch {
   CrossParams p;
   int split;    // CTAs of a cluster along the keys
   int parts;    // clusters along the keys; over 1: through `work` and a second kernel
-  float* work;  // [unit][row][part][d + 2]
+  float* work;  // over 1 part: [unit][row][part][cross_part_floats(d)]
   int device;
 };
 cudaError_t launch_cross_token(const CrossTokenLaunch& L, bool bf16, cudaStream_t stream);

@@ -281,9 +281,9 @@ __global__ void __launch_bounds__(Tok<DP, MT>::kWarps * 32, Tok<DP, MT>::kCtas)
       acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
       acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
     }
-    if (parts > 1) {  // [unit][row][part]: d values, maximum, sum
-      float* to = work + ((static_cast<int64_t>(unit) * rows_all + row0 + r) * parts + part) * (p.d + 8);
-      if (c * 4 < p.d) *reinterpret_cast<float4*>(to + 8 + c * 4) = acc;
+    if (parts > 1) {  // [unit][row][part]
+      float* to = work + ((static_cast<int64_t>(unit) * rows_all + row0 + r) * parts + part) * cross_part_floats(p.d);
+      if (c * 4 < p.d) *reinterpret_cast<float4*>(to + kPartValues + c * 4) = acc;
       if (c == 0) *reinterpret_cast<float2*>(to) = make_float2(m, l);
       continue;
     }
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const CrossPar
   __shared__ __align__(16) float sums[kJoinThreads][12];  // l and eight values
   const int tid = threadIdx.x;
   const int rows = p.tq * p.group, unit = blockIdx.x / rows, row = blockIdx.x - unit * rows;
-  const int size = p.d + 8, pieces = p.d / 8, sharing = kJoinThreads / pieces;
+  const int size = cross_part_floats(p.d), pieces = p.d / 8, sharing = kJoinThreads / pieces;
   const float* at = work + static_cast<int64_t>(blockIdx.x) * parts * size;
   griddep_launch_dependents();
   griddep_wait();
@@ -380,8 +380,8 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const CrossPar
 #pragma unroll 4
     for (int s = first; s < parts; s += sharing) {
       const float2 st = *reinterpret_cast<const float2*>(at + s * size);
-      const float4 u = *reinterpret_cast<const float4*>(at + s * size + 8 + c * 8);
-      const float4 v = *reinterpret_cast<const float4*>(at + s * size + 12 + c * 8);
+      const float4 u = *reinterpret_cast<const float4*>(at + s * size + kPartValues + c * 8);
+      const float4 v = *reinterpret_cast<const float4*>(at + s * size + kPartValues + 4 + c * 8);
       const float f = exp2_fast(st.x - base);
       l = fmaf(st.y, f, l);
       acc[0] = fmaf(u.x, f, acc[0]), acc[1] = fmaf(u.y, f, acc[1]);

@@ -40,3 +40,11 @@ def test_waits_are_bounded():
     for path in BLOCK:
         for s in lines(path):
             assert "mbar_try_wait" not in s, path
+
+
+def test_parts_of_a_row_are_measured_in_one_place():
+    """The workspace's size and both kernels' strides come from cross_part_floats."""
+    uses = {name: sum("cross_part_floats(" in s for s in lines(os.path.join(CSRC, name))) for name in ("block_host.cpp", "cross_token.cu")}
+    assert uses == {"block_host.cpp": 1, "cross_token.cu": 2}
+    for name in uses:
+        assert not any(re.search(r"\bd \+ \d", s) for s in lines(os.path.join(CSRC, name))), name
