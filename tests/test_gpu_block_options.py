@@ -214,3 +214,58 @@ def test_attention_of_scale_0_weighs_keys_alike_however_large_their_products(tq,
     done()
     ref = tokens.cross_attention(f64(q), f64(k), f64(v), [tq] * 2, [190] * 2, None, 0.0)
     check_cross_result(f64(o), lse, *ref, "bf16", d, 190)
+
+
+@pytest.mark.parametrize("which", range(4))
+@pytest.mark.parametrize("tq,kv", [(1, 300), (1, 20000), (300, 200)])
+def test_attention_with_one_operand_off_16_bytes(tq, kv, which):
+    """Queries, keys, values or the output alone start a value further on: it alone is copied."""
+    q, k, v, o = (strided((2, n, h, 64), "fp16", i, None, int(i == which)) for i, (n, h) in enumerate(((tq, 4), (kv, 2), (kv, 2), (tq, 4))))
+    base = o._base.clone()
+    lse = torch.empty(2, 4, tq, device="cuda")
+    cross_attention(q, k, v, o, lse, None, None, None, 0.125, "fp16")
+    done()
+    ref = tokens.cross_attention(f64(q), f64(k), f64(v), [tq] * 2, [kv] * 2, None, 0.125)
+    check_cross_result(f64(o), lse, *ref, "fp16", 64, kv)
+    assert torch.equal(o._base[:int(which == 3)].view(torch.int16), base[:int(which == 3)].view(torch.int16))
+
+
+# ---------------------------------------------------------------- graph capture
+CAPTURE = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+from tests._tokens import done, strided, norm_rope
+from tests.test_gpu_block import calls_of_every_form
+
+calls = calls_of_every_form()
+q, k = strided((3, 4, 64), "bf16", 5), strided((3, 2, 64), "bf16", 6)
+norm_rope(q, q, k, k, None, None, None, None, 1e-6, None, None, None, None, 0, False, "bf16")  # the one call on the device
+done()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    for call, _ in calls:
+        call()
+for _ in range(2):
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [[t.clone() for t in outs] for _, outs in calls]
+    for _, outs in calls:
+        for t in outs:
+            t.zero_()
+for (call, outs), ref in zip(calls, got):
+    call()
+    done()
+    assert all(a.any() and torch.equal(a, b) for a, b in zip(outs, ref))
+print("captured")
+"""
+
+
+def test_every_form_of_a_block_can_be_captured_once_any_call_has_been_made():
+    """In a process of its own, whose one call before the capture is a norm of heads."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", CAPTURE.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
