@@ -3,9 +3,10 @@
 //
 //   s = alpha residual + beta g(gate) post(x);  y = pre(s) (1 + scale) + shift
 //
-// A row's values stay in registers between their one read and the two writes, in
-// fp32; means and variances are taken from the values themselves (the mean first,
-// then the squares of what is left), so that nothing cancels.  The bound is memory.
+// A row's values stay in registers between their one read and the two writes, in fp32
+// (but for rows of over 16384, which are read again for each sum).  Means come first,
+// then the squares of what is left of the values, so that the squares do not cancel; a
+// value less its mean is off by the mean's own rounding, 2^-24 of it.  The bound is memory.
 #include <algorithm>
 #include <type_traits>
 
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kMostThreads) block_norm_kernel(const BlockPar
 
 // Many rows of up to 8192 values: teams of 8 or 16 lanes of a warp or of whole warps
 // take consecutive rows, 16 values a thread.  Rows come through a ring in shared memory
-// (cp.async, several rows ahead), and what stands beside a row (weights, gate,
+// (cp.async, one row ahead or two), and what stands beside a row (weights, gate,
 // modulation) is multiplied together once a group and stays in registers:
 //
 //   s = alpha r + a (x - mean) root + b,   a = beta g w_post,   b = beta g b_post
@@ -329,9 +330,9 @@ __global__ void __launch_bounds__(kMostThreads) block_norm_kernel(const BlockPar
 // bytes are copied by each warp for itself, from the 16 bytes that its 512 values start
 // in to the 16 that they end in (which are in their pages).
 //
-// 16384 rows of 4096 in bf16: 89 us, 6.0 TB/s, 89% of the measured copy rate (8192 of
-// 8192 98, 131072 of 512 86, 262144 of 128 47); with an fp32 sum 126 us, 94%.  Odd
-// widths, a value at a time: 16384 of 4095 139 us, 65536 of 1001 119; what bounds these
+// 16384 rows of 4096 in bf16: 86 us, 6.2 TB/s, 92% of the measured copy rate (8192 of
+// 8192 94, 131072 of 512 86, 262144 of 128 47); with an fp32 sum 126 us, 94%.  Odd
+// widths, a value at a time: 16384 of 4095 144 us, 65536 of 1001 118; what bounds these
 // is instructions.  All 128 registers are taken, so what can be made again from the row
 // is (3 to 7% of an odd width).  Not kept: teams of powers of two in warps, their values
 // apart by the team's width (101, 143, 219, and 140 for rows of 128 on a whole warp),
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
         }
       }
     }
-    // rows stages - 1 at most are in flight: this one is the oldest
+    // stages is 2 or 3, and stages - 1 rows are in flight: this one is the oldest
     if (p.stages == 2) cp_async_wait<0>();
     else cp_async_wait<1>();
     if constexpr (V == 1) __syncwarp(lanes);  // its lanes have copied its part together
@@ -639,9 +640,9 @@ cudaError_t launch_teams(const BlockParams& p, int device, int sms, cudaStream_t
   q.x_bytes = bytes(sizeof(T));
   q.stage_bytes = q.x_bytes + (p.residual ? bytes(sizeof(S)) : 0);
   // One row ahead, for one or two teams two while that is 64 KB at most: more in flight
-  // slows the writes down (us with 2, 3 and as many stages as fit: 131072 rows of 512 86,
-  // 100, 101, of 2048 89, 92, 94, with an fp32 sum 16384 of 4096 126, 147, 146; but 16384
-  // of 4096 95, 91, 93 and 8192 of 8192 98, 97, 100).
+  // slows the writes down (us with 2 and 3 stages: 131072 rows of 512 87, 98, 32768 of 2048
+  // 89, 97, with an fp32 sum 16384 of 4096 126, 143; but 16384 of 4096 93, 86 and 8192 of
+  // 8192 96, 93).
   const int all = teams * ctas;
   q.stages = all <= 2 && 2 * all * q.stage_bytes <= 64 * 1024 ? 3 : 2;
   const auto whole = [](const void* q, int64_t ld) { return (reinterpret_cast<uintptr_t>(q) | ld * sizeof(float)) % 32 == 0; };
@@ -663,9 +664,9 @@ template <typename T, typename S>
 cudaError_t launch_t(const BlockParams& p, bool vector, int device, int sms, cudaStream_t stream) {
   const int n = p.n;
   // Rows of a CTA each start sooner, teams keep what stands beside the rows: us, bf16,
-  // 153, 300 and 608 rows of 1024 values 3.3, 3.4, 6.2 and 3.4, 3.4, 3.4; of 4096 3.6,
-  // 4.8, 9.1 and 3.9, 5.3, 7.6; 153 and 300 rows of 8192 9.3, 10.4 and 7.1, 8.1, of 128
-  // 3.3, 3.4 and 2.9, 2.9.
+  // 153, 300 and 608 rows of 1024 values 3.3, 3.4, 6.2 and 3.4, 3.6, 3.5; of 4096 3.6,
+  // 4.8, 9.0 and 4.0, 5.5, 7.8; 153 and 300 rows of 8192 9.2, 10.2 and 7.2, 8.2, of 128
+  // 3.3, 3.4 and 3.1, 3.1.
   if (p.t > (n > 256 && n <= kMostThreads * 8 ? 2 : 1) * sms && n <= kRingThreads * 16)
     return vector ? launch_ring<T, S, 8>(p, device, sms, stream) : launch_ring<T, S, 1>(p, device, sms, stream);
   if (n <= kMostThreads * 8)

@@ -27,10 +27,10 @@
 // Heads of over 64 values are bound by the tensor cores: for 64 keys the operands of a
 // row tile's two products take 640 cycles through shared memory (its queries are read
 // again for each unit), two tiles 1280 of some 1500, and a long run lowers the clock:
-// 8160 queries and keys, 16 heads of 128, 363 us, 1500 TFLOP/s, 398 without the last
-// round divided; 392 with all of the softmax's arithmetic left out.  Stages handed back
-// by the softmax warps instead of the issuing threads: 423.  2040 x 2040, 4 heads of
-// 256: 39 us (47).
+// 8160 queries and keys, 16 heads of 128, 361 us in a graph, 1510 TFLOP/s, and 388 in a
+// long run of calls, at 1410; 398 without the last round divided, 392 of them with all of
+// the softmax's arithmetic left out.  Stages handed back by the softmax warps instead of
+// the issuing threads: 423.  2040 x 2040, 4 heads of 256: 39 us (47).
 // Heads of up to 64 are bound by the chain from scores to weights to the next scores,
 // four of which share an SM's issue slots: 8160 x 8160, 16 heads of 64, 326 us, 840
 // TFLOP/s (276 without the softmax's arithmetic).  Four row tiles of 8160 queries to 77

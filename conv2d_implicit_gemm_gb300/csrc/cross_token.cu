@@ -10,6 +10,11 @@
 // SMs idle, over as many CTAs as the device holds, whose parts a second kernel
 // joins; the order is always the same.
 //
+// The weights are rounded to the storage type before their product with the values, as
+// both operands of a product have one type (their sum is taken before the rounding): the
+// outputs' error against 64 bits is 1.1 to 1.4 times that of a form in 32 bits throughout,
+// of one rounding of the output alone.
+//
 // 64 streams of one token, 20 heads of 64, up to 1500 keys: 44 us, 5.4 TB/s, 80% of the
 // measured copy rate (full ones 80 us, 6.1 TB/s).  One token over 20000 keys, 8 key heads
 // of 128: 20 us in 19 parts a head, of which the memory's share is 12, the start 4 and the
